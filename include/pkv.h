@@ -69,6 +69,10 @@ extern "C" {
 #define PKV_I8_BLOCK_BYTES (2 * PKV_PAGE_TOKENS * PKV_HEAD_DIM + 2 * PKV_PAGE_TOKENS * 4) /* 2176 */
 #define PKV_I8_PAGE_BYTES (PKV_NUM_KV_HEADS * PKV_I8_BLOCK_BYTES)                       /* 17408 */
 
+/* Block-scaled 8-bit pages (bs8): the bf16 page layout with one byte per
+ * value, [2 (K,V)][8][16][64], and one fp32 scale per (page, K|V, KV head). */
+#define PKV_BS8_PAGE_BYTES (PKV_PAGE_ELEMS) /* 16384 */
+
 typedef enum pkv_status {
   PKV_OK = 0,
   PKV_ERR_INVALID_ARGUMENT = 1,   /* null pointer, negative size, bad stride  */
@@ -115,6 +119,35 @@ int pkv_rope_inv_freq_llama3(double* inv_freq, double theta, double factor,
  * The caller copies the tables to the device for kv_append_rope. */
 int pkv_rope_table_fill(float* host_cos, float* host_sin, int max_pos, const double* inv_freq);
 
+/* Frequencies of a rotary dimension of 2 * pairs (1 <= pairs <= 32: the whole
+ * 64-wide head or its first part) and their scaling for contexts longer than
+ * the trained one.  With f_i = theta^(-2i / (2 pairs)), i < pairs:
+ *   NONE    inv_freq[i] = f_i
+ *   LINEAR  f_i / factor                          (position interpolation)
+ *   NTK     theta replaced by theta * factor^(d / (d - 2)), d = 2 pairs >= 4
+ *   YARN    f_i / factor * r_i + f_i * (1 - r_i), r_i = clamp((i - lo) /
+ *           max(hi - lo, 0.001), 0, 1), lo = max(0, floor(at(beta_fast))),
+ *           hi = min(d - 1, ceil(at(beta_slow))), at(b) = pairs *
+ *           ln(original_max_pos / (2 pi b)) / ln(theta): pairs that turn more
+ *           than beta_fast times over the original context keep their
+ *           frequency, those below beta_slow turns are divided;
+ *           *attention_factor = 0.1 ln(factor) + 1 (else 1), which multiplies
+ *           the tables of q and k.
+ * factor >= 1.  inv_freq: host double[pairs] (out); attention_factor: host
+ * double (out).  original_max_pos and the betas matter for YARN only. */
+#define PKV_ROPE_SCALING_NONE 0
+#define PKV_ROPE_SCALING_LINEAR 1
+#define PKV_ROPE_SCALING_NTK 2
+#define PKV_ROPE_SCALING_YARN 3
+int pkv_rope_inv_freq_scaled(double* inv_freq, int pairs, double theta, int scaling, double factor,
+                             int original_max_pos, double beta_fast, double beta_slow,
+                             double* attention_factor);
+
+/* host_cos/host_sin: host float[max_pos][pairs] (out);
+ * cos[p][i] = (float)(cos((double)p * inv_freq[i]) * attention_factor). */
+int pkv_rope_table_fill_scaled(float* host_cos, float* host_sin, int max_pos, int pairs,
+                               const double* inv_freq, double attention_factor);
+
 /* ------------------------------------------------------------------------
  * kv_append_rope - write T new tokens' K/V into their pages.
  *
@@ -148,6 +181,49 @@ int kv_append_rope(const void* k, const void* v, const int32_t* positions,
                    const float* rope_cos, const float* rope_sin, int max_pos,
                    const void* q_in, void* q_out,
                    int* d_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kv_append_norm_rope - kv_append_rope for models that normalise the heads of
+ * q and k, rotate only a part of the head, or pair its dims differently.
+ *
+ * For every q and k head row x (64 values) of token t at position p =
+ * positions[t], in fp32:
+ *   y_d = x_d * r * w_d, r = 1 / sqrt(mean(x^2) + eps)   (y = x without w)
+ *   the first 2 * rope_pairs dims rotated by row p of the tables: pairs
+ *   (i, i + rope_pairs), or (2 i, 2 i + 1) when interleaved:
+ *   (a, b) -> (a c_i - b s_i, a s_i + b c_i); the other dims as they are,
+ * rounded to bf16 once.  K and V go to their page slots as in kv_append_rope
+ * (V bit for bit); the rows are also written to k_out if that is given.  With
+ * kv_pool NULL nothing is appended: q and k are normalised and rotated into
+ * q_out and k_out.  Without weights, with 32 pairs and the half layout the
+ * pages and q_out equal kv_append_rope's bit for bit.
+ *
+ *   q, k, v       device bf16, token rows of [32][64], [8][64], [8][64]
+ *                 contiguous values, q_stride / k_stride / v_stride elements
+ *                 apart (e.g. slices of one fused projection's rows); 16-byte
+ *                 aligned, strides multiples of 8.  q may be NULL (then q_out
+ *                 and q_weight too), v is unused without a pool
+ *   q_weight, k_weight  device [64], fp32 (weight_f32 = 1) or bf16 (0); NULL:
+ *                 that side is not normalised
+ *   eps           finite, >= 0 (unused without weights)
+ *   rope_cos/sin  device float [max_pos][rope_pairs] (pkv_rope_table_fill or
+ *                 pkv_rope_table_fill_scaled)
+ *   q_out         device bf16 [T][32][64] (may be q itself, when contiguous)
+ *   k_out         device bf16 [T][8][64] or NULL; required without a pool
+ *   positions, token_seq, block_tables, num_seqs, bt_row_stride, max_blocks,
+ *   kv_pool, num_pages, d_err: as for kv_append_rope
+ * A token whose row, position or page id is out of range writes nothing to
+ * the pool, gets zero q_out and k_out rows and sets *d_err =
+ * PKV_ERR_DEVICE_INDEX.
+ * ---------------------------------------------------------------------- */
+int kv_append_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                        const void* v, long long v_stride, const void* q_weight,
+                        const void* k_weight, int weight_f32, float eps, const float* rope_cos,
+                        const float* rope_sin, int max_pos, int rope_pairs, int interleaved,
+                        const int32_t* positions, const int32_t* token_seq, int T,
+                        const int32_t* block_tables, int num_seqs, int bt_row_stride,
+                        int max_blocks, void* kv_pool, int num_pages, void* q_out, void* k_out,
+                        int* d_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * paged_gqa_decode - one decode step of grouped-query attention over
@@ -490,6 +566,83 @@ int paged_gqa_decode_append_layers(const void* q, const void* k_new, const void*
                                    size_t stage_bytes);
 
 /* ------------------------------------------------------------------------
+ * Block-scaled 8-bit pages (bs8) - a cache of half the bf16 size whose scales
+ * cost 64 bytes a page: one fp32 scale per block, a block being the 16 slots
+ * of one page, K or V, and KV head.
+ *   kv_pool    device bytes [num_pages][2 (K,V)][8][16][64], 16-byte aligned:
+ *              int8 codes (two's complement) or e4m3 codes
+ *   kv_scales  device float [num_pages][2][8]; a code c stands for c * scale
+ * scale = amax / top over the block's tokens and code = round-half-even(x /
+ * scale), both divisions IEEE fp32, top = 127 for int8 (codes clamped to
+ * [-127, 127]) and 448 for e4m3; scale 0 gives zero codes.  x is the row the
+ * bf16 cache would hold.  Rows must be finite.
+ * ---------------------------------------------------------------------- */
+#define PKV_BS8_INT8 0
+#define PKV_BS8_E4M3 1
+
+/* kv_append_rope_bs8: the newest tokens of every sequence written into their
+ * pages.  Sequence s holds seq_lens[s] tokens after the call; the last
+ * cu_new[s+1] - cu_new[s] of them are new and are rows cu_new[s] ..
+ * cu_new[s+1] - 1 of k, v and q_in (as paged_gqa_prefill counts its queries;
+ * one row per sequence is a decode step).  K is rotated at its position as in
+ * kv_append_rope (half layout, 32 pairs, rounded to bf16) when tables are
+ * given, taken as it is without (rows rotated before, e.g. by
+ * kv_append_norm_rope).  The tokens of a call that share a block set its scale
+ * together: tokens from slot 0 on set it anew; tokens behind held ones keep
+ * the larger of the scale found and their own, and when that grows the held
+ * codes are written again as round(code * old / new) -- so a block written
+ * token by token loses at most half a step of its final scale per growth.
+ * Slots behind the last token keep their bytes.
+ *   k, v, q_in   device bf16 token rows [8][64], [8][64], [32][64],
+ *                k_stride / v_stride / q_stride elements apart, 16-byte
+ *                aligned, strides multiples of 8; q_in needs the tables
+ *   cu_new       device int32 [num_seqs + 1], ascending from 0; rows behind
+ *                cu_new[num_seqs] are left alone
+ *   seq_lens     device int32 [num_seqs]
+ *   rope_cos/sin device float [max_pos][32], 16-byte aligned, or both NULL
+ *   q_out        device bf16 [T][32][64] (may be q_in, when contiguous)
+ * A sequence with fewer tokens than new ones, more than 16 * max_blocks or
+ * max_pos tokens, or rows beyond T, and a token whose page id is outside
+ * [0, num_pages), write nothing, get zero q_out rows and set *d_err =
+ * PKV_ERR_DEVICE_INDEX.  No two sequences of a call may write one page. */
+int kv_append_rope_bs8(const void* k, long long k_stride, const void* v, long long v_stride,
+                       const int32_t* cu_new, const int32_t* seq_lens, int T,
+                       const int32_t* block_tables, int num_seqs, int bt_row_stride,
+                       int max_blocks, void* kv_pool, float* kv_scales, int num_pages,
+                       int code_type, const float* rope_cos, const float* rope_sin, int max_pos,
+                       const void* q_in, long long q_stride, void* q_out, int* d_err,
+                       void* stream);
+
+/* kv_read_bs8: pages as bf16 pages, out[i] = code * scale (rounded once) of
+ * page page_ids[i], device bf16 [count][2][8][16][64]: a bf16 pool of `count`
+ * pages, e.g. for paged_gqa_prefill over a cached prefix.  Slots that hold no
+ * token read as whatever their bytes stand for.  A page id outside
+ * [0, num_pages) gives a zero page and sets *d_err. */
+int kv_read_bs8(const void* kv_pool, const float* kv_scales, int num_pages, int code_type,
+                const int32_t* page_ids, int count, void* out, int* d_err, void* stream);
+
+/* paged_gqa_decode over bs8 pages: attention over the values the codes stand
+ * for, scores and sums in fp32, output rounded to bf16; lengths of zero, bad
+ * lengths and bad page ids as paged_gqa_decode.
+ * Codes enter fp16 tensor-core MMAs exactly; q is scaled by a power of two per
+ * (sequence, KV head) so that its largest |value| lies in [2^14, 2^15); the
+ * probabilities are rounded to fp16 (relative 2^-12) for the P V product.
+ *   kv_scales    16-byte aligned
+ *   max_seq_len  host upper bound of seq_lens (sizes the grid; a larger
+ *                actual length is still handled; 0: 16 max_blocks)
+ *   workspace    at least paged_gqa_decode_bs8_workspace_bytes(num_seqs)
+ *                bytes, 16-byte aligned, of any content: every call writes
+ *                what it reads.  Calls that may run at the same time, two
+ *                captured graphs among them, need distinct workspaces
+ * At most 4096 sequences per call. */
+size_t paged_gqa_decode_bs8_workspace_bytes(int num_seqs);
+int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_scales, int num_pages,
+                         int code_type, const int32_t* block_tables, int bt_row_stride,
+                         int max_blocks, const int32_t* seq_lens, int num_seqs, int max_seq_len,
+                         void* out, float scale, void* workspace, size_t workspace_bytes,
+                         int* d_err, void* stream);
+
+/* ------------------------------------------------------------------------
  * paged_gqa_prefill - causal GQA attention of each sequence's newest tokens
  * over its own pages: a whole prompt, or a chunk of one after a cached
  * prefix ("Gestion de la KV cache et strategies de batching": attention
@@ -547,6 +700,45 @@ int paged_gqa_prefill_ex(const void* q, int num_tokens, const int32_t* cu_q,
  * ---------------------------------------------------------------------- */
 int pkv_argmax_f32(const float* logits, int rows, int vocab, long long row_stride,
                    int32_t* out_ids, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pkv_process_logits - penalties for repeated tokens, biases and a grammar's
+ * mask on the logits, and the next token, in one pass.
+ *
+ * Row r, token i, x = logits[r][i] in fp32, each operation rounded to nearest:
+ *   1. i in the row's history: x = x > 0 ? x / repetition : x * repetition
+ *   2. i occurs n > 0 times in the history's generated part (behind the first
+ *      prompt_lens[r] ids): x = x - frequency * n, then x = x - presence
+ *   3. i among bias_ids: x = x + its bias (the last entry of an id counts)
+ *   4. bit i % 32 of allow_mask[r][i / 32] is 0: x = -inf
+ * out[r][i] = x.  out_ids[r] = the first index of the largest non-NaN x among
+ * the tokens that the mask leaves; -1 if there is none.
+ *   logits        device [rows][row_stride], PKV_LOGITS_F32 / BF16 / F16
+ *   out           device float [rows][out_stride] or NULL (ids only); may be
+ *                 logits itself (F32, the same stride)
+ *   out_ids       device int32 [rows] or NULL; one of out and out_ids is given
+ *   history       device int32 [rows][history_stride] or NULL: prompt ids,
+ *                 then generated ones; history_lens [rows] of them count (at
+ *                 most history_stride); ids outside [0, vocab) are padding
+ *   prompt_lens   device int32 [rows] or NULL (all generated)
+ *   repetition, presence, frequency  device float [rows] or NULL (1, 0, 0);
+ *                 finite, repetition > 0; only with a history
+ *   bias_ids, bias_values  device [rows][bias_count] int32 and float, ids
+ *                 outside [0, vocab) are padding; unused with bias_count 0
+ *   allow_mask    device uint32 [rows][mask_stride] or NULL, mask_stride >=
+ *                 ceil(vocab / 32)
+ * One cluster of 8 CTAs per row; deterministic.  Host-side checks only.
+ * ---------------------------------------------------------------------- */
+#define PKV_LOGITS_F32 0
+#define PKV_LOGITS_BF16 1
+#define PKV_LOGITS_F16 2
+int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long long row_stride,
+                       float* out, long long out_stride, int32_t* out_ids,
+                       const int32_t* history, long long history_stride,
+                       const int32_t* history_lens, const int32_t* prompt_lens,
+                       const float* repetition, const float* presence, const float* frequency,
+                       const int32_t* bias_ids, const float* bias_values, int bias_count,
+                       const uint32_t* allow_mask, long long mask_stride, void* stream);
 
 /* Wait for `stream`, then copy the device error word to *code_out (host).
  * If `clear` is non-zero the word is reset to 0 afterwards. */

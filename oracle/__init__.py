@@ -20,6 +20,11 @@ to check by eye, in FP64 NumPy with per-element loops where that is clearer:
                  dequantised pages.
 * ``argmax``     next-token selection over FP32 logits (first index of the
                  largest non-NaN value).
+* ``norm_rope``  per-head RMS norm and rotation (either layout, part of the
+                 head) and frequencies scaled for long contexts.
+* ``bs8_kv``     pages of 8-bit codes with one scale per block of 16 slots and
+                 head: the append and attention over them.
+* ``logits``     penalties, biases and masks on logits, and the next token.
 * ``admission``  the admission-credit rule and a FIFO continuous-batching
                  simulation with on-demand page allocation.
 
@@ -39,4 +44,4 @@ Sources (titles of the pages that define the path):
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 (closed forms, invariants, brute force, library routines); none is unpinned.
 """
-from . import admission, argmax, bf16, int8_kv, paged_kv, rope  # noqa: F401
+from . import admission, argmax, bf16, bs8_kv, int8_kv, logits, norm_rope, paged_kv, rope  # noqa: F401

@@ -52,6 +52,7 @@ class PkvError(RuntimeError):
 
 
 _p, _i, _f, _d, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _ip = ctypes.POINTER(ctypes.c_int)
 
 
@@ -91,6 +92,18 @@ _SIGS = {
     "paged_gqa_decode_append_layers": (_i, [_p, _p, _p, _p, _p, _i, _i, _p, _p, _i, _p, _i, _i, _p,
                                             ctypes.c_longlong, _i, _i, _p, _i, _f, _p, _sz, _p, _p,
                                             _i, _p, _p, _sz]),
+    "pkv_rope_inv_freq_scaled": (_i, [_p, _i, _d, _i, _d, _i, _d, _d, ctypes.POINTER(_d)]),
+    "pkv_rope_table_fill_scaled": (_i, [_p, _p, _i, _i, _p, _d]),
+    "kv_append_norm_rope": (_i, [_p, _ll, _p, _ll, _p, _ll, _p, _p, _i, _f, _p, _p, _i, _i, _i, _p,
+                                 _p, _i, _p, _i, _i, _i, _p, _i, _p, _p, _p, _p]),
+    "kv_append_rope_bs8": (_i, [_p, _ll, _p, _ll, _p, _p, _i, _p, _i, _i, _i, _p, _p, _i, _i, _p, _p,
+                                _i, _p, _ll, _p, _p, _p]),
+    "kv_read_bs8": (_i, [_p, _p, _i, _i, _p, _i, _p, _p, _p]),
+    "paged_gqa_decode_bs8_workspace_bytes": (_sz, [_i]),
+    "paged_gqa_decode_bs8": (_i, [_p, _p, _p, _i, _i, _p, _i, _i, _p, _i, _i, _p, _f, _p, _sz, _p,
+                                  _p]),
+    "pkv_process_logits": (_i, [_p, _i, _i, _i, _ll, _p, _ll, _p, _p, _ll, _p, _p, _p, _p, _p, _p,
+                                _p, _i, _p, _ll, _p]),
     "pkv_read_device_error": (_i, [_p, _p, _i, _ip]),
     "pkv_credit_pages": (_i, [_i, _i, _i]),
     "pkv_sched_create": (_p, [_i, _i, _i, _i]),
@@ -204,6 +217,39 @@ def rope_tables_device(device, max_pos: int = 2048, inv_freq=None):
     return torch.from_numpy(cos).to(device), torch.from_numpy(sin).to(device)
 
 
+ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def pkv_rope_inv_freq_scaled(rotary_dim: int = HEAD_DIM, theta: float = 500000.0, scaling=None,
+                             factor: float = 1.0, original_max_pos: int = 8192,
+                             beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq [rotary_dim / 2], attention factor) of a head whose first
+    rotary_dim dims are rotated; scaling: None, "linear", "ntk" or "yarn"
+    (pkv.h gives the formulas)."""
+    if rotary_dim % 2 or not 2 <= rotary_dim <= HEAD_DIM:
+        raise ValueError("rotary_dim must be even and within the head")
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
+    out = np.zeros(rotary_dim // 2, np.float64)
+    mul = ctypes.c_double(1.0)
+    _check(_L().pkv_rope_inv_freq_scaled(out.ctypes.data, rotary_dim // 2, theta, ROPE_SCALING[scaling],
+                                        factor, original_max_pos, beta_fast, beta_slow,
+                                        ctypes.byref(mul)), "pkv_rope_inv_freq_scaled")
+    return out, mul.value
+
+
+def rope_tables_scaled_device(device, max_pos: int, inv_freq, attention_factor: float = 1.0):
+    """cos/sin tables [max_pos, pairs] on `device` for kv_append_norm_rope."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if f.ndim != 1 or not 1 <= len(f) <= ROPE_PAIRS:
+        raise ValueError("inv_freq must have 1 to 32 entries")
+    cos = np.empty((max_pos, len(f)), np.float32)
+    sin = np.empty_like(cos)
+    _check(_L().pkv_rope_table_fill_scaled(cos.ctypes.data, sin.ctypes.data, max_pos, len(f), f.ctypes.data,
+                                          attention_factor), "pkv_rope_table_fill_scaled")
+    return torch.from_numpy(cos).to(device), torch.from_numpy(sin).to(device)
+
+
 # ------------------------------------------------------------------- append --
 
 def kv_append_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin,
@@ -245,6 +291,148 @@ def kv_append_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin,
                             _ptr(rope_cos), _ptr(rope_sin), rope_cos.shape[0],
                             _ptr(q_in), _ptr(q_out), _ptr(d_err), _stream(stream))
     _check(st, "kv_append_rope")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(t, name):
+    """The CUDA device of `t`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(dev, stream, where, *args):
+    """The C call `where` with the stream appended: the given one, or the
+    current one of the tensors' device (made current for the call)."""
+    fn = getattr(_L(), where)
+    if stream is not None:
+        st = fn(*args, stream.cuda_stream)
+    elif dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != OK:
+        _check(st, where)
+
+
+def _need_rows(t, name, heads, dev, tokens=None):
+    """`t` as token rows [T, heads, 64] bf16 with contiguous heads and any
+    token stride; returns (T, token stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [T, {heads}, {HEAD_DIM}], got {tuple(shape)}")
+    if tokens is not None and shape[0] != tokens:
+        raise ValueError(f"{name} must have {tokens} tokens, got {shape[0]}")
+    stride = t.stride()
+    if stride[2] != 1 or stride[1] != HEAD_DIM:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return shape[0], stride[0] if shape[0] > 1 else heads * HEAD_DIM
+
+
+def _need_weight(w, name, dev):
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32, got {w.dtype}")
+    _need(w, name, w.dtype, dev)
+    if w.shape != (HEAD_DIM,):
+        raise ValueError(f"{name} must be [{HEAD_DIM}]")
+
+
+def _norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, rope_sin, q_out, k_out,
+               q_weight, k_weight, eps, interleaved, d_err, max_blocks, stream):
+    dev = _on_device(k, "k")
+    T, k_stride = _need_rows(k, "k", NUM_KV_HEADS, dev)
+    q_stride = v_stride = S = row = mb = pages = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        q_stride = _need_rows(q, "q", NUM_Q_HEADS, dev, T)[1]
+        _need(q_out, "q_out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
+        if q_out.numel() != T * NUM_Q_HEADS * HEAD_DIM:
+            raise ValueError("q_out must be [T, 32, 64]")
+    elif q_weight is not None:
+        raise ValueError("q_weight needs q")
+    if k_out is not None:
+        _need(k_out, "k_out", torch.bfloat16, dev, (NUM_KV_HEADS, HEAD_DIM))
+        if k_out.numel() != T * NUM_KV_HEADS * HEAD_DIM:
+            raise ValueError("k_out must be [T, 8, 64]")
+    _need(positions, "positions", torch.int32, dev)
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    if kv_pool is not None:
+        _need(kv_pool, "kv_pool", torch.bfloat16, dev, (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM))
+        v_stride = _need_rows(v, "v", NUM_KV_HEADS, dev, T)[1]
+        _need(block_tables, "block_tables", torch.int32, dev)
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must be [num_seqs, row_stride]")
+        if token_seq is not None:
+            _need(token_seq, "token_seq", torch.int32, dev)
+            if token_seq.numel() != T:
+                raise ValueError("token_seq must have one entry per token")
+        S, row = block_tables.shape
+        mb = row if max_blocks is None else max_blocks
+        pages = kv_pool.numel() // (2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM)
+    _need(rope_cos, "rope_cos", torch.float32, dev)
+    _need(rope_sin, "rope_sin", torch.float32, dev)
+    if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape or not 1 <= rope_cos.shape[1] <= ROPE_PAIRS:
+        raise ValueError("rope_cos and rope_sin must be [max_pos, pairs] with 1 to 32 pairs")
+    dtypes = set()
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_weight(w, name, dev)
+            dtypes.add(w.dtype)
+    if len(dtypes) > 1:
+        raise TypeError("q_weight and k_weight must have the same dtype")
+    if d_err is not None:
+        _need(d_err, "d_err", torch.int32, dev)
+    if T == 0:
+        return
+    _call(dev, stream, "kv_append_norm_rope", _addr(q), q_stride, k.data_ptr(), k_stride,
+          v.data_ptr() if kv_pool is not None else None, v_stride, _addr(q_weight), _addr(k_weight),
+          int(torch.float32 in dtypes), eps, rope_cos.data_ptr(), rope_sin.data_ptr(), rope_cos.shape[0],
+          rope_cos.shape[1], int(bool(interleaved)), positions.data_ptr(), _addr(token_seq), T,
+          _addr(block_tables), S, row, mb, _addr(kv_pool), pages, _addr(q_out), _addr(k_out),
+          _addr(d_err))
+
+
+def kv_append_norm_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin, token_seq=None,
+                        q_in=None, q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
+                        interleaved=False, d_err=None, max_blocks=None, stream=None):
+    """kv_append_rope for models that normalise the heads of q and k (RMS over
+    the 64 dims, then q_weight / k_weight), rotate only the first
+    2 * rope_cos.shape[1] dims, or pair the dims (2 i, 2 i + 1)
+    (interleaved=True): one pass from the projections' rows to the pages.
+
+    k, v [T, 8, 64] and q_in [T, 32, 64] bf16 may be slices of one fused
+    [T, 48, 64] projection (any token stride that is a multiple of 8).
+    rope_cos/sin [max_pos, pairs] fp32 (rope_tables_scaled_device).  Weights
+    [64] bf16 or fp32; None: not normalised.  Tokens and pages as for
+    kv_append_rope; k_out [T, 8, 64], if given, gets the K rows as well."""
+    _on_device(kv_pool, "kv_pool")
+    _norm_rope(q_in, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, rope_sin, q_out, k_out,
+               q_weight, k_weight, eps, interleaved, d_err, max_blocks, stream)
+
+
+def qk_norm_rope(q, k, positions, rope_cos, rope_sin, q_out, k_out, q_weight=None, k_weight=None,
+                 eps=1e-6, interleaved=False, d_err=None, stream=None):
+    """The q and k heads normalised and rotated as kv_append_norm_rope does,
+    into q_out and k_out, without an append (e.g. before kv_append_rope_bs8, or
+    for a prompt's own attention)."""
+    if k_out is None:
+        raise ValueError("k_out must be given")
+    _norm_rope(q, k, None, positions, None, None, None, rope_cos, rope_sin, q_out, k_out, q_weight,
+               k_weight, eps, interleaved, d_err, None, stream)
 
 
 # ------------------------------------------------------------------- decode --
@@ -524,6 +712,151 @@ def paged_gqa_decode_append_int8(q, k_new, v_new, kv_pool, block_tables, seq_len
     _check(st, "paged_gqa_decode_append_int8")
 
 
+# ------------------------------------------- block-scaled 8-bit pages (bs8) --
+
+BS8_CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def new_bs8_pool(num_pages: int, device, dtype=torch.int8):
+    """An empty block-scaled pool: (codes [num_pages, 2, 8, 16, 64] int8 or
+    float8_e4m3fn, scales [num_pages, 2, 8] fp32), all zero.  A code stands for
+    code * scale of its (page, K|V, KV head)."""
+    if dtype not in BS8_CODES:
+        raise TypeError(f"dtype must be one of {list(BS8_CODES)}")
+    codes = torch.zeros((num_pages, 2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM), dtype=torch.int8, device=device)
+    return codes.view(dtype), torch.zeros((num_pages, 2, NUM_KV_HEADS), dtype=torch.float32, device=device)
+
+
+def _need_bs8(kv_pool, kv_scales):
+    """Checks a pool and its scales; returns (device, pages, code type)."""
+    dev = _on_device(kv_pool, "kv_pool")
+    if kv_pool.dtype not in BS8_CODES:
+        raise TypeError(f"kv_pool must be int8 or float8_e4m3fn, got {kv_pool.dtype}")
+    if tuple(kv_pool.shape[1:]) != (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM) or not kv_pool.is_contiguous():
+        raise ValueError("kv_pool must be a contiguous [num_pages, 2, 8, 16, 64]")
+    pages = kv_pool.shape[0]
+    _need(kv_scales, "kv_scales", torch.float32, dev)
+    if tuple(kv_scales.shape) != (pages, 2, NUM_KV_HEADS):
+        raise ValueError("kv_scales must be [num_pages, 2, 8]")
+    return dev, pages, BS8_CODES[kv_pool.dtype]
+
+
+def kv_append_rope_bs8(k, v, cu_new, seq_lens, block_tables, kv_pool, kv_scales, rope_cos=None,
+                       rope_sin=None, q_in=None, q_out=None, d_err=None, max_blocks=None, stream=None):
+    """The newest tokens of every sequence written into block-scaled 8-bit pages.
+
+    Rows cu_new[s] .. cu_new[s + 1] - 1 of k and v are the last tokens of the
+    seq_lens[s] that sequence s then holds (cu_new = arange for a decode step).
+    With tables [max_pos, 32], K (and q_in into q_out) are rotated as in
+    kv_append_rope; without, K is taken as it is.  The new tokens of a block
+    set its scale together, and a block whose scale grows has its held codes
+    written again (pkv.h).  k, v [T, 8, 64], q_in [T, 32, 64] bf16 with any
+    token stride that is a multiple of 8."""
+    dev, pages, code = _need_bs8(kv_pool, kv_scales)
+    T, k_stride = _need_rows(k, "k", NUM_KV_HEADS, dev)
+    v_stride, q_stride, max_pos = _need_rows(v, "v", NUM_KV_HEADS, dev, T)[1], 0, 0
+    _need(cu_new, "cu_new", torch.int32, dev)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    S = seq_lens.numel()
+    if cu_new.numel() != S + 1:
+        raise ValueError("cu_new must have num_seqs + 1 entries")
+    _need(block_tables, "block_tables", torch.int32, dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] < S:
+        raise ValueError("block_tables must be [>= num_seqs, row_stride]")
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    if rope_cos is not None:
+        _need(rope_cos, "rope_cos", torch.float32, dev, (ROPE_PAIRS,))
+        _need(rope_sin, "rope_sin", torch.float32, dev, (ROPE_PAIRS,))
+        max_pos = rope_cos.numel() // ROPE_PAIRS
+        if rope_sin.numel() != rope_cos.numel():
+            raise ValueError("rope_cos and rope_sin must have the same shape")
+    if (q_in is None) != (q_out is None):
+        raise ValueError("q_in and q_out go together")
+    if q_in is not None:
+        if rope_cos is None:
+            raise ValueError("q_in needs rope_cos and rope_sin")
+        q_stride = _need_rows(q_in, "q_in", NUM_Q_HEADS, dev, T)[1]
+        _need(q_out, "q_out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
+        if q_out.numel() != T * NUM_Q_HEADS * HEAD_DIM:
+            raise ValueError("q_out must be [T, 32, 64]")
+    if d_err is not None:
+        _need(d_err, "d_err", torch.int32, dev)
+    if T == 0 or S == 0:
+        return
+    row = block_tables.shape[1]
+    _call(dev, stream, "kv_append_rope_bs8", k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+          cu_new.data_ptr(), seq_lens.data_ptr(), T, block_tables.data_ptr(), S, row,
+          row if max_blocks is None else max_blocks, kv_pool.data_ptr(), kv_scales.data_ptr(), pages,
+          code, _addr(rope_cos), _addr(rope_sin), max_pos, _addr(q_in), q_stride, _addr(q_out),
+          _addr(d_err))
+
+
+def kv_read_bs8(kv_pool, kv_scales, page_ids, out=None, d_err=None, stream=None):
+    """Pages page_ids of a block-scaled pool as bf16 pages
+    [len(page_ids), 2, 8, 16, 64] (a bf16 pool, e.g. for paged_gqa_prefill over
+    a cached prefix with block table 0 .. n - 1)."""
+    dev, pages, code = _need_bs8(kv_pool, kv_scales)
+    _need(page_ids, "page_ids", torch.int32, dev)
+    n = page_ids.numel()
+    if out is None:
+        out = torch.empty((n, 2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev, (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM))
+    if out.numel() != n * 2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM:
+        raise ValueError("out must hold one bf16 page per page id")
+    if d_err is not None:
+        _need(d_err, "d_err", torch.int32, dev)
+    if n:
+        _call(dev, stream, "kv_read_bs8", kv_pool.data_ptr(), kv_scales.data_ptr(), pages, code,
+              page_ids.data_ptr(), n, out.data_ptr(), _addr(d_err))
+    return out
+
+
+def paged_gqa_decode_bs8_workspace_bytes(num_seqs: int) -> int:
+    return int(_L().paged_gqa_decode_bs8_workspace_bytes(num_seqs))
+
+
+def alloc_bs8_workspace(num_seqs: int, device) -> torch.Tensor:
+    """Caller-owned workspace for paged_gqa_decode_bs8 of up to num_seqs sequences."""
+    with torch.cuda.device(device):
+        n = paged_gqa_decode_bs8_workspace_bytes(num_seqs)
+    if n <= 0:
+        raise PkvError(5, "paged_gqa_decode_bs8_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, scale, workspace=None,
+                         max_seq_len=None, d_err=None, max_blocks=None, stream=None):
+    """paged_gqa_decode over block-scaled 8-bit pages (new_bs8_pool): q, out
+    [num_seqs, 32, 64] bf16, q rotated.  workspace: alloc_bs8_workspace, one
+    for each stream or captured graph that may run at the same time."""
+    dev, pages, code = _need_bs8(kv_pool, kv_scales)
+    _need(q, "q", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
+    _need(out, "out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
+    S = q.numel() // (NUM_Q_HEADS * HEAD_DIM)
+    if out.numel() != q.numel():
+        raise ValueError("out must match q")
+    _need(block_tables, "block_tables", torch.int32, dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] < S:
+        raise ValueError("block_tables must be [>= num_seqs, row_stride]")
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if seq_lens.numel() != S:
+        raise ValueError("seq_lens must have num_seqs entries")
+    if d_err is not None:
+        _need(d_err, "d_err", torch.int32, dev)
+    if S == 0:
+        return
+    row = block_tables.shape[1]
+    mb = row if max_blocks is None else max_blocks
+    if workspace is None:
+        workspace = alloc_bs8_workspace(S, dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    _call(dev, stream, "paged_gqa_decode_bs8", q.data_ptr(), kv_pool.data_ptr(), kv_scales.data_ptr(),
+          pages, code, block_tables.data_ptr(), row, mb, seq_lens.data_ptr(), S,
+          PAGE_TOKENS * mb if max_seq_len is None else int(max_seq_len), out.data_ptr(), float(scale),
+          workspace.data_ptr(), workspace.numel(), _addr(d_err))
+
+
 def paged_gqa_decode_append(q, k_new, v_new, kv_pool, block_tables, seq_lens, out, rope_cos,
                             rope_sin, scale, q_out=None, workspace=None, max_seq_len=None,
                             d_err=None, max_blocks=None, warps_per_cta=0, min_units_per_warp=0,
@@ -713,6 +1046,87 @@ def argmax_rows(logits, out=None, stream=None):
     _check(_L().pkv_argmax_f32(_ptr(logits), rows, vocab, logits.stride(0), _ptr(out),
                                _stream(stream)), "pkv_argmax_f32")
     return out
+
+
+LOGITS_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def process_logits(logits, out=None, ids=None, history=None, history_lens=None, prompt_lens=None,
+                   repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None,
+                   allow_mask=None, stream=None):
+    """Penalties, biases and a grammar's mask on next-token logits, and the next
+    token of each row; returns ids ([rows] int32, -1 where nothing is allowed).
+
+    logits [rows, vocab] fp32, bf16 or fp16 (row stride may exceed vocab).
+    out [rows, vocab] fp32 gets the processed logits (None: ids only; logits
+    itself for fp32: in place).  history [rows, H] int32: each row's prompt
+    ids, then the generated ones, history_lens [rows] of them, the first
+    prompt_lens [rows] from the prompt; repetition counts both, presence and
+    frequency the generated ones ([rows] fp32 each, None: off).  bias_ids /
+    bias_values [rows, B] int32 / fp32; ids outside the vocabulary are padding.
+    allow_mask [rows, >= ceil(vocab / 32)] int32, bit i % 32 of word i / 32 set:
+    token i is allowed."""
+    dev = _on_device(logits, "logits")
+    if logits.dtype not in LOGITS_DTYPES or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D float32, bfloat16 or float16 tensor")
+    rows, vocab = logits.shape
+    if vocab < 1 or (logits.stride(1) != 1 and vocab > 1):
+        raise ValueError("logits rows must be contiguous and not empty")
+    row_stride = logits.stride(0) if rows > 1 else vocab
+    out_stride = H = B = mask_stride = 0
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype != torch.float32:
+            raise TypeError("out must be a float32 tensor")
+        if out.device != dev or tuple(out.shape) != (rows, vocab) or (out.stride(1) != 1 and vocab > 1):
+            raise ValueError("out must be [rows, vocab] on the logits' device with contiguous rows")
+        out_stride = out.stride(0) if rows > 1 else vocab
+    if ids is None:
+        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+    else:
+        _need(ids, "ids", torch.int32, dev)
+        if ids.numel() != rows:
+            raise ValueError("ids must have one entry per row")
+    if history is None:
+        if any(t is not None for t in (history_lens, prompt_lens, repetition, presence, frequency)):
+            raise ValueError("lengths and penalties need a history")
+    else:
+        _need(history, "history", torch.int32, dev)
+        if history.dim() != 2 or history.shape[0] != rows:
+            raise ValueError("history must be [rows, H]")
+        H = history.shape[1]
+        if history_lens is None:
+            raise ValueError("history needs history_lens")
+        for t, name, dtype in ((history_lens, "history_lens", torch.int32),
+                               (prompt_lens, "prompt_lens", torch.int32),
+                               (repetition, "repetition", torch.float32),
+                               (presence, "presence", torch.float32),
+                               (frequency, "frequency", torch.float32)):
+            if t is not None:
+                _need(t, name, dtype, dev)
+                if t.numel() != rows:
+                    raise ValueError(f"{name} must have one entry per row")
+        if H == 0:  # nothing to count
+            history = history_lens = prompt_lens = repetition = presence = frequency = None
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        _need(bias_ids, "bias_ids", torch.int32, dev)
+        _need(bias_values, "bias_values", torch.float32, dev)
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != rows or bias_values.shape != bias_ids.shape:
+            raise ValueError("bias_ids and bias_values must be [rows, B]")
+        B = bias_ids.shape[1]
+    if allow_mask is not None:
+        _need(allow_mask, "allow_mask", torch.int32, dev)
+        if allow_mask.dim() != 2 or allow_mask.shape[0] != rows or allow_mask.shape[1] < (vocab + 31) // 32:
+            raise ValueError("allow_mask must be [rows, >= ceil(vocab / 32)]")
+        mask_stride = allow_mask.shape[1]
+    if rows == 0:
+        return ids
+    _call(dev, stream, "pkv_process_logits", logits.data_ptr(), LOGITS_DTYPES[logits.dtype], rows, vocab,
+          row_stride, _addr(out), out_stride, ids.data_ptr(), _addr(history), H, _addr(history_lens),
+          _addr(prompt_lens), _addr(repetition), _addr(presence), _addr(frequency), _addr(bias_ids),
+          _addr(bias_values), B, _addr(allow_mask), mask_stride)
+    return ids
 
 
 def pkv_read_device_error(d_err, clear: bool = True, stream=None) -> int:

@@ -1,0 +1,673 @@
+// One decode step of grouped-query attention over pages of 8-bit codes with
+// one scale per block (16 slots of one page, K or V, and KV head), sm_103a.
+//
+// For sequence s with n tokens, KV head g and its query heads h (flash
+// decoding, one pass with a running maximum, exponentials in base 2):
+//   x_j = scale log2(e) ks(page of j) (q_h . ck_j),  p_j = 2^(x_j - m)
+//   out_h = sum_pages vs(page) sum_{j in page} p_j cv_j / sum_j p_j
+// The scales are one number per page and head, so they multiply a page's
+// four scores and its finished P V product, and the codes themselves enter
+// the MMAs.
+//
+// Work: the pages of all sequences, one after another, are one long list;
+// every CTA takes an equal share of it (an even number of pages), whatever
+// the lengths.  A share that ends inside a sequence leaves a partial (o, m, l)
+// in the workspace, and a second kernel merges the parts of such sequences.
+// One CTA is a producer warp and 8 consumer warps, one per KV head: the
+// producer copies whole pages -- 16 KiB, all heads, one TMA box each -- into a
+// ring of stages of two pages, under the 64-byte swizzle, and every consumer
+// reads its head's 2 KiB of each page from there.
+//
+// A consumer's page: S = q K^T as m16n8k16 with the four query heads in rows
+// 0..3 (two n-tiles of 8 tokens, four k-steps), whose accumulator layout is
+// the B operand's of O^T = V^T P^T, so the probabilities never leave their
+// lanes; V^T is loaded by ldmatrix.trans on byte pairs, which puts the codes
+// of two tokens and two dims into one register.  Codes become fp16 exactly:
+// e4m3 by conversion, int8 by placing code + 128 into the mantissa of 1024
+// and subtracting 1152.  q is scaled per (sequence, KV head) by the power of
+// two that brings its largest value into [2^14, 2^15): exact in fp16 unless
+// smaller by 2^-31.  Probabilities carry a factor 2^14 that cancels in the
+// division and are rounded to fp16 for the product (half a step is 2^-12 of
+// one, against 2^-9 of the bf16 result); their sum is over the unrounded ones.
+//
+// Bound: memory, 1 KiB + 4 B of scales per token.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "bs8.cuh"
+#include "internal.h"
+#include "pkv.h"
+#include "ptx.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kHeads = PKV_NUM_KV_HEADS;
+constexpr int kConsumers = kHeads;                      // one warp per KV head
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kStages = 3;
+constexpr int kStagePages = 2;
+constexpr int kScaleBytes = 2 * kHeads * 4;             // of one page
+constexpr int kStageBytes = kStagePages * kBs8PageBytes;
+constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + kStagePages * kScaleBytes);
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxSeqsBs8 = 4096;
+constexpr int kMinPages = 4;                            // least share of a CTA
+constexpr uint32_t kWaitUs = 2000000;                   // limit of every wait
+constexpr float kLift = 14.f;                           // probabilities carry 2^14
+constexpr float kNothing = -1.f;                        // l of a part with a bad page
+
+// Workspace: per CTA two parts (of a sequence begun in an earlier CTA, and of
+// one that goes on in the next) of 32 heads, o [64] then (m, l) pairs; then
+// per sequence its first and last CTA.
+constexpr int kPartFloats = PKV_NUM_Q_HEADS * (PKV_HEAD_DIM + 2);
+
+struct Bs8DecodeParams {
+  const uint16_t* q;
+  const float* scales;
+  const int32_t *block_tables, *seq_lens;
+  uint16_t* out;
+  float* parts;
+  int2* span;  // [num_seqs] first and last CTA of a split sequence, or (-1, -1)
+  int* d_err;
+  float scale;
+  int num_pages, bt_stride, max_blocks, num_seqs, min_pages;
+};
+
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+constexpr uint32_t kMagic = 0x64646464u;   // bytes of 1024 in fp16
+constexpr uint32_t kOffset = 0x64806480u;  // 1152 twice
+
+// four consecutive codes -> (0, 1), (2, 3) as fp16 pairs
+template <bool kE4m3>
+__device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kE4m3) {
+    lo = cvt_e4m3x2(w);
+    hi = cvt_e4m3x2(w >> 16);
+  } else {
+    w ^= 0x80808080u;
+    lo = sub_f16x2(__byte_perm(w, kMagic, 0x4140), kOffset);
+    hi = sub_f16x2(__byte_perm(w, kMagic, 0x4342), kOffset);
+  }
+}
+
+// bytes (a0, a1, b0, b1) of two tokens a, b and two dims -> (a0, b0), (a1, b1)
+template <bool kE4m3>
+__device__ __forceinline__ void codes_by_dim(uint32_t w, uint32_t& d0, uint32_t& d1) {
+  if (kE4m3) {
+    w = __byte_perm(w, 0, 0x3120);
+    d0 = cvt_e4m3x2(w);
+    d1 = cvt_e4m3x2(w >> 16);
+  } else {
+    w ^= 0x80808080u;
+    d0 = sub_f16x2(__byte_perm(w, kMagic, 0x4240), kOffset);
+    d1 = sub_f16x2(__byte_perm(w, kMagic, 0x4341), kOffset);
+  }
+}
+
+// Pages that sequence s brings to the list: none for an empty or refused one.
+__device__ __forceinline__ int pages_of(const Bs8DecodeParams& p, int s, bool& refused) {
+  const int n = __ldg(p.seq_lens + s);
+  refused = n < 0 || n > (long long)p.max_blocks * PKV_PAGE_TOKENS;
+  return refused ? 0 : (n + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
+}
+
+struct Smem {
+  uint64_t full[kStages], empty[kStages];
+  long long sum[kThreads / 32 + 1];
+  long long before;  // pages before first_seq, the sequence that the CTA begins in
+  int first_seq;
+  int bad[kStages];
+};
+
+template <bool kE4m3>
+struct Head {  // a consumer's state for one segment
+  uint32_t qa[4], qb[4];  // q fragments: dims 16 t + 4 i, + 1 and + 2, + 3
+  float o[4][4];          // O^T: dims 16 c + 2 g (+ 1), heads 2 t, 2 t + 1
+  float m, l, unit;       // running maximum and this lane's sum of head g; scale of the scores
+
+  __device__ void start(const Bs8DecodeParams& p, int seq, int head) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float x[16];
+    if (g < PKV_GROUP) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + g) * PKV_HEAD_DIM + 16 * t);
+      const uint4 a = src[0], b = src[1];
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[2 * e] = bf16lo_to_f32(w[e]);
+        x[2 * e + 1] = bf16hi_to_f32(w[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+    // 2^up brings the largest |q| into [2^14, 2^15); none for 0, infinities and
+    // (through fmaxf, which drops them) rows of NaN alone.  up lies in
+    // [-113, 141]: two factors keep each a normal number.
+    int up = 0;
+    if (bits != 0 && bits < 0x7F800000u) up = 14 - max((int)(bits >> 23) - 127, -127);
+    const float f0 = __uint_as_float((uint32_t)(127 + up / 2) << 23);
+    const float f1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
+    const float d0 = __uint_as_float((uint32_t)(127 - up / 2) << 23);
+    const float d1 = __uint_as_float((uint32_t)(127 - (up - up / 2)) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      qa[i] = pack_f16x2(x[4 * i] * f0 * f1, x[4 * i + 1] * f0 * f1);
+      qb[i] = pack_f16x2(x[4 * i + 2] * f0 * f1, x[4 * i + 3] * f0 * f1);
+    }
+    unit = p.scale * 1.4426950408889634f * d0 * d1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+  }
+
+  // Two pages in shared memory at `pages`, scales at `scales`; `live` tokens of
+  // the 32 are the sequence's.
+  __device__ __forceinline__ void step(uint32_t pages, const float* scales, int head, int live) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float x[2][4];
+#pragma unroll
+    for (int u = 0; u < kStagePages; ++u) {
+      const float ks = scales[u * 2 * kHeads + head] * unit;
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        // K rows of 64 bytes, 16-byte chunks swizzled by (row / 2) % 4
+        const int row = 8 * tile + g;
+        const uint32_t at = pages + u * kBs8PageBytes + head * kBs8BlockBytes + row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b0, b1;
+          codes_in_order<kE4m3>(w[i], b0, b1);
+          mma_f16(d, qa[i], 0u, qb[i], 0u, b0, b1);
+        }
+        x[u][2 * tile] = d[0] * ks;
+        x[u][2 * tile + 1] = d[1] * ks;
+      }
+    }
+    const bool tail = live < kStagePages * PKV_PAGE_TOKENS;
+    if (tail) {
+#pragma unroll
+      for (int u = 0; u < kStagePages; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (u * PKV_PAGE_TOKENS + (e >> 1) * 8 + 2 * t + (e & 1) >= live) x[u][e] = -INFINITY;
+    }
+    float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                      fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (__any_sync(0xffffffffu, top > m)) {  // some head's maximum grows: rescale
+      const float now = fmaxf(m, top);
+      const float keep = m == -INFINITY ? 0.f : exp2_approx(m - now);
+      const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        o[c][0] *= k0;
+        o[c][1] *= k1;
+        o[c][2] *= k0;
+        o[c][3] *= k1;
+      }
+      l *= keep;
+      m = now;
+    }
+    const float shift = m - kLift;
+#pragma unroll
+    for (int u = 0; u < kStagePages; ++u) {
+      const float vs = scales[u * 2 * kHeads + kHeads + head];
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[u][e] - shift);
+      l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+      const uint32_t b0 = pack_f16x2(pr[0], pr[1]), b1 = pack_f16x2(pr[2], pr[3]);
+      // V^T: matrices of 8 tokens x 16 bytes, (chunk, tokens 0..7), (chunk, 8..15), and the next chunk's
+      const int row = lane & 15;
+      const uint32_t base = pages + u * kBs8PageBytes + (kHeads + head) * kBs8BlockBytes + row * 64;
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        const int chunk = 2 * c2 + (lane >> 4);
+        uint32_t w[4];
+        ldsm_x4_t(base + ((chunk ^ ((row >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+        if (tail) {  // codes behind the sequence's end may be anything, NaN among them
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = u * PKV_PAGE_TOKENS + (e & 1) * 8 + 2 * t;
+            if (tok >= live) w[e] = 0u;
+            else if (tok + 1 >= live) w[e] &= 0x0000FFFFu;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a0, a1, a2, a3;
+          codes_by_dim<kE4m3>(w[2 * h], a0, a1);
+          codes_by_dim<kE4m3>(w[2 * h + 1], a2, a3);
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(d, a0, a1, a2, a3, b0, b1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[2 * c2 + h][e] = fmaf(vs, d[e], o[2 * c2 + h][e]);
+        }
+      }
+    }
+  }
+
+  // The segment's result: the output rows, or a part for the merge.
+  __device__ void finish(const Bs8DecodeParams& p, int seq, int head, bool bad, float* part) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float sum = l + __shfl_xor_sync(0xffffffffu, l, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (part) {
+      if (g < PKV_GROUP && t == 0)
+        *reinterpret_cast<float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * (head * PKV_GROUP + g)) =
+            make_float2(m, bad ? kNothing : sum);
+      if (t < 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float* dst = part + (head * PKV_GROUP + 2 * t + h) * PKV_HEAD_DIM + 2 * g;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) *reinterpret_cast<float2*>(dst + 16 * c) = make_float2(o[c][h], o[c][2 + h]);
+        }
+      }
+      return;
+    }
+    const float s0 = __shfl_sync(0xffffffffu, sum, 8 * t & 31), s1 = __shfl_sync(0xffffffffu, sum, (8 * t + 4) & 31);
+    if (t < 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float inv = bad ? 0.f : 1.f / (h ? s1 : s0);
+        uint16_t* dst = p.out + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + 2 * t + h) * PKV_HEAD_DIM + 2 * g;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint32_t*>(dst + 16 * c) = bad ? 0u : pack_bf16x2(o[c][h] * inv, o[c][2 + h] * inv);
+      }
+    }
+  }
+};
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const __grid_constant__ CUtensorMap map,
+                                                                          const Bs8DecodeParams p) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ Smem sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t scale_at = ring + kStages * kStageBytes;
+  const float* scale_ptr = reinterpret_cast<const float*>(dyn + (scale_at - smem_u32(dyn)));
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kConsumers);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait();
+
+  // the list of pages: this thread's sequences, then the sums over all
+  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    bool refused;
+    mine += pages_of(p, s, refused);
+  }
+  long long run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
+  }
+  if (lane == 31) sh.sum[warp] = run;
+  __syncthreads();
+  long long before = run - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh.sum[w];
+    total += sh.sum[w];
+  }
+  const long long ctas = gridDim.x;
+  long long share = (total + ctas - 1) / ctas;
+  share = max(share + (share & 1), (long long)p.min_pages);
+  const long long begin = min(total, share * blockIdx.x), end = min(total, begin + share);
+  // where sequences of this thread's begin, who splits them, and which have nothing to read
+  {
+    long long at = before;
+    for (int s = s0; s < s1; ++s) {
+      bool refused;
+      const int n = pages_of(p, s, refused);
+      if (at <= begin && begin < at + n) {
+        sh.first_seq = s;
+        sh.before = at;
+      }
+      if (s % (int)ctas == (int)blockIdx.x) {
+        const int c0 = (int)(at / share), c1 = n ? (int)((at + n - 1) / share) : c0;
+        p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
+        if (n == 0) {
+          uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
+          for (int i = 0; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+          if (refused) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+        }
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  if (begin >= end) return;
+
+  int seq = sh.first_seq;
+  int page = (int)(begin - sh.before);  // of the sequence
+  long long at = begin;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == kConsumers) {  // producer
+    bool alive = true;
+    int filled = 0;
+    while (at < end && alive) {
+      bool refused;
+      const int pages = pages_of(p, seq, refused);
+      const int todo = (int)min((long long)(pages - page), end - at);
+      const int32_t* table = p.block_tables + (size_t)seq * p.bt_stride + page;
+      for (int i = 0; i < todo && alive; i += 32) {
+        int id = i + lane < todo ? __ldg(table + i + lane) : 0;
+        const bool wrong = id < 0 || id >= p.num_pages;
+        if (wrong) id = 0;
+        const uint32_t wrongs = __ballot_sync(0xffffffffu, wrong);
+        if (wrongs && lane == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+        for (int k = 0; k < 32 && i + k < todo; k += kStagePages) {
+          const int id0 = __shfl_sync(0xffffffffu, id, k), id1 = __shfl_sync(0xffffffffu, id, k + 1);
+          if (lane == 0) {
+            if (filled >= kStages && !mbar_wait_bounded(smem_u32(&sh.empty[stage]), phase ^ 1u, kWaitUs)) {
+              alive = false;
+            } else {
+              const int n = i + k + 1 < todo ? 2 : 1;
+              const uint32_t bar = smem_u32(&sh.full[stage]);
+              const uint32_t dst = ring + stage * kStageBytes, sc = scale_at + stage * kStagePages * kScaleBytes;
+              sh.bad[stage] = (wrongs >> k) & 3u;
+              mbar_arrive_expect_tx(bar, n * (kBs8PageBytes + kScaleBytes));
+              tma_load_page(dst, &map, id0, bar);
+              bulk_load(sc, p.scales + (size_t)id0 * 2 * kHeads, kScaleBytes, bar);
+              if (n == 2) {
+                tma_load_page(dst + kBs8PageBytes, &map, id1, bar);
+                bulk_load(sc + kScaleBytes, p.scales + (size_t)id1 * 2 * kHeads, kScaleBytes, bar);
+              }
+            }
+          }
+          alive = __shfl_sync(0xffffffffu, (int)alive, 0) != 0;
+          if (!alive) break;
+          ++filled;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      at += todo;
+      page = 0;
+      ++seq;
+      while (at < end && seq < p.num_seqs && pages_of(p, seq, refused) == 0) ++seq;
+    }
+    if (!alive) {  // every copy in flight lands before the CTA's shared memory goes
+      if (lane == 0) {
+        report_error(p.d_err, PKV_ERR_TIMEOUT);
+        for (int i = 0; i < kStages; ++i) {
+          const int back = (stage + i) % kStages;
+          mbar_wait_bounded(smem_u32(&sh.full[back]), back >= stage ? phase ^ 1u : phase, kWaitUs);
+        }
+      }
+    }
+    return;
+  }
+
+  const int head = warp;
+  Head<kE4m3> st;
+  bool alive = true;
+  while (at < end && alive) {
+    bool refused;
+    const int pages = pages_of(p, seq, refused);
+    const int len = __ldg(p.seq_lens + seq);
+    const int todo = (int)min((long long)(pages - page), end - at);
+    st.start(p, seq, head);
+    bool bad = false;
+    for (int i = 0; i < todo; i += kStagePages) {
+      if (!mbar_wait_bounded(smem_u32(&sh.full[stage]), phase, kWaitUs)) {
+        alive = false;
+        break;
+      }
+      const int n = min(kStagePages, todo - i);
+      bad |= sh.bad[stage] != 0;
+      st.step(ring + stage * kStageBytes, scale_ptr + stage * kStagePages * 2 * kHeads, head,
+              min(n * PKV_PAGE_TOKENS, len - (page + i) * PKV_PAGE_TOKENS));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!alive) break;
+    const bool whole = todo == pages;
+    // a part: of a sequence that began in an earlier CTA (slot 0) or begins here (slot 1)
+    float* part = whole ? nullptr : p.parts + ((size_t)blockIdx.x * 2 + (page > 0 ? 0 : 1)) * kPartFloats;
+    st.finish(p, seq, head, bad, part);
+    at += todo;
+    page = 0;
+    ++seq;
+    while (at < end && seq < p.num_seqs && pages_of(p, seq, refused) == 0) ++seq;
+  }
+  if (!alive && lane == 0) report_error(p.d_err, PKV_ERR_TIMEOUT);
+}
+
+// Merge of the parts of split sequences.  A CTA of 16 warps takes
+// `heads` query heads of one sequence, 16 / heads warps each; a warp's lanes
+// hold two dims each and walk every (16 / heads)-th part, and the warps of a
+// head meet in shared memory.  The order is fixed, so the result does not
+// depend on timing.  Few sequences have many parts each and get one head per
+// CTA; many have few parts and get 16.
+constexpr int kMergeWarps = 16;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) bs8_merge_kernel(const float* parts, const int2* span,
+                                                                     uint16_t* out, int heads) {
+  __shared__ float2 acc[kMergeWarps][32];
+  __shared__ float top[kMergeWarps], den[kMergeWarps];
+  __shared__ int bads[kMergeWarps];
+  const int ctas = PKV_NUM_Q_HEADS / heads;
+  const int seq = blockIdx.x / ctas;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = kMergeWarps / heads, me = warp % team;
+  const int head = (blockIdx.x % ctas) * heads + warp / team;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int2 c = span[seq];
+  if (c.x < 0) return;
+  float m = -INFINITY, l = 0.f;
+  float2 o = make_float2(0.f, 0.f);
+  bool bad = false;
+#pragma unroll 4
+  for (int i = c.x + me; i <= c.y; i += team) {
+    // the sequence begins in its first CTA (slot 1) and continues in the others (slot 0)
+    const float* part = parts + ((size_t)i * 2 + (i == c.x ? 1 : 0)) * kPartFloats;
+    const float2 ml = *reinterpret_cast<const float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * head);
+    const float2 v = *reinterpret_cast<const float2*>(part + head * PKV_HEAD_DIM + 2 * lane);
+    bad |= ml.y == kNothing;
+    const float now = fmaxf(m, ml.x);
+    const float a = m == -INFINITY ? 0.f : exp2_approx(m - now), b = exp2_approx(ml.x - now);
+    o.x = o.x * a + v.x * b;
+    o.y = o.y * a + v.y * b;
+    l = l * a + ml.y * b;
+    m = now;
+  }
+  acc[warp][lane] = o;
+  if (lane == 0) {
+    top[warp] = m;
+    den[warp] = l;
+    bads[warp] = bad;
+  }
+  __syncthreads();
+  if (me) return;
+  for (int w = warp + 1; w < warp + team; ++w) {
+    if (top[w] == -INFINITY && den[w] == 0.f && !bads[w]) continue;  // no part came to that warp
+    const float now = fmaxf(m, top[w]);
+    const float a = m == -INFINITY ? 0.f : exp2_approx(m - now), b = exp2_approx(top[w] - now);
+    const float2 v = acc[w][lane];
+    o.x = o.x * a + v.x * b;
+    o.y = o.y * a + v.y * b;
+    l = l * a + den[w] * b;
+    m = now;
+    bad |= bads[w] != 0;
+  }
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint32_t*>(out + ((size_t)seq * PKV_NUM_Q_HEADS + head) * PKV_HEAD_DIM + 2 * lane) =
+      bad ? 0u : pack_bf16x2(o.x * inv, o.y * inv);
+}
+
+size_t parts_bytes(int sms) { return (size_t)sms * kCtasPerSm * 2 * kPartFloats * sizeof(float); }
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" size_t paged_gqa_decode_bs8_workspace_bytes(int num_seqs) {
+  if (num_seqs < 0 || num_seqs > kMaxSeqsBs8) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  const int sms = sm_count(dev);
+  if (sms <= 0) return 0;
+  return parts_bytes(sms) + (size_t)(num_seqs > 0 ? num_seqs : 1) * sizeof(int2);
+}
+
+extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_scales, int num_pages,
+                                    int code_type, const int32_t* block_tables, int bt_row_stride,
+                                    int max_blocks, const int32_t* seq_lens, int num_seqs, int max_seq_len,
+                                    void* out, float scale, void* workspace, size_t workspace_bytes,
+                                    int* d_err, void* stream) {
+  if (num_seqs < 0 || num_pages < 1 || max_blocks < 1 || bt_row_stride < max_blocks || max_seq_len < 0 ||
+      (code_type != PKV_BS8_INT8 && code_type != PKV_BS8_E4M3) || !isfinite(scale))
+    return PKV_ERR_INVALID_ARGUMENT;
+  if (num_seqs == 0) return PKV_OK;
+  if (!q || !kv_pool || !kv_scales || !block_tables || !seq_lens || !out || !workspace)
+    return PKV_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(kv_scales) || !aligned16(out) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
+        reinterpret_cast<uintptr_t>(d_err)) & 3u))
+    return PKV_ERR_MISALIGNED;
+  if (num_seqs > kMaxSeqsBs8 || max_blocks > (1 << 26)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  int dev = 0;
+  int rc = bind_stream_device(stream, &dev);
+  if (rc != PKV_OK) return rc;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
+  if (workspace_bytes < parts_bytes(sms) + (size_t)num_seqs * sizeof(int2)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+
+  Bs8DecodeParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.scales = kv_scales;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.parts = static_cast<float*>(workspace);
+  p.span = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes(sms));
+  p.d_err = d_err;
+  p.scale = scale;
+  p.num_pages = num_pages;
+  p.bt_stride = bt_row_stride;
+  p.max_blocks = max_blocks;
+  p.num_seqs = num_seqs;
+  p.min_pages = kMinPages;
+
+  CUtensorMap map;
+  rc = make_bs8_map(&map, kv_pool, num_pages);
+  if (rc != PKV_OK) return rc;
+  const bool e4m3 = code_type == PKV_BS8_E4M3;
+  rc = cuda_status(e4m3 ? cudaFuncSetAttribute(bs8_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemBytes)
+                        : cudaFuncSetAttribute(bs8_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemBytes),
+                   "cudaFuncSetAttribute(decode bs8)");
+  if (rc != PKV_OK) return rc;
+
+  // no more CTAs than the length bound can give work to (the shares follow the actual lengths)
+  const long long longest = max_seq_len > 0 ? max_seq_len : (long long)max_blocks * PKV_PAGE_TOKENS;
+  const long long most = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS * num_seqs;
+  long long ctas = (most + kMinPages - 1) / kMinPages;
+  if (ctas > (long long)sms * kCtasPerSm) ctas = (long long)sms * kCtasPerSm;
+  if (ctas < 1) ctas = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  rc = cuda_status(e4m3 ? cudaLaunchKernelEx(&cfg, bs8_decode_kernel<true>, map, p)
+                        : cudaLaunchKernelEx(&cfg, bs8_decode_kernel<false>, map, p),
+                   "cudaLaunchKernelEx(decode bs8)");
+  if (rc != PKV_OK || ctas == 1) return rc;  // one CTA splits nothing
+  const int heads = num_seqs <= 8 ? 1 : num_seqs <= 64 ? 8 : 16;
+  cfg.gridDim = dim3((unsigned)(num_seqs * (PKV_NUM_Q_HEADS / heads)));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, bs8_merge_kernel, (const float*)p.parts, (const int2*)p.span, p.out, heads),
+                     "cudaLaunchKernelEx(merge bs8)");
+}

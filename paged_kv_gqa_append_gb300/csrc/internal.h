@@ -38,6 +38,9 @@ int make_pool_map(CUtensorMap* map, const void* pool, int num_pages);
 // The same view with a one-tile box {64, 16, 1, 1}.
 int make_pool_tile_map(CUtensorMap* map, const void* pool, int num_pages);
 
+// TMA tensor map of a block-scaled 8-bit pool, one page per box.
+int make_bs8_map(CUtensorMap* map, const void* pool, int num_pages);
+
 // The host-side argument checks of paged_gqa_decode that need no workspace
 // and no CUDA call (sizes, null pointers, alignment, the scale): PKV_OK or
 // the status the decode call would return for these arguments.

@@ -89,4 +89,30 @@ int make_pool_tile_map(CUtensorMap* map, const void* pool, int num_pages) {
   return encode_4d(cache, map, pool, num_pages, dims, strides, box);
 }
 
+// A block-scaled 8-bit pool as bytes [num_pages][256][64], box {64, 256, 1}
+// (one page), 64-byte swizzle: rows of 64 bytes whose 16-byte chunks are
+// exchanged by (row / 2) % 4, so that both 16 consecutive rows at one chunk
+// (ldmatrix) and two rows whole fall on all 32 banks.
+int make_bs8_map(CUtensorMap* map, const void* pool, int num_pages) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) {
+    set_last_error("cudaGetDriverEntryPointByVersion", "cuTensorMapEncodeTiled unavailable");
+    return PKV_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {64, PKV_BS8_PAGE_BYTES / 64, (cuuint64_t)num_pages};
+  const cuuint64_t strides[2] = {64, PKV_BS8_PAGE_BYTES};
+  const cuuint32_t box[3] = {64, PKV_BS8_PAGE_BYTES / 64, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char msg[64];
+    snprintf(msg, sizeof(msg), "CUresult %d", (int)r);
+    set_last_error("cuTensorMapEncodeTiled(bs8)", msg);
+    return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
+}
+
 }  // namespace pkv
