@@ -293,9 +293,16 @@ def kv_append_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin,
     _check(st, "kv_append_rope")
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_KV_ROW, _Q_ROW = (NUM_KV_HEADS, HEAD_DIM), (NUM_Q_HEADS, HEAD_DIM)
+_KV_ROW_ELEMS, _Q_ROW_ELEMS = NUM_KV_HEADS * HEAD_DIM, NUM_Q_HEADS * HEAD_DIM
+_PAGE = (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM)
+_PAGE_ELEMS = 2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM
 
+
+# The checks below cost about 0.1 us per attribute of a tensor, which is what
+# a small call's host time is made of: each attribute is read once, and the
+# error messages are made only when a check fails (_need says what is wrong).
 
 def _on_device(t, name):
     """The CUDA device of `t`."""
@@ -306,104 +313,138 @@ def _on_device(t, name):
     return t.device
 
 
+def _vec(t, name, dtype, dev, n):
+    """`t` as a contiguous tensor of n elements; returns its address."""
+    try:
+        if t.dtype is dtype and t.device == dev and t.is_contiguous() and t.numel() == n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, dev)
+    raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _opt(t, name, dtype, dev, n):
+    return None if t is None else _vec(t, name, dtype, dev, n)
+
+
+def _rows(t, name, heads, dev, tokens=-1):
+    """`t` as token rows [T, heads, 64] bf16 with contiguous heads and any
+    token stride; returns (address, token stride, T)."""
+    try:
+        shape, stride = t.shape, t.stride()
+        if (t.dtype is _BF16 and t.device == dev and len(shape) == 3 and shape[1] == heads
+                and shape[2] == HEAD_DIM and stride[2] == 1 and stride[1] == HEAD_DIM
+                and (tokens < 0 or shape[0] == tokens)):
+            n = shape[0]
+            return t.data_ptr(), stride[0] if n > 1 else heads * HEAD_DIM, n
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    want = "T" if tokens < 0 else tokens
+    if len(shape) != 3 or tuple(shape[1:]) != (heads, HEAD_DIM) or (tokens >= 0 and shape[0] != tokens):
+        raise ValueError(f"{name} must be [{want}, {heads}, {HEAD_DIM}], got {tuple(shape)}")
+    raise ValueError(f"{name}: the heads of a token must be contiguous")
+
+
+def _block_rows(t, dev, rows=0):
+    """block_tables as (address, rows, row stride)."""
+    try:
+        shape = t.shape
+        if t.dtype is _I32 and t.device == dev and t.is_contiguous() and len(shape) == 2 and shape[0] >= rows:
+            return t.data_ptr(), shape[0], shape[1]
+    except AttributeError:
+        pass
+    _need(t, "block_tables", _I32, dev)
+    raise ValueError("block_tables must be [>= num_seqs, row_stride]")
+
+
+def _device_error(t, dev):
+    if t is None:
+        return None
+    try:
+        if t.dtype is _I32 and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, "d_err", _I32, dev)
+
+
 def _call(dev, stream, where, *args):
     """The C call `where` with the stream appended: the given one, or the
     current one of the tensors' device (made current for the call)."""
-    fn = getattr(_L(), where)
+    fn = getattr(_LIB or _L(), where)
     if stream is not None:
         st = fn(*args, stream.cuda_stream)
-    elif dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        index = dev.index
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        if index == torch._C._cuda_getDevice():
+            st = fn(*args, raw)
+        else:
+            with torch.cuda.device(dev):
+                st = fn(*args, raw)
     if st != OK:
         _check(st, where)
 
 
-def _need_rows(t, name, heads, dev, tokens=None):
-    """`t` as token rows [T, heads, 64] bf16 with contiguous heads and any
-    token stride; returns (T, token stride)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must be [T, {heads}, {HEAD_DIM}], got {tuple(shape)}")
-    if tokens is not None and shape[0] != tokens:
-        raise ValueError(f"{name} must have {tokens} tokens, got {shape[0]}")
-    stride = t.stride()
-    if stride[2] != 1 or stride[1] != HEAD_DIM:
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return shape[0], stride[0] if shape[0] > 1 else heads * HEAD_DIM
+def _empty(shape, dtype, dev, stream):
+    """A new tensor for a call on `stream`: allocated there, so that the
+    allocator neither hands out memory that another stream still uses nor
+    reuses it before the call has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _need_weight(w, name, dev):
-    if w.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be bfloat16 or float32, got {w.dtype}")
-    _need(w, name, w.dtype, dev)
-    if w.shape != (HEAD_DIM,):
-        raise ValueError(f"{name} must be [{HEAD_DIM}]")
+def _weight(w, name, dev):
+    """(address, whether fp32) of a norm's weights."""
+    if w is None:
+        return None, None
+    if getattr(w, "dtype", None) not in (_BF16, _F32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return _vec(w, name, w.dtype, dev, HEAD_DIM), w.dtype is _F32
 
 
 def _norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, rope_sin, q_out, k_out,
                q_weight, k_weight, eps, interleaved, d_err, max_blocks, stream):
     dev = _on_device(k, "k")
-    T, k_stride = _need_rows(k, "k", NUM_KV_HEADS, dev)
-    q_stride = v_stride = S = row = mb = pages = 0
+    k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
+    q_ptr = v_ptr = bt = pool = seq = None
+    q_stride = v_stride = S = row = pages = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        q_stride = _need_rows(q, "q", NUM_Q_HEADS, dev, T)[1]
-        _need(q_out, "q_out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
-        if q_out.numel() != T * NUM_Q_HEADS * HEAD_DIM:
-            raise ValueError("q_out must be [T, 32, 64]")
+        q_ptr, q_stride, _ = _rows(q, "q", NUM_Q_HEADS, dev, T)
     elif q_weight is not None:
         raise ValueError("q_weight needs q")
-    if k_out is not None:
-        _need(k_out, "k_out", torch.bfloat16, dev, (NUM_KV_HEADS, HEAD_DIM))
-        if k_out.numel() != T * NUM_KV_HEADS * HEAD_DIM:
-            raise ValueError("k_out must be [T, 8, 64]")
-    _need(positions, "positions", torch.int32, dev)
-    if positions.numel() != T:
-        raise ValueError("positions must have one entry per token")
+    qo, ko = _opt(q_out, "q_out", _BF16, dev, T * _Q_ROW_ELEMS), _opt(k_out, "k_out", _BF16, dev, T * _KV_ROW_ELEMS)
+    pos = _vec(positions, "positions", _I32, dev, T)
     if kv_pool is not None:
-        _need(kv_pool, "kv_pool", torch.bfloat16, dev, (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM))
-        v_stride = _need_rows(v, "v", NUM_KV_HEADS, dev, T)[1]
-        _need(block_tables, "block_tables", torch.int32, dev)
-        if block_tables.dim() != 2:
-            raise ValueError("block_tables must be [num_seqs, row_stride]")
-        if token_seq is not None:
-            _need(token_seq, "token_seq", torch.int32, dev)
-            if token_seq.numel() != T:
-                raise ValueError("token_seq must have one entry per token")
-        S, row = block_tables.shape
-        mb = row if max_blocks is None else max_blocks
-        pages = kv_pool.numel() // (2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM)
-    _need(rope_cos, "rope_cos", torch.float32, dev)
-    _need(rope_sin, "rope_sin", torch.float32, dev)
-    if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape or not 1 <= rope_cos.shape[1] <= ROPE_PAIRS:
+        _need(kv_pool, "kv_pool", _BF16, dev, _PAGE)
+        pool, pages = kv_pool.data_ptr(), kv_pool.numel() // _PAGE_ELEMS
+        v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
+        bt, S, row = _block_rows(block_tables, dev)
+        seq = _opt(token_seq, "token_seq", _I32, dev, T)
+    shape = rope_cos.shape
+    if len(shape) != 2 or not 1 <= shape[1] <= ROPE_PAIRS or rope_sin.shape != shape:
         raise ValueError("rope_cos and rope_sin must be [max_pos, pairs] with 1 to 32 pairs")
-    dtypes = set()
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_weight(w, name, dev)
-            dtypes.add(w.dtype)
-    if len(dtypes) > 1:
+    n = shape[0] * shape[1]
+    cos, sin = _vec(rope_cos, "rope_cos", _F32, dev, n), _vec(rope_sin, "rope_sin", _F32, dev, n)
+    qw, q_f32 = _weight(q_weight, "q_weight", dev)
+    kw, k_f32 = _weight(k_weight, "k_weight", dev)
+    if q_f32 is not None and k_f32 is not None and q_f32 != k_f32:
         raise TypeError("q_weight and k_weight must have the same dtype")
-    if d_err is not None:
-        _need(d_err, "d_err", torch.int32, dev)
+    err = _device_error(d_err, dev)
     if T == 0:
         return
-    _call(dev, stream, "kv_append_norm_rope", _addr(q), q_stride, k.data_ptr(), k_stride,
-          v.data_ptr() if kv_pool is not None else None, v_stride, _addr(q_weight), _addr(k_weight),
-          int(torch.float32 in dtypes), eps, rope_cos.data_ptr(), rope_sin.data_ptr(), rope_cos.shape[0],
-          rope_cos.shape[1], int(bool(interleaved)), positions.data_ptr(), _addr(token_seq), T,
-          _addr(block_tables), S, row, mb, _addr(kv_pool), pages, _addr(q_out), _addr(k_out),
-          _addr(d_err))
+    _call(dev, stream, "kv_append_norm_rope", q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, qw, kw,
+          1 if q_f32 or k_f32 else 0, eps, cos, sin, shape[0], shape[1], 1 if interleaved else 0, pos, seq, T,
+          bt, S, row, row if max_blocks is None else max_blocks, pool, pages, qo, ko, err)
 
 
 def kv_append_norm_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin, token_seq=None,
@@ -727,18 +768,17 @@ def new_bs8_pool(num_pages: int, device, dtype=torch.int8):
     return codes.view(dtype), torch.zeros((num_pages, 2, NUM_KV_HEADS), dtype=torch.float32, device=device)
 
 
-def _need_bs8(kv_pool, kv_scales):
-    """Checks a pool and its scales; returns (device, pages, code type)."""
+def _bs8_pool(kv_pool, kv_scales):
+    """Checks a pool and its scales; returns (device, pool address, scales
+    address, pages, code type)."""
     dev = _on_device(kv_pool, "kv_pool")
-    if kv_pool.dtype not in BS8_CODES:
+    shape = kv_pool.shape
+    code = BS8_CODES.get(kv_pool.dtype)
+    if code is None:
         raise TypeError(f"kv_pool must be int8 or float8_e4m3fn, got {kv_pool.dtype}")
-    if tuple(kv_pool.shape[1:]) != (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM) or not kv_pool.is_contiguous():
+    if shape[1:] != _PAGE or not kv_pool.is_contiguous():
         raise ValueError("kv_pool must be a contiguous [num_pages, 2, 8, 16, 64]")
-    pages = kv_pool.shape[0]
-    _need(kv_scales, "kv_scales", torch.float32, dev)
-    if tuple(kv_scales.shape) != (pages, 2, NUM_KV_HEADS):
-        raise ValueError("kv_scales must be [num_pages, 2, 8]")
-    return dev, pages, BS8_CODES[kv_pool.dtype]
+    return dev, kv_pool.data_ptr(), _vec(kv_scales, "kv_scales", _F32, dev, shape[0] * 2 * NUM_KV_HEADS), shape[0], code
 
 
 def kv_append_rope_bs8(k, v, cu_new, seq_lens, block_tables, kv_pool, kv_scales, rope_cos=None,
@@ -752,63 +792,52 @@ def kv_append_rope_bs8(k, v, cu_new, seq_lens, block_tables, kv_pool, kv_scales,
     set its scale together, and a block whose scale grows has its held codes
     written again (pkv.h).  k, v [T, 8, 64], q_in [T, 32, 64] bf16 with any
     token stride that is a multiple of 8."""
-    dev, pages, code = _need_bs8(kv_pool, kv_scales)
-    T, k_stride = _need_rows(k, "k", NUM_KV_HEADS, dev)
-    v_stride, q_stride, max_pos = _need_rows(v, "v", NUM_KV_HEADS, dev, T)[1], 0, 0
-    _need(cu_new, "cu_new", torch.int32, dev)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
+    dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
+    k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
+    v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
     S = seq_lens.numel()
-    if cu_new.numel() != S + 1:
-        raise ValueError("cu_new must have num_seqs + 1 entries")
-    _need(block_tables, "block_tables", torch.int32, dev)
-    if block_tables.dim() != 2 or block_tables.shape[0] < S:
-        raise ValueError("block_tables must be [>= num_seqs, row_stride]")
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    cu = _vec(cu_new, "cu_new", _I32, dev, S + 1)
+    bt, _, row = _block_rows(block_tables, dev, S)
+    cos = sin = q_ptr = q_dst = None
+    max_pos = q_stride = 0
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin go together")
     if rope_cos is not None:
-        _need(rope_cos, "rope_cos", torch.float32, dev, (ROPE_PAIRS,))
-        _need(rope_sin, "rope_sin", torch.float32, dev, (ROPE_PAIRS,))
-        max_pos = rope_cos.numel() // ROPE_PAIRS
-        if rope_sin.numel() != rope_cos.numel():
-            raise ValueError("rope_cos and rope_sin must have the same shape")
+        shape = rope_cos.shape
+        if len(shape) != 2 or shape[1] != ROPE_PAIRS:
+            raise ValueError("rope_cos and rope_sin must be [max_pos, 32]")
+        max_pos = shape[0]
+        cos = _vec(rope_cos, "rope_cos", _F32, dev, max_pos * ROPE_PAIRS)
+        sin = _vec(rope_sin, "rope_sin", _F32, dev, max_pos * ROPE_PAIRS)
     if (q_in is None) != (q_out is None):
         raise ValueError("q_in and q_out go together")
     if q_in is not None:
         if rope_cos is None:
             raise ValueError("q_in needs rope_cos and rope_sin")
-        q_stride = _need_rows(q_in, "q_in", NUM_Q_HEADS, dev, T)[1]
-        _need(q_out, "q_out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
-        if q_out.numel() != T * NUM_Q_HEADS * HEAD_DIM:
-            raise ValueError("q_out must be [T, 32, 64]")
-    if d_err is not None:
-        _need(d_err, "d_err", torch.int32, dev)
+        q_ptr, q_stride, _ = _rows(q_in, "q_in", NUM_Q_HEADS, dev, T)
+        q_dst = _vec(q_out, "q_out", _BF16, dev, T * _Q_ROW_ELEMS)
+    err = _device_error(d_err, dev)
     if T == 0 or S == 0:
         return
-    row = block_tables.shape[1]
-    _call(dev, stream, "kv_append_rope_bs8", k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-          cu_new.data_ptr(), seq_lens.data_ptr(), T, block_tables.data_ptr(), S, row,
-          row if max_blocks is None else max_blocks, kv_pool.data_ptr(), kv_scales.data_ptr(), pages,
-          code, _addr(rope_cos), _addr(rope_sin), max_pos, _addr(q_in), q_stride, _addr(q_out),
-          _addr(d_err))
+    _call(dev, stream, "kv_append_rope_bs8", k_ptr, k_stride, v_ptr, v_stride, cu, lens, T, bt, S, row,
+          row if max_blocks is None else max_blocks, pool, scales, pages, code, cos, sin, max_pos, q_ptr,
+          q_stride, q_dst, err)
 
 
 def kv_read_bs8(kv_pool, kv_scales, page_ids, out=None, d_err=None, stream=None):
     """Pages page_ids of a block-scaled pool as bf16 pages
     [len(page_ids), 2, 8, 16, 64] (a bf16 pool, e.g. for paged_gqa_prefill over
     a cached prefix with block table 0 .. n - 1)."""
-    dev, pages, code = _need_bs8(kv_pool, kv_scales)
-    _need(page_ids, "page_ids", torch.int32, dev)
+    dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
     n = page_ids.numel()
+    ids = _vec(page_ids, "page_ids", _I32, dev, n)
     if out is None:
-        out = torch.empty((n, 2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev, (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM))
-    if out.numel() != n * 2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM:
-        raise ValueError("out must hold one bf16 page per page id")
-    if d_err is not None:
-        _need(d_err, "d_err", torch.int32, dev)
+        out = _empty((n, *_PAGE), _BF16, dev, stream)
+    dst = _vec(out, "out", _BF16, dev, n * _PAGE_ELEMS)
+    err = _device_error(d_err, dev)
     if n:
-        _call(dev, stream, "kv_read_bs8", kv_pool.data_ptr(), kv_scales.data_ptr(), pages, code,
-              page_ids.data_ptr(), n, out.data_ptr(), _addr(d_err))
+        _call(dev, stream, "kv_read_bs8", pool, scales, pages, code, ids, n, dst, err)
     return out
 
 
@@ -816,13 +845,14 @@ def paged_gqa_decode_bs8_workspace_bytes(num_seqs: int) -> int:
     return int(_L().paged_gqa_decode_bs8_workspace_bytes(num_seqs))
 
 
-def alloc_bs8_workspace(num_seqs: int, device) -> torch.Tensor:
-    """Caller-owned workspace for paged_gqa_decode_bs8 of up to num_seqs sequences."""
+def alloc_bs8_workspace(num_seqs: int, device, stream=None) -> torch.Tensor:
+    """Caller-owned workspace for paged_gqa_decode_bs8 of up to num_seqs
+    sequences (allocated on `stream`, default the current one)."""
     with torch.cuda.device(device):
         n = paged_gqa_decode_bs8_workspace_bytes(num_seqs)
     if n <= 0:
-        raise PkvError(5, "paged_gqa_decode_bs8_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        raise PkvError(3 if num_seqs > 4096 else 5, "paged_gqa_decode_bs8_workspace_bytes")
+    return _empty(n, torch.uint8, device, stream)
 
 
 def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, scale, workspace=None,
@@ -830,31 +860,25 @@ def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, sca
     """paged_gqa_decode over block-scaled 8-bit pages (new_bs8_pool): q, out
     [num_seqs, 32, 64] bf16, q rotated.  workspace: alloc_bs8_workspace, one
     for each stream or captured graph that may run at the same time."""
-    dev, pages, code = _need_bs8(kv_pool, kv_scales)
-    _need(q, "q", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
-    _need(out, "out", torch.bfloat16, dev, (NUM_Q_HEADS, HEAD_DIM))
-    S = q.numel() // (NUM_Q_HEADS * HEAD_DIM)
-    if out.numel() != q.numel():
-        raise ValueError("out must match q")
-    _need(block_tables, "block_tables", torch.int32, dev)
-    if block_tables.dim() != 2 or block_tables.shape[0] < S:
-        raise ValueError("block_tables must be [>= num_seqs, row_stride]")
-    _need(seq_lens, "seq_lens", torch.int32, dev)
-    if seq_lens.numel() != S:
-        raise ValueError("seq_lens must have num_seqs entries")
-    if d_err is not None:
-        _need(d_err, "d_err", torch.int32, dev)
+    dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
+    shape = q.shape
+    if shape[-2:] != _Q_ROW:
+        raise ValueError(f"q must end in shape {_Q_ROW}, got {tuple(shape)}")
+    n = q.numel()
+    S = n // _Q_ROW_ELEMS
+    q_ptr, dst = _vec(q, "q", _BF16, dev, n), _vec(out, "out", _BF16, dev, n)
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    bt, _, row = _block_rows(block_tables, dev, S)
+    mb = row if max_blocks is None else max_blocks
+    err = _device_error(d_err, dev)
     if S == 0:
         return
-    row = block_tables.shape[1]
-    mb = row if max_blocks is None else max_blocks
     if workspace is None:
-        workspace = alloc_bs8_workspace(S, dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    _call(dev, stream, "paged_gqa_decode_bs8", q.data_ptr(), kv_pool.data_ptr(), kv_scales.data_ptr(),
-          pages, code, block_tables.data_ptr(), row, mb, seq_lens.data_ptr(), S,
-          PAGE_TOKENS * mb if max_seq_len is None else int(max_seq_len), out.data_ptr(), float(scale),
-          workspace.data_ptr(), workspace.numel(), _addr(d_err))
+        workspace = alloc_bs8_workspace(S, dev, stream)
+    size = workspace.numel()
+    _call(dev, stream, "paged_gqa_decode_bs8", q_ptr, pool, scales, pages, code, bt, row, mb, lens, S,
+          PAGE_TOKENS * mb if max_seq_len is None else max_seq_len, dst, scale,
+          _vec(workspace, "workspace", torch.uint8, dev, size), size, err)
 
 
 def paged_gqa_decode_append(q, k_new, v_new, kv_pool, block_tables, seq_lens, out, rope_cos,
@@ -1067,65 +1091,62 @@ def process_logits(logits, out=None, ids=None, history=None, history_lens=None, 
     allow_mask [rows, >= ceil(vocab / 32)] int32, bit i % 32 of word i / 32 set:
     token i is allowed."""
     dev = _on_device(logits, "logits")
-    if logits.dtype not in LOGITS_DTYPES or logits.dim() != 2:
+    shape, stride, dtype = logits.shape, logits.stride(), LOGITS_DTYPES.get(logits.dtype)
+    if dtype is None or len(shape) != 2:
         raise TypeError("logits must be a 2-D float32, bfloat16 or float16 tensor")
-    rows, vocab = logits.shape
-    if vocab < 1 or (logits.stride(1) != 1 and vocab > 1):
+    rows, vocab = shape
+    if vocab < 1 or (stride[1] != 1 and vocab > 1):
         raise ValueError("logits rows must be contiguous and not empty")
-    row_stride = logits.stride(0) if rows > 1 else vocab
+    dst = hist = h_lens = p_lens = rep = pres = freq = b_ids = b_vals = mask = None
     out_stride = H = B = mask_stride = 0
     if out is not None:
-        if not isinstance(out, torch.Tensor) or out.dtype != torch.float32:
+        if getattr(out, "dtype", None) is not _F32:
             raise TypeError("out must be a float32 tensor")
-        if out.device != dev or tuple(out.shape) != (rows, vocab) or (out.stride(1) != 1 and vocab > 1):
+        out_stride = out.stride()
+        if out.device != dev or out.shape != shape or (out_stride[1] != 1 and vocab > 1):
             raise ValueError("out must be [rows, vocab] on the logits' device with contiguous rows")
-        out_stride = out.stride(0) if rows > 1 else vocab
+        dst, out_stride = out.data_ptr(), out_stride[0] if rows > 1 else vocab
     if ids is None:
-        ids = torch.empty(rows, dtype=torch.int32, device=dev)
-    else:
-        _need(ids, "ids", torch.int32, dev)
-        if ids.numel() != rows:
-            raise ValueError("ids must have one entry per row")
+        ids = _empty(rows, _I32, dev, stream)
+    id_ptr = _vec(ids, "ids", _I32, dev, rows)
     if history is None:
-        if any(t is not None for t in (history_lens, prompt_lens, repetition, presence, frequency)):
+        if not (history_lens is prompt_lens is repetition is presence is frequency is None):
             raise ValueError("lengths and penalties need a history")
     else:
-        _need(history, "history", torch.int32, dev)
-        if history.dim() != 2 or history.shape[0] != rows:
+        h_shape = history.shape
+        if len(h_shape) != 2 or h_shape[0] != rows:
             raise ValueError("history must be [rows, H]")
-        H = history.shape[1]
         if history_lens is None:
             raise ValueError("history needs history_lens")
-        for t, name, dtype in ((history_lens, "history_lens", torch.int32),
-                               (prompt_lens, "prompt_lens", torch.int32),
-                               (repetition, "repetition", torch.float32),
-                               (presence, "presence", torch.float32),
-                               (frequency, "frequency", torch.float32)):
-            if t is not None:
-                _need(t, name, dtype, dev)
-                if t.numel() != rows:
-                    raise ValueError(f"{name} must have one entry per row")
+        H = h_shape[1]
+        hist = _vec(history, "history", _I32, dev, rows * H)
+        h_lens = _vec(history_lens, "history_lens", _I32, dev, rows)
+        p_lens = _opt(prompt_lens, "prompt_lens", _I32, dev, rows)
+        rep = _opt(repetition, "repetition", _F32, dev, rows)
+        pres = _opt(presence, "presence", _F32, dev, rows)
+        freq = _opt(frequency, "frequency", _F32, dev, rows)
         if H == 0:  # nothing to count
-            history = history_lens = prompt_lens = repetition = presence = frequency = None
+            hist = h_lens = p_lens = rep = pres = freq = None
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
-        _need(bias_ids, "bias_ids", torch.int32, dev)
-        _need(bias_values, "bias_values", torch.float32, dev)
-        if bias_ids.dim() != 2 or bias_ids.shape[0] != rows or bias_values.shape != bias_ids.shape:
+        b_shape = bias_ids.shape
+        if len(b_shape) != 2 or b_shape[0] != rows or bias_values.shape != b_shape:
             raise ValueError("bias_ids and bias_values must be [rows, B]")
-        B = bias_ids.shape[1]
+        B = b_shape[1]
+        b_ids = _vec(bias_ids, "bias_ids", _I32, dev, rows * B)
+        b_vals = _vec(bias_values, "bias_values", _F32, dev, rows * B)
     if allow_mask is not None:
-        _need(allow_mask, "allow_mask", torch.int32, dev)
-        if allow_mask.dim() != 2 or allow_mask.shape[0] != rows or allow_mask.shape[1] < (vocab + 31) // 32:
+        m_shape = allow_mask.shape
+        if len(m_shape) != 2 or m_shape[0] != rows or m_shape[1] < (vocab + 31) // 32:
             raise ValueError("allow_mask must be [rows, >= ceil(vocab / 32)]")
-        mask_stride = allow_mask.shape[1]
+        mask_stride = m_shape[1]
+        mask = _vec(allow_mask, "allow_mask", _I32, dev, rows * mask_stride)
     if rows == 0:
         return ids
-    _call(dev, stream, "pkv_process_logits", logits.data_ptr(), LOGITS_DTYPES[logits.dtype], rows, vocab,
-          row_stride, _addr(out), out_stride, ids.data_ptr(), _addr(history), H, _addr(history_lens),
-          _addr(prompt_lens), _addr(repetition), _addr(presence), _addr(frequency), _addr(bias_ids),
-          _addr(bias_values), B, _addr(allow_mask), mask_stride)
+    _call(dev, stream, "pkv_process_logits", logits.data_ptr(), dtype, rows, vocab,
+          stride[0] if rows > 1 else vocab, dst, out_stride, id_ptr, hist, H, h_lens, p_lens, rep, pres, freq,
+          b_ids, b_vals, B, mask, mask_stride)
     return ids
 
 
