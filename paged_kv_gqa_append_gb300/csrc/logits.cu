@@ -11,21 +11,32 @@
 // that the mask leaves, -1 if there is none.
 //
 // A cluster of 8 CTAs handles a row, each a contiguous eighth of the
-// vocabulary (a multiple of 32 tokens, one mask word).  A CTA keeps one word
-// per token of its part in shared memory -- how often it was generated,
-// whether it was seen at all, and the last bias entry + 1 -- and fills it from
-// the row's whole history and bias list, which it reads from L2: integer
-// atomics in its own shared memory, the same words in any order.  (Reading an
-// eighth each and adding through distributed shared memory took two cluster
-// barriers, and cost more than the reads.)  Then the part is streamed once, 16
-// bytes at a time, each thread keeping its best (value, id); warp shuffles,
-// shared memory and the cluster's first CTA reduce them under a total order.
-// The first loads of the stream are issued before the words are built.
+// vocabulary (a multiple of 32 tokens, one mask word).  The tokens that steps 1
+// to 3 change are few, so they are worked out first: a CTA reads the row's whole
+// history and bias list (from L2) and keeps those of its part in a hash table in
+// shared memory -- open addressing, 2048 slots, at most about half of them used
+// -- with how often a token was generated, whether it was seen at all, and its
+// last bias entry.  A warp first packs the ids of its share that are in the part
+// (an eighth, on average), so that the slower entering runs with full warps.
+// Integer atomics give the same numbers in any order, wherever a token's slot
+// is.  Whoever enters a token lists its slot, and the listed ones are then
+// finished, one thread each, and taken out of the bitmap of the tokens that the
+// stream is to handle, which starts as the mask.
+// A part with more than 1024 such tokens is done in passes over smaller ranges,
+// halved until one fits (a range of 1024 tokens always does).
 //
-// The word is 32 bits: 10 of bias entry, 1 seen, 21 of count, so that a part
-// of the 128256-token vocabulary is 64 KiB and three CTAs share an SM.  Longer
-// histories or more biases take 64-bit words; parts larger than the table go
-// in passes.
+// The stream over the part (16 bytes per load) tests a few bits per load and
+// treats what is not its own as -inf; the finished tokens are written over that,
+// and compete, behind it (looking them up from the stream made it five times as
+// long: some lane of a warp nearly always has one).  The table is
+// small on purpose: what shared memory takes from the L1 is missing as room for
+// loads in flight (a word per token of the part, 64 KiB a CTA, took 85 us for
+// 256 rows of 128256 with penalties and biases).  The ids and the stream's first
+// batch are loaded ahead, so that memory is busy while the table is filled.  A
+// thread keeps its largest value and its id; warp shuffles and shared memory reduce
+// them under a total order, and every CTA sends its best to the cluster's first
+// one, which alone waits for them (a closing cluster barrier kept all 8 until
+// the last had drained its stores).
 //
 // Bound: memory, the logits read (and written, when they are kept).
 #include <cooperative_groups.h>
@@ -34,7 +45,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <string.h>
 
 #include "internal.h"
 #include "pkv.h"
@@ -45,24 +55,31 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
 constexpr int kCtas = 8;
-constexpr int kTableBytes = 65536;
-constexpr int kBatch = 8;  // 16-byte loads in flight per thread
+constexpr int kMostTokens = 16384;  // of a pass: the bitmaps
+constexpr int kSlots = 2048;        // of the table
+constexpr int kList = 1024;         // tokens entered; a CTA's threads more may be before all see that it is full
+constexpr uint32_t kSeen = 1u << 31;
+constexpr uint32_t kEmpty = 0xFFFFFFFFu;
+constexpr uint32_t kMaskedBits = 0xFFFFDEADu;  // a NaN that stands for "masked out" in the table
+constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's other CTAs
 
-template <typename W>
-struct Word;
-template <>
-struct Word<uint32_t> {
-  static constexpr int kEntry = 22;
-  static constexpr uint32_t kSeen = 1u << 21;
-  static constexpr long long kMostHistory = (1 << 21) - 1, kMostBiases = (1 << 10) - 1;
+// How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
+// filled while others stream (256 x 128256 fp32 with penalties, biases and
+// output 68 us, with 2 x 512 threads 81 us).  When all CTAs fit on the GPU at
+// once there is nothing else to overlap with, and more threads shorten both
+// parts (32 x 128256 bf16 13.0 us, with 256 threads 16.0 us).
+struct Many {
+  static constexpr int kThreads = 256, kResident = 4;
+  static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
+  static constexpr int kIds = 8;    // ids in flight per thread, at most 8 (3 bits of the queue)
 };
-template <>
-struct Word<unsigned long long> {
-  static constexpr int kEntry = 32;
-  static constexpr unsigned long long kSeen = 1ull << 31;
+struct Few {
+  static constexpr int kThreads = 512, kResident = 2;
+  static constexpr int kBatch = 2;
+  static constexpr int kIds = 4;
 };
+
 
 struct LogitsParams {
   const void* logits;
@@ -74,7 +91,7 @@ struct LogitsParams {
   const int32_t* bias_ids;
   const float* bias_values;
   const uint32_t* mask;
-  int vocab, part, table, bias_count;  // tokens per CTA, tokens per pass
+  int vocab, part, bias_count;  // part: tokens per CTA
 };
 
 // 16 bytes of logits in fp32
@@ -114,38 +131,83 @@ __device__ __forceinline__ void take(float v, int i, float& bv, int& bi) {
   }
 }
 
+// 8 bytes into the shared memory of the cluster's first CTA, counted on its
+// barrier; both addresses as they are in this CTA's own window.
+__device__ __forceinline__ void send8(uint32_t dst, uint32_t bar, uint64_t value) {
+  asm volatile(
+      "{\n\t.reg .b32 a, b;\n\t"
+      "mapa.shared::cluster.u32 a, %0, 0;\n\tmapa.shared::cluster.u32 b, %1, 0;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %2, [b];\n\t}" ::"r"(dst),
+      "r"(bar), "l"(value)
+      : "memory");
+}
+
+// Phase 0 of `bar`, whose bytes come from other CTAs of the cluster; false after kWaitUs.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > (uint64_t)kWaitUs * 1000ull) return false;
+  }
+}
+
 struct Row {
   float rep, pres, freq;
   const float* bias;
 };
 
-// steps 1 to 3 for a token whose word is not 0
-template <typename W>
-__device__ __forceinline__ float change(float x, W word, const Row& r) {
-  using L = Word<W>;
-  const uint32_t n = (uint32_t)(word & (L::kSeen - 1));
-  if (word & (L::kSeen | (L::kSeen - 1))) x = x > 0.f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
-  if (n) {
-    x = __fsub_rn(x, __fmul_rn(r.freq, (float)n));
+// steps 1 to 3 for a token of the table: its count (with kSeen) and bias entry + 1
+__device__ __forceinline__ float change(float x, uint32_t count, uint32_t entry, const Row& r) {
+  if (count) x = x > 0.f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
+  count &= ~kSeen;
+  if (count) {
+    x = __fsub_rn(x, __fmul_rn(r.freq, (float)count));
     x = __fsub_rn(x, r.pres);
   }
-  const uint32_t entry = (uint32_t)(word >> L::kEntry);
   if (entry) x = __fadd_rn(x, __ldg(r.bias + entry - 1));
   return x;
 }
 
-template <typename T, typename W>
-__global__ void __launch_bounds__(kThreads, 3) logits_kernel(const LogitsParams p) {
-  using L = Word<W>;
+__device__ __forceinline__ uint32_t first_slot(int at) { return ((uint32_t)at * 2654435769u) >> 21; }
+static_assert(kSlots == 1 << 11, "first_slot");
+
+// A thread's share of a list of ids, kIds at a time (-1: none).
+template <int kThreads, int kIds>
+__device__ __forceinline__ void load_ids(const int32_t* ids, int k0, int count, int (&id)[kIds]) {
+#pragma unroll
+  for (int u = 0; u < kIds; ++u) id[u] = k0 + u * kThreads < count ? __ldg(ids + k0 + u * kThreads) : -1;
+}
+
+template <typename T, int kThreads, int kResident, int kBatch, int kIds>
+__global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const LogitsParams p) {
+  static_assert(kList + kThreads <= kSlots * 3 / 4 && kIds <= 8, "the table never fills up; the queue's bits");
   constexpr int N = 16 / (int)sizeof(T);  // tokens per 16 bytes
-  extern __shared__ __align__(16) uint8_t dyn[];
-  W* const table = reinterpret_cast<W*>(dyn);
-  __shared__ float best_v[kThreads / 32], part_v[kCtas];
-  __shared__ int best_i[kThreads / 32], part_i[kCtas];
+  // the table: token of the pass, its count (then its finished logit), its bias entry + 1
+  __shared__ __align__(16) uint32_t key[kSlots], count[kSlots], entry[kSlots];
+  __shared__ float best_v[kThreads / 32];
+  __shared__ int best_i[kThreads / 32];
+  __shared__ uint64_t best_of[kCtas], arrived;  // of the cluster's first CTA: (id, value bits) of all
+  __shared__ uint32_t allow[kMostTokens / 32];  // the stream's tokens, a bit per token of the pass
+  __shared__ uint16_t list[kList];
+  __shared__ uint32_t queue[kThreads / 32][kIds * 32];  // token of the pass, and which id of the round it is
+  __shared__ int listed;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int row = blockIdx.x / kCtas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (rank == 0 && threadIdx.x == 0) {
+    mbar_init(smem_u32(&arrived), 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(smem_u32(&arrived), kCtas * 8);
+  }
   cluster.barrier_arrive();  // waited for before the first write into another CTA's shared memory
   pdl_wait();
   pdl_launch_dependents();
@@ -153,119 +215,195 @@ __global__ void __launch_bounds__(kThreads, 3) logits_kernel(const LogitsParams 
   const T* x = static_cast<const T*>(p.logits) + (size_t)row * (size_t)p.stride;
   float* out = p.out ? p.out + (size_t)row * (size_t)p.out_stride : nullptr;
   const uint32_t* mask = p.mask ? p.mask + (size_t)row * (size_t)p.mask_stride : nullptr;
-  Row r{1.f, 0.f, 0.f, p.bias_values + (size_t)row * (size_t)p.bias_stride};
-  int hist = 0, prompt = 0;
-  if (p.history) {
-    hist = (int)max(0ll, min((long long)__ldg(p.history_lens + row), p.hist_stride));
-    prompt = p.prompt_lens ? __ldg(p.prompt_lens + row) : 0;
-    if (p.repetition) r.rep = __ldg(p.repetition + row);
-    if (p.presence) r.pres = __ldg(p.presence + row);
-    if (p.frequency) r.freq = __ldg(p.frequency + row);
-  }
-  const bool tables = hist > 0 || p.bias_count > 0;
+  const int32_t* history = p.history + (size_t)row * (size_t)p.hist_stride;
+  const int32_t* bias_ids = p.bias_ids + (size_t)row * (size_t)p.bias_stride;
 
-  float bv = -INFINITY;
+  float bv = -INFINITY;  // the largest value above -inf, and its id
   int bi = -1;
-  for (int base = 0; base < p.part; base += p.table) {
-    const long long first = (long long)rank * p.part + base;
-    const int size = min(p.table, p.part - base);  // tokens of this pass
-    const int n = (int)max(0ll, min((long long)size, (long long)p.vocab - first));
+  bool nothing_yet = true;
+  int span = min(p.part, kMostTokens);
+  for (int base = 0; base < p.part;) {
+    const int first = min(p.vocab, (int)min((long long)rank * p.part + base, (long long)p.vocab));
+    const int n = min(min(span, p.part - base), p.vocab - first);  // tokens of this pass
     const bool wide = ((reinterpret_cast<uintptr_t>(x + first) | (out ? reinterpret_cast<uintptr_t>(out + first) : 0)) & 15u) == 0;
     const int vecs = wide ? n / N : 0;
     const uint4* src = reinterpret_cast<const uint4*>(x + first);
+    int hist = 0, prompt = 0;
+    int hist_id[kIds], bias_id[kIds];  // the first of both lists
+    load_ids<kThreads>(history, threadIdx.x, (int)p.hist_stride, hist_id);
+    load_ids<kThreads>(bias_ids, threadIdx.x, p.bias_count, bias_id);
+    if (p.history) {
+      hist = (int)max(0ll, min((long long)__ldg(p.history_lens + row), p.hist_stride));
+      if (p.prompt_lens) prompt = __ldg(p.prompt_lens + row);
+    }
+    const bool bits = mask || p.history || p.bias_count > 0;
+    if (bits)
+      for (int i = threadIdx.x; i < (n + 31) / 32; i += kThreads) allow[i] = mask ? __ldg(mask + (first >> 5) + i) : 0xFFFFFFFFu;
     uint4 raw[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if ((int)threadIdx.x + u * kThreads < vecs) raw[u] = __ldcs(src + threadIdx.x + u * kThreads);
 
+    const bool tables = hist > 0 || p.bias_count > 0;
     if (tables) {
-      for (int i = threadIdx.x; i < size * (int)sizeof(W) / 16; i += kThreads)
-        reinterpret_cast<uint4*>(dyn)[i] = make_uint4(0, 0, 0, 0);
-      __syncthreads();
-      if (p.bias_count > 0) {
-        const int32_t* b = p.bias_ids + (size_t)row * (size_t)p.bias_stride;
-        for (int k = threadIdx.x; k < p.bias_count; k += kThreads) {
-          const long long at = (long long)__ldg(b + k) - first;
-          if (at >= 0 && at < n) atomicMax(table + at, (W)(k + 1) << L::kEntry);
+      // padding (negative, or behind the vocabulary) is in no part
+      const auto mine = [&](int id) { return id >= 0 && (unsigned)(id - first) < (unsigned)n; };
+      // the slot of token `at`, entered if it is new; -1 once the list is full
+      const auto slot_of = [&](int at, bool& entered) {
+        uint32_t i = first_slot(at);
+        for (int tries = 0; tries < kSlots; ++tries, i = (i + 1) & (kSlots - 1)) {
+          uint32_t k = *(volatile uint32_t*)(key + i);
+          if (k == (uint32_t)at) return (int)i;
+          if (k != kEmpty) continue;
+          if (*(volatile int*)&listed >= kList) return -1;
+          k = atomicCAS(key + i, kEmpty, (uint32_t)at);
+          entered = k == kEmpty;
+          if (entered || k == (uint32_t)at) return (int)i;
         }
-        __syncthreads();  // the maxima stand before counts come under them
-      }
-      if (hist > 0) {
-        const int32_t* h = p.history + (size_t)row * (size_t)p.hist_stride;
-        for (int k0 = threadIdx.x; k0 < hist; k0 += kBatch * kThreads) {
-          int id[kBatch];
+        return -1;
+      };
+      // f(slot, index in the list) for every id of the part: a warp packs its share's ids, then
+      // enters them with full warps
+      const auto enter = [&](const int32_t* ids, int total, const int (&head)[kIds], auto&& f) {
+        for (int k0 = threadIdx.x & ~31; k0 < total; k0 += kIds * kThreads) {
+          int id[kIds], packed = 0;
+          if (k0 < kThreads) {
 #pragma unroll
-          for (int u = 0; u < kBatch; ++u) id[u] = k0 + u * kThreads < hist ? __ldg(h + k0 + u * kThreads) : -1;
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const long long at = (long long)id[u] - first;
-            if (id[u] < 0 || at < 0 || at >= n) continue;
-            if (k0 + u * kThreads < prompt)
-              atomicOr(table + at, L::kSeen);
-            else
-              atomicAdd(table + at, (W)1);
+            for (int u = 0; u < kIds; ++u) id[u] = k0 + lane + u * kThreads < total ? head[u] : -1;
+          } else {
+            load_ids<kThreads>(ids, k0 + lane, total, id);
           }
-        }
-        __syncthreads();
-      }
-    }
-
-    for (int k0 = threadIdx.x; k0 < vecs; k0 += kBatch * kThreads) {
+          __syncwarp();  // the last round's queue has been read
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + u * kThreads;
-        if (k >= vecs) break;
-        float v[N];
-        widen(raw[u], v, (const T*)nullptr);
-        uint32_t allowed = (1u << N) - 1;
-        if (mask) allowed &= __ldg(mask + ((first + N * k) >> 5)) >> (N * k & 31);
-        if (tables) {
-#pragma unroll
-          for (int e0 = 0; e0 < N; e0 += 16 / (int)sizeof(W)) {
-            const uint4 words = *reinterpret_cast<const uint4*>(table + N * k + e0);
-            if (words.x | words.y | words.z | words.w) {
-              W w[16 / sizeof(W)];
-              memcpy(w, &words, 16);
-#pragma unroll
-              for (int e = 0; e < 16 / (int)sizeof(W); ++e)
-                if (w[e]) v[e0 + e] = change<W>(v[e0 + e], w[e], r);
+          for (int u = 0; u < kIds; ++u) {
+            const bool in = mine(id[u]);
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            if (in) queue[warp][packed + __popc(all & ((1u << lane) - 1))] = (uint32_t)(id[u] - first) << 8 | (uint32_t)(u << 5 | lane);
+            packed += __popc(all);
+          }
+          __syncwarp();
+          for (int i0 = 0; i0 < packed; i0 += 32) {
+            bool entered = false;
+            int slot = -1;
+            if (i0 + lane < packed) {
+              const uint32_t e = queue[warp][i0 + lane];
+              slot = slot_of((int)(e >> 8), entered);
+              if (slot >= 0) f(slot, k0 + (int)(e & 31u) + (int)(e >> 5 & 7u) * kThreads);
+            }
+            const uint32_t fresh = __ballot_sync(0xffffffffu, entered);
+            if (fresh) {
+              int where = 0;
+              if (lane == 0) where = atomicAdd(&listed, __popc(fresh));
+              where = __shfl_sync(0xffffffffu, where, 0) + __popc(fresh & ((1u << lane) - 1));
+              if (entered && where < kList) list[where] = (uint16_t)slot;
             }
           }
         }
-        float top = -INFINITY;
+      };
+      Row r{1.f, 0.f, 0.f, p.bias_values + (size_t)row * (size_t)p.bias_stride};
+      if (p.repetition) r.rep = __ldg(p.repetition + row);
+      if (p.presence) r.pres = __ldg(p.presence + row);
+      if (p.frequency) r.freq = __ldg(p.frequency + row);
+      for (int i = threadIdx.x; i < kSlots / 4; i += kThreads) {
+        reinterpret_cast<uint4*>(key)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+        reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(entry)[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (threadIdx.x == 0) listed = 0;
+      __syncthreads();
+      if (p.bias_count > 0)
+        enter(bias_ids, p.bias_count, bias_id, [&](int slot, int k) { atomicMax(entry + slot, (uint32_t)k + 1u); });
+      enter(history, hist, hist_id, [&](int slot, int k) {
+        if (k < prompt)
+          atomicOr(count + slot, kSeen);
+        else
+          atomicAdd(count + slot, 1u);
+      });
+      __syncthreads();
+      if (listed >= kList && n > kList) {  // it may be incomplete: a smaller range
+        span = max(kList, ((n + 1) / 2 + 31) & ~31);
+        __syncthreads();
+        continue;
+      }
+      for (int i = threadIdx.x; i < listed; i += kThreads) {
+        const int slot = list[i], at = (int)key[slot];
+        const float v = change(load1(x + first + at), count[slot], entry[slot], r);
+        // out of the stream's hands; one that was masked out before stays -inf
+        const bool was = atomicAnd(allow + (at >> 5), ~(1u << (at & 31))) >> (at & 31) & 1u;
+        count[slot] = was ? (v != v ? 0x7FFFFFFFu : __float_as_uint(v)) : kMaskedBits;
+      }
+    }
+    if (bits) __syncthreads();
+
+    // Whole batches have no branch inside, so that their tests and loads overlap; a thread's ids
+    // ascend, so of equal values the first stands.
+    for (int k0 = threadIdx.x; k0 < vecs; k0 += kBatch * kThreads) {
+      uint32_t allowed[kBatch];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          if (!((allowed >> e) & 1u)) v[e] = -INFINITY;
-          top = fmaxf(top, v[e]);  // fmaxf drops NaN
-        }
-        // a larger value came (or there is none yet): the ids of a thread ascend, so the first of it stands
-        if (top > bv || (bi < 0 && allowed)) {
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * kThreads;
+        allowed[u] = 0;
+        if (k < vecs) allowed[u] = (bits ? allow[N * k >> 5] >> (N * k & 31) : 0xFFu) & ((1u << N) - 1);
+      }
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            if ((allowed >> e) & 1u) take(v[e], (int)first + N * k + e, bv, bi);
-        }
-        if (out) {
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * kThreads;
+        float v[N];
+        widen(raw[u], v, (const T*)nullptr);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = (allowed[u] >> e) & 1u ? v[e] : -INFINITY;
+        float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));  // fmaxf drops NaN
+        if (N == 8) top = fmaxf(top, fmaxf(fmaxf(v[N - 4], v[N - 3]), fmaxf(v[N - 2], v[N - 1])));
+        int at = N - 1;
+#pragma unroll
+        for (int e = N - 2; e >= 0; --e) at = v[e] == top ? e : at;
+        const bool better = top > bv;
+        bv = better ? top : bv;
+        bi = better ? first + N * k + at : bi;
+        if (out && k < vecs) {
 #pragma unroll
           for (int e = 0; e < N; e += 4)
             __stcs(reinterpret_cast<float4*>(out + first + N * k + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
         }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + (kBatch + u) * kThreads;
-        if (k < vecs) raw[u] = __ldcs(src + k);
+        const int next = k + kBatch * kThreads;
+        if (next < vecs) raw[u] = __ldcs(src + next);
       }
     }
+    const auto single = [&](int k, bool& can) {
+      can = !bits || ((allow[k >> 5] >> (k & 31)) & 1u);
+      return can ? load1(x + first + k) : -INFINITY;
+    };
     for (int k = N * vecs + threadIdx.x; k < n; k += kThreads) {
-      float v = load1(x + first + k);
-      if (tables && table[k]) v = change<W>(v, table[k], r);
-      if (mask && !((__ldg(mask + ((first + k) >> 5)) >> (k & 31)) & 1u))
-        v = -INFINITY;
-      else
-        take(v, (int)first + k, bv, bi);
+      bool can;
+      const float v = single(k, can);
+      if (can && v > bv) {
+        bv = v;
+        bi = first + k;
+      }
       if (out) __stcs(out + first + k, v);
     }
-    if (base + p.table < p.part) __syncthreads();  // the next pass clears the table
+    if (tables) {
+      __syncthreads();  // the stream has written its -inf
+      for (int i = threadIdx.x; i < listed; i += kThreads) {
+        const int slot = list[i], id = first + (int)key[slot];
+        const uint32_t value = count[slot];
+        if (value != kMaskedBits) take(__uint_as_float(value), id, bv, bi);
+        if (out) out[id] = value != kMaskedBits ? __uint_as_float(value) : -INFINITY;
+      }
+    }
+    // Nothing above -inf in the part so far: the first -inf that is allowed counts (rare).
+    if (nothing_yet) {
+      nothing_yet = !__syncthreads_or(bv > -INFINITY);
+      if (nothing_yet) {
+        for (int k = threadIdx.x; k < n; k += kThreads) {
+          bool can;
+          const float v = single(k, can);
+          if (can) take(v, first + k, bv, bi);
+        }
+      }
+    }
+    base += min(span, p.part - base);
+    if (base < p.part) __syncthreads();  // the next pass uses the table again
   }
 
 #pragma unroll
@@ -289,33 +427,20 @@ __global__ void __launch_bounds__(kThreads, 3) logits_kernel(const LogitsParams 
       const int oi = __shfl_down_sync(0xffffffffu, bi, o);
       take(ov, oi, bv, bi);
     }
-    if (lane == 0) {
-      cluster.map_shared_rank(part_v, 0)[rank] = bv;
-      cluster.map_shared_rank(part_i, 0)[rank] = bi;
-    }
+    if (lane == 0 && p.ids)
+      send8(smem_u32(&best_of[rank]), smem_u32(&arrived),
+            (uint64_t)(uint32_t)bi << 32 | (uint64_t)__float_as_uint(bv));
   }
-  cluster.sync();
-  if (rank == 0 && threadIdx.x == 0 && p.ids) {
-    float v = 0.f;
-    int i = -1;
-    for (int k = 0; k < kCtas; ++k) take(part_v[k], part_i[k], v, i);
-    p.ids[row] = i;
-  }
+  if (rank != 0 || threadIdx.x != 0 || !p.ids) return;
+  float v = 0.f;
+  int i = -1;
+  if (wait_cluster(smem_u32(&arrived)))
+    for (int k = 0; k < kCtas; ++k) take(__uint_as_float((uint32_t)best_of[k]), (int)(best_of[k] >> 32), v, i);
+  p.ids[row] = i;
 }
 
-template <typename T, typename W>
-int launch_logits(LogitsParams& p, int rows, bool tables, cudaStream_t stream) {
-  size_t smem = 0;
-  p.table = p.part;
-  if (tables) {
-    constexpr int kMost = kTableBytes / (int)sizeof(W);
-    if (p.table > kMost) p.table = kMost;
-    smem = (size_t)p.table * sizeof(W);
-    const int rc = cuda_status(cudaFuncSetAttribute(logits_kernel<T, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    kTableBytes),
-                               "cudaFuncSetAttribute(logits)");
-    if (rc != PKV_OK) return rc;
-  }
+template <typename T, typename Shape>
+int launch_logits(const LogitsParams& p, int rows, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCtas;
@@ -325,20 +450,18 @@ int launch_logits(LogitsParams& p, int rows, bool tables, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * kCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(Shape::kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, logits_kernel<T, W>, p), "cudaLaunchKernelEx(logits)");
+  return cuda_status(cudaLaunchKernelEx(&cfg, logits_kernel<T, Shape::kThreads, Shape::kResident, Shape::kBatch, Shape::kIds>, p),
+                     "cudaLaunchKernelEx(logits)");
 }
 
 template <typename T>
-int launch_logits(LogitsParams& p, int rows, cudaStream_t stream) {
-  const bool tables = p.history || p.bias_count > 0;
-  const bool narrow = p.hist_stride <= Word<uint32_t>::kMostHistory && p.bias_count <= Word<uint32_t>::kMostBiases;
-  return narrow ? launch_logits<T, uint32_t>(p, rows, tables, stream)
-                : launch_logits<T, unsigned long long>(p, rows, tables, stream);
+int launch_logits(const LogitsParams& p, int rows, int sms, cudaStream_t stream) {
+  return (long long)rows * kCtas <= (long long)sms * Few::kResident ? launch_logits<T, Few>(p, rows, stream)
+                                                                   : launch_logits<T, Many>(p, rows, stream);
 }
 
 }  // namespace
@@ -401,7 +524,7 @@ extern "C" int pkv_process_logits(const void* logits, int dtype, int rows, int v
   p.bias_count = bias_count;
   p.part = ((vocab + kCtas - 1) / kCtas + 31) & ~31;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == PKV_LOGITS_F32) return launch_logits<float>(p, rows, st);
-  if (dtype == PKV_LOGITS_BF16) return launch_logits<__nv_bfloat16>(p, rows, st);
-  return launch_logits<__half>(p, rows, st);
+  if (dtype == PKV_LOGITS_F32) return launch_logits<float>(p, rows, sm_count(dev), st);
+  if (dtype == PKV_LOGITS_BF16) return launch_logits<__nv_bfloat16>(p, rows, sm_count(dev), st);
+  return launch_logits<__half>(p, rows, sm_count(dev), st);
 }

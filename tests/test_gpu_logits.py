@@ -75,7 +75,18 @@ def test_each_alone(lib, cuda_device, names):
     run(lib, cuda_device, case(6, 6, 2500, 77, 12), names, out=None)
 
 
-def test_vocabulary_larger_than_the_tables(lib, cuda_device):
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("vocab,hist,bias", [(20011, 30000, 0), (9001, 5, 6000), (16500, 12000, 4000), (8200, 20000, 1)])
+def test_more_changed_tokens_than_a_pass_holds(lib, cuda_device, dtype, vocab, hist, bias):
+    """Over 1024 distinct tokens in an eighth of the vocabulary: smaller passes."""
+    c = case(vocab, 3, vocab, hist, bias, dtype)
+    c["history"][:, ::2] = np.random.default_rng(vocab).integers(0, vocab, c["history"][:, ::2].shape)
+    c["history_lens"][:] = [hist, hist // 2, hist]
+    run(lib, cuda_device, c, NAMES)
+    run(lib, cuda_device, c, NAMES, out=None)
+
+
+def test_large_vocabulary(lib, cuda_device):
     """Over 8 x 16384 tokens the parts go in passes; the last one is ragged."""
     c = case(7, 2, 300001, 500, 50)
     c["history"][:, :100] = np.random.default_rng(1).integers(0, 300001, (2, 100))
