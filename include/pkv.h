@@ -634,7 +634,8 @@ int kv_read_bs8(const void* kv_pool, const float* kv_scales, int num_pages, int 
  *                bytes, 16-byte aligned, of any content: every call writes
  *                what it reads.  Calls that may run at the same time, two
  *                captured graphs among them, need distinct workspaces
- * At most 4096 sequences per call. */
+ * At most 4096 sequences, and fewer than 2^30 entries num_seqs * max_blocks of
+ * the tables. */
 size_t paged_gqa_decode_bs8_workspace_bytes(int num_seqs);
 int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_scales, int num_pages,
                          int code_type, const int32_t* block_tables, int bt_row_stride,

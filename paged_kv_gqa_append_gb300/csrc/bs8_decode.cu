@@ -158,8 +158,8 @@ __device__ __forceinline__ int pages_of(const Bs8DecodeParams& p, int s, bool& r
 
 struct Smem {
   uint64_t full[kStages], empty[kStages];
-  long long sum[kThreads / 32 + 1];
-  long long before;  // pages before first_seq, the sequence that the CTA begins in
+  int sum[kThreads / 32];
+  int before;  // pages before first_seq, the sequence that the CTA begins in
   int first_seq;
   int bad[kStages];
 };
@@ -357,34 +357,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   }
   pdl_wait();
 
-  // the list of pages: this thread's sequences, then the sums over all
-  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  // the list of pages (below 2^30 of them): this consumer thread's sequences, then the sums over all
+  const int per = (p.num_seqs + kConsumers * 32 - 1) / (kConsumers * 32);
   const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
-  long long mine = 0;
+  int mine = 0;
   for (int s = s0; s < s1; ++s) {
     bool refused;
     mine += pages_of(p, s, refused);
   }
-  long long run = mine;
+  int run = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, run, o);
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += v;
   }
   if (lane == 31) sh.sum[warp] = run;
   __syncthreads();
-  long long before = run - mine, total = 0;
+  int before = run - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sh.sum[w];
     total += sh.sum[w];
   }
-  const long long ctas = gridDim.x;
-  long long share = (total + ctas - 1) / ctas;
-  share = max(share + (share & 1), (long long)p.min_pages);
-  const long long begin = min(total, share * blockIdx.x), end = min(total, begin + share);
-  // where sequences of this thread's begin, who splits them, and which have nothing to read
-  {
-    long long at = before;
+  int share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+  share = max(share + (share & 1), p.min_pages);
+  const int begin = (int)min((unsigned)total, (unsigned)share * blockIdx.x), end = min(total, begin + share);
+  if (before <= begin && begin < before + mine) {
+    int at = before;
     for (int s = s0; s < s1; ++s) {
       bool refused;
       const int n = pages_of(p, s, refused);
@@ -392,8 +391,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
         sh.first_seq = s;
         sh.before = at;
       }
-      if (s % (int)ctas == (int)blockIdx.x) {
-        const int c0 = (int)(at / share), c1 = n ? (int)((at + n - 1) / share) : c0;
+      at += n;
+    }
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  // which CTAs share a sequence, and the rows of those with nothing to read, by one CTA for each
+  // sequence; the producer is past this already, and the consumers have no page yet
+  {
+    int at = before;
+    for (int s = s0; s < s1; ++s) {
+      bool refused;
+      const int n = pages_of(p, s, refused);
+      if (s % (int)gridDim.x == (int)blockIdx.x) {
+        const int c0 = (int)((unsigned)at / (unsigned)share), c1 = n ? (int)((unsigned)(at + n - 1) / (unsigned)share) : c0;
         p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
         if (n == 0) {
           uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
@@ -404,13 +415,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       at += n;
     }
   }
-  __syncthreads();
-  pdl_launch_dependents();
   if (begin >= end) return;
 
   int seq = sh.first_seq;
-  int page = (int)(begin - sh.before);  // of the sequence
-  long long at = begin;
+  int page = begin - sh.before;  // of the sequence
+  int at = begin;
   int stage = 0;
   uint32_t phase = 0;
 
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
     while (at < end && alive) {
       bool refused;
       const int pages = pages_of(p, seq, refused);
-      const int todo = (int)min((long long)(pages - page), end - at);
+      const int todo = min(pages - page, end - at);
       const int32_t* table = p.block_tables + (size_t)seq * p.bt_stride + page;
       for (int i = 0; i < todo && alive; i += 32) {
         int id = i + lane < todo ? __ldg(table + i + lane) : 0;
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
     bool refused;
     const int pages = pages_of(p, seq, refused);
     const int len = __ldg(p.seq_lens + seq);
-    const int todo = (int)min((long long)(pages - page), end - at);
+    const int todo = min(pages - page, end - at);
     st.start(p, seq, head);
     bool bad = false;
     for (int i = 0; i < todo; i += kStagePages) {
@@ -512,67 +521,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   if (!alive && lane == 0) report_error(p.d_err, PKV_ERR_TIMEOUT);
 }
 
-// Merge of the parts of split sequences.  A CTA of 16 warps takes
-// `heads` query heads of one sequence, 16 / heads warps each; a warp's lanes
-// hold two dims each and walk every (16 / heads)-th part, and the warps of a
-// head meet in shared memory.  The order is fixed, so the result does not
-// depend on timing.  Few sequences have many parts each and get one head per
-// CTA; many have few parts and get 16.
-constexpr int kMergeWarps = 16;
+// Merge of the parts of split sequences.  A CTA of 512 threads takes `heads`
+// query heads of one sequence.  All threads fetch the parts' (m, l), one warp
+// per head turns them into weights 2^(m - M) / L in shared memory, and
+// meanwhile every thread has its first part outputs in flight -- four dims of every
+// (32 / heads)-th part -- and then adds them up weighted, with no chain between
+// the loads.  The order is fixed, so the result does not depend on timing.  Few
+// sequences have many parts each and get one head per CTA; many have few parts
+// and get 8 or 16.
+constexpr int kMergeThreads = 512;
+constexpr int kMergeBatch = 8;
 
-__global__ void __launch_bounds__(kMergeWarps * 32) bs8_merge_kernel(const float* parts, const int2* span,
-                                                                     uint16_t* out, int heads) {
-  __shared__ float2 acc[kMergeWarps][32];
-  __shared__ float top[kMergeWarps], den[kMergeWarps];
-  __shared__ int bads[kMergeWarps];
+__global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* parts, const int2* span,
+                                                                  uint16_t* out, int heads) {
+  extern __shared__ float2 weights[];  // [heads][parts of the sequence]: (m, l), then (weight, -)
+  __shared__ float4 sums[kMergeThreads / 32][16];
+  __shared__ int bads[kMergeThreads / 32];
   const int ctas = PKV_NUM_Q_HEADS / heads;
-  const int seq = blockIdx.x / ctas;
+  const int seq = blockIdx.x / ctas, head0 = (blockIdx.x % ctas) * heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = kMergeWarps / heads, me = warp % team;
-  const int head = (blockIdx.x % ctas) * heads + warp / team;
   pdl_wait();
   pdl_launch_dependents();
   const int2 c = span[seq];
   if (c.x < 0) return;
-  float m = -INFINITY, l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
-  bool bad = false;
-#pragma unroll 4
-  for (int i = c.x + me; i <= c.y; i += team) {
-    // the sequence begins in its first CTA (slot 1) and continues in the others (slot 0)
-    const float* part = parts + ((size_t)i * 2 + (i == c.x ? 1 : 0)) * kPartFloats;
-    const float2 ml = *reinterpret_cast<const float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * head);
-    const float2 v = *reinterpret_cast<const float2*>(part + head * PKV_HEAD_DIM + 2 * lane);
-    bad |= ml.y == kNothing;
-    const float now = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.f : exp2_approx(m - now), b = exp2_approx(ml.x - now);
-    o.x = o.x * a + v.x * b;
-    o.y = o.y * a + v.y * b;
-    l = l * a + ml.y * b;
-    m = now;
+  const int n = c.y - c.x + 1;
+  // the sequence begins in its first CTA (slot 1) and continues in the others (slot 0)
+  const float* base = parts + (size_t)c.x * 2 * kPartFloats;
+  const auto part = [&](int i) { return base + ((size_t)i * 2 + (i == 0 ? 1 : 0)) * kPartFloats; };
+
+  const int per = kMergeThreads / heads;  // threads of a head
+  const int mine = threadIdx.x / per;
+  const int group = (threadIdx.x % per) >> 4, groups = per >> 4, dims = 4 * (threadIdx.x & 15);
+  const int at = (head0 + mine) * PKV_HEAD_DIM + dims;
+  float4 v[kMergeBatch];
+#pragma unroll
+  for (int u = 0; u < kMergeBatch; ++u) {
+    const int i = group + u * groups;
+    if (i < n) v[u] = *reinterpret_cast<const float4*>(part(i) + at);
   }
-  acc[warp][lane] = o;
-  if (lane == 0) {
-    top[warp] = m;
-    den[warp] = l;
-    bads[warp] = bad;
+  for (int i = threadIdx.x; i < n * heads; i += kMergeThreads)
+    weights[(i % heads) * n + i / heads] =
+        *reinterpret_cast<const float2*>(part(i / heads) + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * (head0 + i % heads));
+  __syncthreads();
+  if (warp < heads) {
+    float2* row = weights + warp * n;
+    float m = -INFINITY, sum = 0.f;
+    bool bad = false;
+    for (int i = lane; i < n; i += 32) {
+      m = fmaxf(m, row[i].x);
+      bad |= row[i].y == kNothing;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = lane; i < n; i += 32) {
+      const float w = exp2_approx(row[i].x - m);
+      sum = fmaf(row[i].y, w, sum);
+      row[i].x = w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) bads[warp] = bad;
+    const float inv = 1.f / sum;
+    for (int i = lane; i < n; i += 32) row[i].x *= inv;
   }
   __syncthreads();
-  if (me) return;
-  for (int w = warp + 1; w < warp + team; ++w) {
-    if (top[w] == -INFINITY && den[w] == 0.f && !bads[w]) continue;  // no part came to that warp
-    const float now = fmaxf(m, top[w]);
-    const float a = m == -INFINITY ? 0.f : exp2_approx(m - now), b = exp2_approx(top[w] - now);
-    const float2 v = acc[w][lane];
-    o.x = o.x * a + v.x * b;
-    o.y = o.y * a + v.y * b;
-    l = l * a + den[w] * b;
-    m = now;
-    bad |= bads[w] != 0;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = group; i0 < n; i0 += kMergeBatch * groups) {
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int i = i0 + u * groups;
+      if (i < n) {
+        const float w = weights[mine * n + i].x;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int i = i0 + (kMergeBatch + u) * groups;
+      if (i < n) v[u] = *reinterpret_cast<const float4*>(part(i) + at);
+    }
   }
-  const float inv = 1.f / l;
-  *reinterpret_cast<uint32_t*>(out + ((size_t)seq * PKV_NUM_Q_HEADS + head) * PKV_HEAD_DIM + 2 * lane) =
-      bad ? 0u : pack_bf16x2(o.x * inv, o.y * inv);
+  acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+  acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+  acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+  acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+  if (lane < 16) sums[warp][lane] = acc;
+  __syncthreads();
+  const int team = per >> 5;  // warps of a head
+  if (warp % team || lane >= 16) return;
+  for (int w = warp + 1; w < warp + team; ++w) {
+    const float4 e = sums[w][lane];
+    acc.x += e.x;
+    acc.y += e.y;
+    acc.z += e.z;
+    acc.w += e.w;
+  }
+  const bool bad = bads[mine] != 0;
+  *reinterpret_cast<uint2*>(out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM + at) =
+      bad ? make_uint2(0, 0) : make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
 size_t parts_bytes(int sms) { return (size_t)sms * kCtasPerSm * 2 * kPartFloats * sizeof(float); }
@@ -609,7 +659,7 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
       ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
         reinterpret_cast<uintptr_t>(d_err)) & 3u))
     return PKV_ERR_MISALIGNED;
-  if (num_seqs > kMaxSeqsBs8 || max_blocks > (1 << 26)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (num_seqs > kMaxSeqsBs8 || (long long)max_blocks * num_seqs >= (1ll << 30)) return PKV_ERR_UNSUPPORTED_SHAPE;
   int dev = 0;
   int rc = bind_stream_device(stream, &dev);
   if (rc != PKV_OK) return rc;
@@ -666,8 +716,8 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   if (rc != PKV_OK || ctas == 1) return rc;  // one CTA splits nothing
   const int heads = num_seqs <= 8 ? 1 : num_seqs <= 64 ? 8 : 16;
   cfg.gridDim = dim3((unsigned)(num_seqs * (PKV_NUM_Q_HEADS / heads)));
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.dynamicSmemBytes = 0;
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = (size_t)heads * ctas * sizeof(float2);
   return cuda_status(cudaLaunchKernelEx(&cfg, bs8_merge_kernel, (const float*)p.parts, (const int2*)p.span, p.out, heads),
                      "cudaLaunchKernelEx(merge bs8)");
 }
