@@ -270,7 +270,8 @@ struct Head {  // a consumer's state for one segment
     const float shift = m - kLift;
 #pragma unroll
     for (int u = 0; u < kStagePages; ++u) {
-      const float vs = scales[u * 2 * kHeads + kHeads + head];
+      // a page that the last stage does not have: whatever shared memory holds is no scale
+      const float vs = u * PKV_PAGE_TOKENS < live ? scales[u * 2 * kHeads + kHeads + head] : 0.f;
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[u][e] - shift);
@@ -522,24 +523,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
 }
 
 // Merge of the parts of split sequences.  A CTA of 512 threads takes `heads`
-// query heads of one sequence.  All threads fetch the parts' (m, l), one warp
-// per head turns them into weights 2^(m - M) / L in shared memory, and
-// meanwhile every thread has its first part outputs in flight -- four dims of every
-// (32 / heads)-th part -- and then adds them up weighted, with no chain between
-// the loads.  The order is fixed, so the result does not depend on timing.  Few
-// sequences have many parts each and get one head per CTA; many have few parts
-// and get 8 or 16.
+// query heads of one sequence; 16 lanes -- four dims each -- add up every
+// (32 / heads)-th part of a head, weighted by 2^(m - M) / L.  The same 16 lanes
+// first find M and L themselves from all parts' (m, l), so that nothing is
+// exchanged before the sums, and everything a thread needs is loaded at once:
+// this kernel is latency (the end of the decode kernel seen, the record, the
+// parts), about 3 us behind it.  The order is fixed, so the result does not
+// depend on timing.  Few sequences have many parts each and get one head per
+// CTA; many have few parts and get 8 or 16.
 constexpr int kMergeThreads = 512;
-constexpr int kMergeBatch = 8;
+constexpr int kMergeBatch = 8;  // parts in flight per thread
 
+// kKept: how many of all parts' (m, l) a lane has in flight and keeps, beyond
+// which it reads them twice: 20 for one head per CTA (320 parts, more than there
+// are CTAs; 4 would cost a long sequence 5 us), else 4.
+template <int kKept>
 __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* parts, const int2* span,
                                                                   uint16_t* out, int heads) {
-  extern __shared__ float2 weights[];  // [heads][parts of the sequence]: (m, l), then (weight, -)
   __shared__ float4 sums[kMergeThreads / 32][16];
-  __shared__ int bads[kMergeThreads / 32];
   const int ctas = PKV_NUM_Q_HEADS / heads;
-  const int seq = blockIdx.x / ctas, head0 = (blockIdx.x % ctas) * heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seq = blockIdx.x / ctas;
+  const int per = kMergeThreads / heads;  // threads of a head
+  const int head = (blockIdx.x % ctas) * heads + threadIdx.x / per;
+  const int group = (threadIdx.x % per) >> 4, groups = per >> 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
+  const int dims = head * PKV_HEAD_DIM + 4 * sub, ml = PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * head;
   pdl_wait();
   pdl_launch_dependents();
   const int2 c = span[seq];
@@ -548,70 +556,78 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
   // the sequence begins in its first CTA (slot 1) and continues in the others (slot 0)
   const float* base = parts + (size_t)c.x * 2 * kPartFloats;
   const auto part = [&](int i) { return base + ((size_t)i * 2 + (i == 0 ? 1 : 0)) * kPartFloats; };
+  const auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(part(i) + ml); };
 
-  const int per = kMergeThreads / heads;  // threads of a head
-  const int mine = threadIdx.x / per;
-  const int group = (threadIdx.x % per) >> 4, groups = per >> 4, dims = 4 * (threadIdx.x & 15);
-  const int at = (head0 + mine) * PKV_HEAD_DIM + dims;
+  float2 all[kKept];
+#pragma unroll
+  for (int u = 0; u < kKept; ++u) all[u] = sub + 16 * u < n ? ml_of(sub + 16 * u) : make_float2(-INFINITY, 0.f);
   float4 v[kMergeBatch];
+  float mine[kMergeBatch];
 #pragma unroll
   for (int u = 0; u < kMergeBatch; ++u) {
     const int i = group + u * groups;
-    if (i < n) v[u] = *reinterpret_cast<const float4*>(part(i) + at);
-  }
-  for (int i = threadIdx.x; i < n * heads; i += kMergeThreads)
-    weights[(i % heads) * n + i / heads] =
-        *reinterpret_cast<const float2*>(part(i / heads) + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * (head0 + i % heads));
-  __syncthreads();
-  if (warp < heads) {
-    float2* row = weights + warp * n;
-    float m = -INFINITY, sum = 0.f;
-    bool bad = false;
-    for (int i = lane; i < n; i += 32) {
-      m = fmaxf(m, row[i].x);
-      bad |= row[i].y == kNothing;
+    mine[u] = -INFINITY;
+    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
+      mine[u] = ml_of(i).x;
+      v[u] = *reinterpret_cast<const float4*>(part(i) + dims);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int i = lane; i < n; i += 32) {
-      const float w = exp2_approx(row[i].x - m);
-      sum = fmaf(row[i].y, w, sum);
-      row[i].x = w;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) bads[warp] = bad;
-    const float inv = 1.f / sum;
-    for (int i = lane; i < n; i += 32) row[i].x *= inv;
   }
-  __syncthreads();
+  float m = all[0].x;
+#pragma unroll
+  for (int u = 1; u < kKept; ++u) m = fmaxf(m, all[u].x);
+#pragma unroll 4
+  for (int i = sub + 16 * kKept; i < n; i += 16) m = fmaxf(m, ml_of(i).x);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float sum = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < kKept; ++u) {
+    if (sub + 16 * u < n) sum = fmaf(all[u].y, exp2_approx(all[u].x - m), sum);
+    bad |= all[u].y == kNothing;
+  }
+#pragma unroll 4
+  for (int i = sub + 16 * kKept; i < n; i += 16) {
+    const float2 e = ml_of(i);
+    sum = fmaf(e.y, exp2_approx(e.x - m), sum);
+    bad |= e.y == kNothing;
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16) & 0xFFFFu) != 0;
+
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = group; i0 < n; i0 += kMergeBatch * groups) {
+  for (int i0 = group;; i0 += kMergeBatch * groups) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int i = i0 + u * groups;
-      if (i < n) {
-        const float w = weights[mine * n + i].x;
-        acc.x = fmaf(w, v[u].x, acc.x);
-        acc.y = fmaf(w, v[u].y, acc.y);
-        acc.z = fmaf(w, v[u].z, acc.z);
-        acc.w = fmaf(w, v[u].w, acc.w);
-      }
+      if (i0 + u * groups >= n) continue;
+      const float w = exp2_approx(mine[u] - m);
+      acc.x = fmaf(w, v[u].x, acc.x);
+      acc.y = fmaf(w, v[u].y, acc.y);
+      acc.z = fmaf(w, v[u].z, acc.z);
+      acc.w = fmaf(w, v[u].w, acc.w);
     }
+    if (i0 + kMergeBatch * groups >= n) break;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
       const int i = i0 + (kMergeBatch + u) * groups;
-      if (i < n) v[u] = *reinterpret_cast<const float4*>(part(i) + at);
+      if (i < n) {
+        mine[u] = ml_of(i).x;
+        v[u] = *reinterpret_cast<const float4*>(part(i) + dims);
+      }
     }
   }
+  __syncwarp();
   acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
   acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
   acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
   acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-  if (lane < 16) sums[warp][lane] = acc;
-  __syncthreads();
   const int team = per >> 5;  // warps of a head
+  if (team > 1) {
+    if (lane < 16) sums[warp][lane] = acc;
+    __syncthreads();
+  }
   if (warp % team || lane >= 16) return;
   for (int w = warp + 1; w < warp + team; ++w) {
     const float4 e = sums[w][lane];
@@ -620,9 +636,10 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
     acc.z += e.z;
     acc.w += e.w;
   }
-  const bool bad = bads[mine] != 0;
-  *reinterpret_cast<uint2*>(out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM + at) =
-      bad ? make_uint2(0, 0) : make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  const float inv = 1.f / sum;
+  *reinterpret_cast<uint2*>(out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM + dims) =
+      bad ? make_uint2(0, 0)
+          : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 size_t parts_bytes(int sms) { return (size_t)sms * kCtasPerSm * 2 * kPartFloats * sizeof(float); }
@@ -717,7 +734,10 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   const int heads = num_seqs <= 8 ? 1 : num_seqs <= 64 ? 8 : 16;
   cfg.gridDim = dim3((unsigned)(num_seqs * (PKV_NUM_Q_HEADS / heads)));
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = (size_t)heads * ctas * sizeof(float2);
-  return cuda_status(cudaLaunchKernelEx(&cfg, bs8_merge_kernel, (const float*)p.parts, (const int2*)p.span, p.out, heads),
+  cfg.dynamicSmemBytes = 0;
+  const float* parts = p.parts;
+  const int2* span = p.span;
+  return cuda_status(heads == 1 ? cudaLaunchKernelEx(&cfg, bs8_merge_kernel<20>, parts, span, p.out, heads)
+                                : cudaLaunchKernelEx(&cfg, bs8_merge_kernel<4>, parts, span, p.out, heads),
                      "cudaLaunchKernelEx(merge bs8)");
 }

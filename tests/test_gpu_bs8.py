@@ -353,6 +353,26 @@ def test_decode_largest_batch_and_page_order(lib, cuda_device):
                np.zeros(S + 1, np.int32), workspace=torch.empty(1 << 27, dtype=torch.uint8, device=cuda_device))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_of_odd_pages_after_a_call_that_leaves_nan(lib, cuda_device, kind):
+    """Stages hold two pages; the missing one of an odd count must not matter,
+    whatever an earlier call left in shared memory."""
+    dev = cuda_device
+    big = [4000] * 20
+    codes, scales = random_pages(50, 5001, kind)
+    bt = tables_for(51, big, 5001)
+    lens = [3, 17, 33, 1, 48, 5, 81, 16] * 5
+    q = rows(52, len(lens), 32, 64)
+    bt2 = tables_for(53, lens, 5001)
+    want = O8.attend(q, codes, scales, bt2, lens, 0.125, kind)
+    nan = np.full_like(scales, np.nan)
+    for _ in range(3):
+        decode(lib, dev, kind, rows(54, 20, 32, 64), np.full_like(codes, 0x7F), nan, bt, big)
+        out, code = decode(lib, dev, kind, q, codes, scales, bt2, lens)
+        assert code == 0
+        close(out, *want, lens)
+
+
 def test_decode_workspace_streams_and_graphs(lib, cuda_device):
     """Any content of the workspace; two captured graphs with workspaces of
     their own on two streams at once; replays over other lengths."""
