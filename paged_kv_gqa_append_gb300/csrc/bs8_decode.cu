@@ -524,23 +524,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
 
 // Merge of the parts of split sequences.  A CTA of 512 threads takes `heads`
 // query heads of one sequence; 16 lanes -- four dims each -- add up every
-// (32 / heads)-th part of a head, weighted by 2^(m - M) / L.  The same 16 lanes
-// first find M and L themselves from all parts' (m, l), so that nothing is
-// exchanged before the sums, and everything a thread needs is loaded at once:
-// this kernel is latency (the end of the decode kernel seen, the record, the
-// parts), about 3 us behind it.  The order is fixed, so the result does not
-// depend on timing.  Few sequences have many parts each and get one head per
-// CTA; many have few parts and get 8 or 16.
+// (32 / heads)-th part of a head, weighted by 2^(m - M) / L, with everything a
+// thread needs loaded at once: this kernel is latency (the end of the decode
+// kernel seen, the record, the parts), about 3 us behind it.  The order is
+// fixed, so the result does not depend on timing.  Many sequences have few parts
+// each: 8 or 16 heads per CTA, and the 16 lanes find M and L themselves from all
+// parts' (m, l), so that nothing is exchanged before the sums.  Few sequences
+// have up to two parts per SM: one head per CTA, whose threads fetch one (m, l)
+// each and exchange M, L and the weights (16 warps that each fetch all of 304
+// cost 5 us).
 constexpr int kMergeThreads = 512;
 constexpr int kMergeBatch = 8;  // parts in flight per thread
+constexpr int kKept = 4;        // of all parts' (m, l): those that a lane has in flight and keeps
 
-// kKept: how many of all parts' (m, l) a lane has in flight and keeps, beyond
-// which it reads them twice: 20 for one head per CTA (320 parts, more than there
-// are CTAs; 4 would cost a long sequence 5 us), else 4.
-template <int kKept>
+template <bool kOneHead>
 __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* parts, const int2* span,
                                                                   uint16_t* out, int heads) {
+  extern __shared__ float weights[];  // one head: of all parts
   __shared__ float4 sums[kMergeThreads / 32][16];
+  __shared__ float tops[kMergeThreads / 32], dens[kMergeThreads / 32];
+  if (kOneHead) heads = 1;
   const int ctas = PKV_NUM_Q_HEADS / heads;
   const int seq = blockIdx.x / ctas;
   const int per = kMergeThreads / heads;  // threads of a head
@@ -559,8 +562,10 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
   const auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(part(i) + ml); };
 
   float2 all[kKept];
+  const int all0 = kOneHead ? threadIdx.x : sub, step = kOneHead ? kMergeThreads : 16;
 #pragma unroll
-  for (int u = 0; u < kKept; ++u) all[u] = sub + 16 * u < n ? ml_of(sub + 16 * u) : make_float2(-INFINITY, 0.f);
+  for (int u = 0; u < (kOneHead ? 1 : kKept); ++u)
+    all[u] = all0 + step * u < n ? ml_of(all0 + step * u) : make_float2(-INFINITY, 0.f);
   float4 v[kMergeBatch];
   float mine[kMergeBatch];
 #pragma unroll
@@ -569,40 +574,60 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
     mine[u] = -INFINITY;
     v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < n) {
-      mine[u] = ml_of(i).x;
+      if (!kOneHead) mine[u] = ml_of(i).x;
       v[u] = *reinterpret_cast<const float4*>(part(i) + dims);
     }
   }
-  float m = all[0].x;
-#pragma unroll
-  for (int u = 1; u < kKept; ++u) m = fmaxf(m, all[u].x);
-#pragma unroll 4
-  for (int i = sub + 16 * kKept; i < n; i += 16) m = fmaxf(m, ml_of(i).x);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float sum = 0.f;
+  float m = all[0].x, sum = 0.f;
   bool bad = false;
+  if (kOneHead) {
+    for (int i = all0 + step; i < n; i += step) m = fmaxf(m, ml_of(i).x);
 #pragma unroll
-  for (int u = 0; u < kKept; ++u) {
-    if (sub + 16 * u < n) sum = fmaf(all[u].y, exp2_approx(all[u].x - m), sum);
-    bad |= all[u].y == kNothing;
-  }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) tops[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, tops[w]);
+    for (int i = all0; i < n; i += step) {
+      const float2 e = i == all0 ? all[0] : ml_of(i);
+      weights[i] = exp2_approx(e.x - m);
+      sum = fmaf(e.y, weights[i], sum);
+      bad |= e.y == kNothing;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) dens[warp] = sum;
+    bad = __syncthreads_or(bad);
+    sum = 0.f;
+    for (int w = 0; w < kMergeThreads / 32; ++w) sum += dens[w];
+  } else {
+#pragma unroll
+    for (int u = 1; u < kKept; ++u) m = fmaxf(m, all[u].x);
 #pragma unroll 4
-  for (int i = sub + 16 * kKept; i < n; i += 16) {
-    const float2 e = ml_of(i);
-    sum = fmaf(e.y, exp2_approx(e.x - m), sum);
-    bad |= e.y == kNothing;
-  }
+    for (int i = all0 + step * kKept; i < n; i += step) m = fmaxf(m, ml_of(i).x);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16) & 0xFFFFu) != 0;
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int u = 0; u < kKept; ++u) {
+      if (all0 + step * u < n) sum = fmaf(all[u].y, exp2_approx(all[u].x - m), sum);
+      bad |= all[u].y == kNothing;
+    }
+#pragma unroll 4
+    for (int i = all0 + step * kKept; i < n; i += step) {
+      const float2 e = ml_of(i);
+      sum = fmaf(e.y, exp2_approx(e.x - m), sum);
+      bad |= e.y == kNothing;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16) & 0xFFFFu) != 0;
+  }
 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = group;; i0 += kMergeBatch * groups) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
       if (i0 + u * groups >= n) continue;
-      const float w = exp2_approx(mine[u] - m);
+      const float w = kOneHead ? weights[i0 + u * groups] : exp2_approx(mine[u] - m);
       acc.x = fmaf(w, v[u].x, acc.x);
       acc.y = fmaf(w, v[u].y, acc.y);
       acc.z = fmaf(w, v[u].z, acc.z);
@@ -613,7 +638,7 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
     for (int u = 0; u < kMergeBatch; ++u) {
       const int i = i0 + (kMergeBatch + u) * groups;
       if (i < n) {
-        mine[u] = ml_of(i).x;
+        if (!kOneHead) mine[u] = ml_of(i).x;
         v[u] = *reinterpret_cast<const float4*>(part(i) + dims);
       }
     }
@@ -734,10 +759,10 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   const int heads = num_seqs <= 8 ? 1 : num_seqs <= 64 ? 8 : 16;
   cfg.gridDim = dim3((unsigned)(num_seqs * (PKV_NUM_Q_HEADS / heads)));
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = heads == 1 ? (size_t)ctas * sizeof(float) : 0;
   const float* parts = p.parts;
   const int2* span = p.span;
-  return cuda_status(heads == 1 ? cudaLaunchKernelEx(&cfg, bs8_merge_kernel<20>, parts, span, p.out, heads)
-                                : cudaLaunchKernelEx(&cfg, bs8_merge_kernel<4>, parts, span, p.out, heads),
+  return cuda_status(heads == 1 ? cudaLaunchKernelEx(&cfg, bs8_merge_kernel<true>, parts, span, p.out, heads)
+                                : cudaLaunchKernelEx(&cfg, bs8_merge_kernel<false>, parts, span, p.out, heads),
                      "cudaLaunchKernelEx(merge bs8)");
 }
