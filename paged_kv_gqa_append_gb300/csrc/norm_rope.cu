@@ -11,16 +11,21 @@
 // once, at the end.  Without a norm and with P = 32 in the half layout these
 // are exactly kv_append_rope's operations, and its bytes.
 //
-// Work: one warp per token and part -- two parts of 16 q heads and one of the
-// k (and v) heads, so a part is 16 head rows = four 512-byte loads that are
-// all in flight before anything else is read.  A row is spread over 8 lanes
-// of 8 dims (one 16-byte load each): the sum of squares is three shuffles,
-// and the half layout's partner dims sit at the same place of lane +-P/8 when
-// P is a multiple of 8.  Other P go through a row buffer in shared memory;
-// interleaved pairs never leave their lane.
+// Work: a row is spread over 8 lanes of 8 dims, and a warp has four rows at a
+// time (a group).  In the half layout, where the pairs are a multiple of 4, a
+// lane holds four dims and their four partners, two 8-byte loads, so that the
+// rotation needs no exchange and a lane only four table entries; interleaved
+// pairs are neighbours in one 16-byte load.  Other half layouts go through a
+// row buffer in shared memory.  The norm's sum of squares is three shuffles.
+//   many tokens: one warp per token, all of its 12 groups -- 8 of q, 2 of k, 2
+//     of v -- in flight before anything else is read;
+//   few tokens, or no q: one warp per token and part of 4 groups (16 q heads,
+//     or k and v), for the shorter way through.
 //
 // Bound: memory.  A token moves 12 KiB (32 + 8 + 8 rows read and written)
-// and one table row.
+// and one table row.  With 16 contiguous bytes per lane and the partners
+// fetched by shuffles, and three warps per token, 32768 tokens took 131 us: 2450
+// instructions a token, half of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -33,11 +38,12 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 12;       // a multiple of 1, 2 and 3: a CTA holds whole tokens
-constexpr int kGroups = 4;       // 4-row groups of a part
 constexpr int kRow = PKV_HEAD_DIM;
+constexpr int kGroups = 4;       // groups of a part
+constexpr int kAllGroups = 12;   // of a token: 8 of q, 2 of k, 2 of v
+constexpr int kQGroups = 8;
 
-enum Layout { kHalfAligned = 0, kHalfAny = 1, kInterleaved = 2 };
+enum Layout { kHalf4 = 0, kHalfAny = 1, kInterleaved = 2 };
 
 struct NormRopeParams {
   const uint16_t *q, *k, *v;             // token rows of [heads][64] bf16
@@ -66,32 +72,74 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
+// Where a lane's 8 dims of a row are: dims[0 .. 3] at `lo`, dims[4 .. 7] at `hi`.
+// Half layout by fours: chunk j and its partner behind `pairs` dims, then the
+// chunks that are not rotated, two by two.  Else 8 neighbours.
 template <int kLayout>
+__device__ __forceinline__ void places(int j, int pairs, int& lo, int& hi, bool& turned) {
+  if (kLayout == kHalf4) {
+    const int chunks = pairs >> 2;
+    turned = j < chunks;
+    lo = turned ? 4 * j : 4 * (2 * chunks + 2 * (j - chunks));
+    hi = turned ? lo + pairs : lo + 4;
+  } else {
+    turned = true;
+    lo = 8 * j;
+    hi = lo + 4;
+  }
+}
+
+template <int kLayout>
+__device__ __forceinline__ uint4 load_row(const uint16_t* row, int lo, int hi) {
+  if (kLayout != kHalf4) return __ldcs(reinterpret_cast<const uint4*>(row + lo));
+  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + lo)), b = __ldcs(reinterpret_cast<const uint2*>(row + hi));
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+template <int kLayout>
+__device__ __forceinline__ void store_row(uint16_t* row, int lo, int hi, const uint4& v) {
+  if (kLayout != kHalf4) {
+    *reinterpret_cast<uint4*>(row + lo) = v;
+  } else {
+    *reinterpret_cast<uint2*>(row + lo) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(row + hi) = make_uint2(v.z, v.w);
+  }
+}
+
+// kWhole: a warp has a whole token, else a part of it.
+template <int kLayout, bool kWhole, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int kMine = kWhole ? kAllGroups : kGroups;
   __shared__ float rows[kLayout == kHalfAny ? kWarps : 1][4][kRow + 4];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane >> 3, j = lane & 7;  // row of a group, and which 8 dims of it
-  const int parts = p.q_parts + 1;
+  const int sub = lane >> 3, j = lane & 7;  // row of a group, and which dims of it
+  const int parts = kWhole ? 1 : p.q_parts + 1;
   const long long unit = (long long)blockIdx.x * kWarps + warp;
-  const int t = (int)(unit / parts), part = (int)(unit - (long long)t * parts);
+  const int t = (int)(unit / parts);
   if (t >= p.T) return;
-  const bool is_q = part < p.q_parts;
+  // this warp's groups g0 .. g0 + kMine - 1 of the token's 12; q is the first 8
+  const int part = (int)(unit - (long long)t * parts);
+  const int g0 = kWhole ? 0 : part < p.q_parts ? part * kGroups : kQGroups;
+  const auto is_q = [&](int g) { return kWhole ? g < kQGroups : g0 < kQGroups; };
+  const auto is_v = [&](int g) { return !is_q(g) && (kWhole ? g >= kQGroups + 2 : g >= 2); };
+  const auto head_of = [&](int g) {  // of q, or of k or v
+    const int n = g0 + g;
+    return (n < kQGroups ? n : (n - kQGroups) & 1) * 4 + sub;
+  };
+  int lo, hi;
+  bool turned;
+  places<kLayout>(j, p.pairs, lo, hi, turned);
 
-  // all of the part's rows: groups 0..3 are 16 q heads, or 8 k heads and 8 v heads
-  uint4 raw[kGroups];
+  uint4 raw[kMine];
+  const uint16_t* q = p.q + (long long)t * p.q_stride;
+  const uint16_t* k = p.k + (long long)t * p.k_stride;
+  const uint16_t* v = p.v + (long long)t * p.v_stride;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const uint16_t* src;
-    if (is_q)
-      src = p.q + (long long)t * p.q_stride + (part * 16 + g * 4 + sub) * kRow;
-    else if (g < 2)
-      src = p.k + (long long)t * p.k_stride + (g * 4 + sub) * kRow;
-    else
-      src = p.v + (long long)t * p.v_stride + ((g - 2) * 4 + sub) * kRow;
-    if (is_q || g < 2 || p.pool) raw[g] = __ldcs(reinterpret_cast<const uint4*>(src + j * 8));
-  }
+  for (int g = 0; g < kMine; ++g)
+    if (!is_v(g) || p.pool)
+      raw[g] = load_row<kLayout>((is_q(g) ? q : is_v(g) ? v : k) + head_of(g) * kRow, lo, hi);
 
   const int pos = __ldg(p.positions + t);
   bool ok = pos >= 0 && pos < p.max_pos;
@@ -104,65 +152,58 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopePa
       ok = page >= 0 && page < p.num_pages;
     }
   }
-  uint16_t* out = is_q ? p.q_out + ((size_t)t * PKV_NUM_Q_HEADS + part * 16) * kRow
-                       : p.k_out ? p.k_out + (size_t)t * PKV_NUM_KV_HEADS * kRow : nullptr;
+  uint16_t* q_out = p.q_out + (size_t)t * PKV_NUM_Q_HEADS * kRow;
+  uint16_t* k_out = p.k_out ? p.k_out + (size_t)t * PKV_NUM_KV_HEADS * kRow : nullptr;
   if (!ok) {
     if (lane == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
-    if (out) {
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-        if (is_q || g < 2)
-          *reinterpret_cast<uint4*>(out + (g * 4 + sub) * kRow + j * 8) = make_uint4(0, 0, 0, 0);
-    }
+    for (int g = 0; g < kMine; ++g)
+      if (!is_v(g) && (is_q(g) || k_out))
+        store_row<kLayout>((is_q(g) ? q_out : k_out) + head_of(g) * kRow, lo, hi, make_uint4(0, 0, 0, 0));
     return;
   }
 
-  // this lane's table entries: of dims 8 j .. 8 j + 7 (half), or of its 4 pairs
-  constexpr int kTab = kLayout == kInterleaved ? 4 : 8;
+  // table entries: of this lane's four pairs, or (any half layout) of its 8 dims
+  constexpr int kTab = kLayout == kHalfAny ? 8 : 4;
   float c[kTab], s[kTab];
   {
     const float* cr = p.cos + (size_t)pos * p.pairs;
     const float* sr = p.sin + (size_t)pos * p.pairs;
-    if (kLayout == kHalfAligned) {
-      const int at = 8 * j < p.pairs ? 8 * j : 8 * j - p.pairs;
-      if (8 * j < 2 * p.pairs) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(cr + at) + h);
-          const float4 b = __ldg(reinterpret_cast<const float4*>(sr + at) + h);
-          c[4 * h] = a.x; c[4 * h + 1] = a.y; c[4 * h + 2] = a.z; c[4 * h + 3] = a.w;
-          s[4 * h] = b.x; s[4 * h + 1] = b.y; s[4 * h + 2] = b.z; s[4 * h + 3] = b.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) { c[e] = 1.f; s[e] = 0.f; }
-      }
+    if (kLayout == kHalf4) {
+      const float4 a = turned ? __ldg(reinterpret_cast<const float4*>(cr + lo)) : make_float4(1.f, 1.f, 1.f, 1.f);
+      const float4 b = turned ? __ldg(reinterpret_cast<const float4*>(sr + lo)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+      s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
     } else {
 #pragma unroll
       for (int e = 0; e < kTab; ++e) {
         const int i = kLayout == kInterleaved ? 4 * j + e : 8 * j + e - (8 * j + e < p.pairs ? 0 : p.pairs);
-        const bool turned = i < p.pairs;
-        c[e] = turned ? __ldg(cr + i) : 1.f;
-        s[e] = turned ? __ldg(sr + i) : 0.f;
+        const bool in = i < p.pairs;
+        c[e] = in ? __ldg(cr + i) : 1.f;
+        s[e] = in ? __ldg(sr + i) : 0.f;
       }
     }
   }
-  float w[8];
-  const void* weight = is_q ? p.q_weight : p.k_weight;
-  if (weight) {
-    if (p.weight_f32) {
+  const auto load_weights = [&](const void* weight, float (&w)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = __ldg(static_cast<const float*>(weight) + 8 * j + e);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[e] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(weight) + 8 * j + e) << 16);
+    for (int e = 0; e < 8; ++e) {
+      const int d = (e < 4 ? lo : hi - 4) + e;
+      w[e] = p.weight_f32 ? __ldg(static_cast<const float*>(weight) + d)
+                          : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(weight) + d) << 16);
     }
-  }
+  };
+  float w[8];
+  const bool first_is_q = g0 < kQGroups;
+  const void* weight = first_is_q ? p.q_weight : p.k_weight;
+  if (weight) load_weights(weight, w);
 
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if (!is_q && g >= 2) break;  // V rows are copied below
+  for (int g = 0; g < kMine; ++g) {
+    if (is_v(g)) break;  // V rows are copied below
+    if (kWhole && g == kQGroups) {
+      weight = p.k_weight;
+      if (weight) load_weights(weight, w);
+    }
     float x[8], y[8];
     unpack8(raw[g], x);
     if (weight) {
@@ -175,24 +216,19 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopePa
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e]);
     }
-    if (kLayout == kInterleaved) {
+    if (kLayout == kHalf4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // (1, 0) entries leave dims that are not rotated as they are
+        y[e] = turned ? __fsub_rn(__fmul_rn(x[e], c[e]), __fmul_rn(x[e + 4], s[e])) : x[e];
+        y[e + 4] = turned ? __fadd_rn(__fmul_rn(x[e], s[e]), __fmul_rn(x[e + 4], c[e])) : x[e + 4];
+      }
+    } else if (kLayout == kInterleaved) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool turned = 4 * j + e < p.pairs;
+        const bool in = 4 * j + e < p.pairs;
         const float a = x[2 * e], b = x[2 * e + 1];
-        y[2 * e] = turned ? __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e])) : a;
-        y[2 * e + 1] = turned ? __fadd_rn(__fmul_rn(a, s[e]), __fmul_rn(b, c[e])) : b;
-      }
-    } else if (kLayout == kHalfAligned) {
-      const int step = p.pairs >> 3;
-      const bool first = j < step, turned = j < 2 * step;
-      const int src = (lane & ~7) | (first ? j + step : turned ? j - step : j);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float b = __shfl_sync(0xffffffffu, x[e], src);
-        const float xc = __fmul_rn(x[e], c[e]), bs = __fmul_rn(b, s[e]);
-        // first half: a c - b s; second half (x is the pair's b, b its a): a s + b c
-        y[e] = !turned ? x[e] : first ? __fsub_rn(xc, bs) : __fadd_rn(bs, xc);
+        y[2 * e] = in ? __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e])) : a;
+        y[2 * e + 1] = in ? __fadd_rn(__fmul_rn(a, s[e]), __fmul_rn(b, c[e])) : b;
       }
     } else {
       float* buf = rows[warp][sub];
@@ -202,26 +238,48 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopePa
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int d = 8 * j + e;
-        const bool first = d < p.pairs, turned = d < 2 * p.pairs;
-        const float b = buf[first ? d + p.pairs : turned ? d - p.pairs : d];
+        const bool first = d < p.pairs, in = d < 2 * p.pairs;
+        const float b = buf[first ? d + p.pairs : in ? d - p.pairs : d];
         const float xc = __fmul_rn(x[e], c[e]), bs = __fmul_rn(b, s[e]);
-        y[e] = !turned ? x[e] : first ? __fsub_rn(xc, bs) : __fadd_rn(bs, xc);
+        // first half: a c - b s; second half (x is the pair's b, b its a): a s + b c
+        y[e] = !in ? x[e] : first ? __fsub_rn(xc, bs) : __fadd_rn(bs, xc);
       }
       __syncwarp();  // the next group writes the buffer again
     }
-    const uint4 res = pack8(y);
-    if (out) *reinterpret_cast<uint4*>(out + (g * 4 + sub) * kRow + j * 8) = res;
-    if (!is_q && p.pool) raw[g] = res;
+    raw[g] = pack8(y);
+    if (is_q(g))
+      store_row<kLayout>(q_out + head_of(g) * kRow, lo, hi, raw[g]);
+    else if (k_out)
+      store_row<kLayout>(k_out + head_of(g) * kRow, lo, hi, raw[g]);
   }
-  if (!is_q && p.pool) {
+  if (p.pool && (kWhole || !first_is_q)) {
     const int slot = pos % PKV_PAGE_TOKENS;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int kv = g >> 1, head = (g & 1) * 4 + sub;
-      uint16_t* dst = p.pool + ((((size_t)page * 2 + kv) * PKV_NUM_KV_HEADS + head) * PKV_PAGE_TOKENS + slot) * kRow;
-      *reinterpret_cast<uint4*>(dst + j * 8) = raw[g];
-    }
+    for (int g = 0; g < kMine; ++g)
+      if (!is_q(g))
+        store_row<kLayout>(p.pool + ((((size_t)page * 2 + (is_v(g) ? 1 : 0)) * PKV_NUM_KV_HEADS + head_of(g)) *
+                                         PKV_PAGE_TOKENS + slot) * kRow,
+                           lo, hi, raw[g]);
   }
+}
+
+// Where one warp per token has enough warps to fill the GPU (about 16 on each
+// SM): 32768 tokens take 65 us whole and 80 us in parts, 257 tokens are 3.2 us
+// either way and 1 token 0.4 us less in parts.
+constexpr int kWholeTokensPerSm = 16;
+
+template <int kLayout>
+cudaError_t launch_norm_rope(const NormRopeParams& p, int sms, cudaLaunchConfig_t& cfg) {
+  if (p.q_parts && p.T >= sms * kWholeTokensPerSm) {
+    constexpr int kWarps = 4;
+    cfg.gridDim = dim3((unsigned)((p.T + kWarps - 1) / kWarps));
+    cfg.blockDim = dim3(kWarps * 32);
+    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<kLayout, true, kWarps>, p);
+  }
+  constexpr int kWarps = 6;
+  cfg.gridDim = dim3((unsigned)(((long long)p.T * (p.q_parts + 1) + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kWarps * 32);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<kLayout, false, kWarps>, p);
 }
 
 }  // namespace
@@ -296,20 +354,18 @@ extern "C" int kv_append_norm_rope(const void* q, long long q_stride, const void
   p.num_pages = num_pages;
   p.q_parts = q ? 2 : 0;
 
-  const long long units = (long long)T * (p.q_parts + 1);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // lane-aligned partners and 16-byte table loads, where the pairs and the tables allow them
-  const bool by_lane = rope_pairs % 8 == 0 && aligned16(rope_cos) && aligned16(rope_sin);
-  cudaError_t e = interleaved ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<kInterleaved>, p)
-                  : by_lane   ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<kHalfAligned>, p)
-                              : cudaLaunchKernelEx(&cfg, norm_rope_kernel<kHalfAny>, p);
+  // 16-byte table loads by fours, where the pairs and the tables allow them
+  const bool by_fours = rope_pairs % 4 == 0 && aligned16(rope_cos) && aligned16(rope_sin);
+  const int sms = sm_count(dev);
+  const cudaError_t e = interleaved ? launch_norm_rope<kInterleaved>(p, sms, cfg)
+                        : by_fours  ? launch_norm_rope<kHalf4>(p, sms, cfg)
+                                    : launch_norm_rope<kHalfAny>(p, sms, cfg);
   return cuda_status(e, "cudaLaunchKernelEx(norm_rope)");
 }
