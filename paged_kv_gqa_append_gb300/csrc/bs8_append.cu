@@ -5,21 +5,24 @@
 // A block's scale covers every token in it, so the tokens that go to the same
 // page are handled together: the unit of work is a run -- the new tokens of
 // one sequence that fall into one page -- and its K or V rows of one head,
-// 16 x 64 values in the registers of one warp (a row over 8 lanes of 8 dims,
-// four rows per step).  A run that starts at slot 0 sets the block's scale to
-// amax / top; a later one keeps the larger of that and the scale found, and
-// when the scale grows the codes held by the earlier slots are decoded under
-// the old scale and encoded under the new one.  The earlier slots are read
-// only then.
+// 16 x 64 values in the registers of one warp (a row over 8 lanes, each with
+// four dims and their four rotation partners; four rows per step).  A run that
+// starts at slot 0 sets the block's scale to amax / top; a later one keeps the
+// larger of that and the scale found, and when the scale grows the codes held by
+// the earlier slots are decoded under the old scale and encoded under the new
+// one.  The earlier slots are read only then.
 //
 // A CTA of 16 warps (8 heads x {K, V}) looks at `chunk` consecutive tokens
 // and handles the runs that begin among them: one token per CTA for decode
 // steps, 16 per CTA when sequences bring 16 tokens or more on average, where
-// most tokens begin no run.  The chunk's q heads are rotated by all warps.
+// most tokens begin no run.  The chunk's q heads are rotated by another CTA, so
+// that neither waits for the other.
 //
-// Bound: memory, 3 KiB per token for K and V, and 8 KiB for q.  A step of few
-// tokens is latency: the sequence search (one round of a 32-way search for up
-// to 1023 sequences), the table entry, the rows, the old scale.
+// Bound: memory, 3 KiB per token for K and V, and 8 KiB for q.  Codes without a
+// division per value (bs8.cuh) and rotations without shuffles took 14400 tokens
+// of eight prompts from 65 us to 35 us.  A step of few tokens is latency: the
+// sequence search (one round of a 32-way search for up to 1023 sequences), the
+// table entry, the rows, the old scale.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -28,7 +31,6 @@
 #include "internal.h"
 #include "pkv.h"
 #include "ptx.cuh"
-#include "rope.cuh"
 
 namespace pkv {
 namespace {
@@ -69,12 +71,12 @@ __device__ int find_sequence(const int32_t* __restrict__ cu, int n, int t) {
 
 // A token's place: its sequence and position; ok only if both can be used.
 struct Place {
-  int seq, pos, end;  // end: the row behind the sequence's last new token
-  bool live, ok;      // live: the token belongs to a sequence
+  int seq, pos, end;      // end: the row behind the sequence's last new token
+  bool live, ok, first;   // live: the token belongs to a sequence; first: of its new ones
 };
 
 __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
-  Place a{-1, 0, t + 1, false, false};
+  Place a{-1, 0, t + 1, false, false, false};
   a.seq = find_sequence(p.cu_new, p.num_seqs, t);
   if (a.seq >= p.num_seqs) {  // rows behind the last sequence are left alone
     a.end = p.T;
@@ -90,7 +92,38 @@ __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
   if (len < fresh || len > (long long)p.max_blocks * PKV_PAGE_TOKENS || (p.cos && len > p.max_pos)) return a;
   a.pos = len - fresh + (t - lo);
   a.ok = true;
+  a.first = t == lo;
   return a;
+}
+
+// Four dims and their partners rotated in place, in kv_append_rope's order of
+// operations: x[0 .. 3] with x[4 .. 7].
+__device__ __forceinline__ void rotate8(float (&x)[8], const float4& c4, const float4& s4) {
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = x[e], b = x[e + 4];
+    x[e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+    x[e + 4] = __fadd_rn(__fmul_rn(a, s[e]), __fmul_rn(b, c[e]));
+  }
+}
+
+// dims 4 j .. 4 j + 3 and 32 + 4 j .. of a row
+__device__ __forceinline__ uint4 load_halves(const uint16_t* row, int j) {
+  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + 4 * j));
+  const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + 32 + 4 * j));
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = bf16lo_to_f32(w[e]);
+    x[2 * e + 1] = bf16hi_to_f32(w[e]);
+  }
+}
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 // K (kv = 0) or V rows of one head of a run: slots [slot, slot + n) of the page.
@@ -110,35 +143,20 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * i + sub - slot;  // row of the run
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (r >= 0 && r < n)
-      raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (long long)(t + r) * stride + head * kRow + 8 * j));
+    if (r >= 0 && r < n) raw[i] = load_halves(src + (long long)(t + r) * stride + head * kRow, j);
   }
   float old = 0.f;
   if (slot && lane == 0) old = *scale;
-  old = __shfl_sync(0xffffffffu, old, 0);
   if (kv == 0 && p.cos) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * i + sub - slot;
-      const uint32_t mine[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      uint32_t res[4];
-      alignas(16) float c[8], s[8];
-      const size_t row = (size_t)(r >= 0 && r < n ? pos + r : pos) * PKV_ROPE_PAIRS + 8 * (j & 3);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<float4*>(c + 4 * h) = __ldg(reinterpret_cast<const float4*>(p.cos + row) + h);
-        *reinterpret_cast<float4*>(s + 4 * h) = __ldg(reinterpret_cast<const float4*>(p.sin + row) + h);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine[e], 4);
-        const uint32_t a = j < 4 ? mine[e] : other, b = j < 4 ? other : mine[e];
-        uint16_t lo0, lo1, hi0, hi1;
-        rope_pair((uint16_t)a, (uint16_t)b, c[2 * e], s[2 * e], lo0, lo1);
-        rope_pair((uint16_t)(a >> 16), (uint16_t)(b >> 16), c[2 * e + 1], s[2 * e + 1], hi0, hi1);
-        res[e] = j < 4 ? (uint32_t)lo0 | ((uint32_t)hi0 << 16) : (uint32_t)lo1 | ((uint32_t)hi1 << 16);
-      }
-      raw[i] = make_uint4(res[0], res[1], res[2], res[3]);
+      if (r < 0 || r >= n) continue;
+      const size_t row = (size_t)(pos + r) * PKV_ROPE_PAIRS + 4 * j;
+      float x[8];
+      widen8(raw[i], x);
+      rotate8(x, __ldg(reinterpret_cast<const float4*>(p.cos + row)), __ldg(reinterpret_cast<const float4*>(p.sin + row)));
+      raw[i] = narrow8(x);
     }
   }
   // largest |x| of the run: bf16 magnitudes order as their bits
@@ -150,40 +168,38 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
     for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
   }
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  old = __shfl_sync(0xffffffffu, old, 0);
   const float fresh = __fdiv_rn(amax, kE4m3 ? 448.f : 127.f);
   const bool grown = slot > 0 && fresh > old;
   const float now = slot == 0 || grown ? fresh : old;
   if (lane == 0 && (slot == 0 || grown)) *scale = now;
+  const Bs8Inverse inv = bs8_inverse(now);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * i + sub;
-    uint2* at = reinterpret_cast<uint2*>(block + r * kRow + 8 * j);
+    uint32_t* lo = reinterpret_cast<uint32_t*>(block + r * kRow + 4 * j);
+    uint32_t* hi = lo + 32 / 4;
     float x[8];
     if (r >= slot && r < slot + n) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = bf16lo_to_f32(w[e]);
-        x[2 * e + 1] = bf16hi_to_f32(w[e]);
-      }
-      *at = bs8_encode8<kE4m3>(x, now);
+      widen8(raw[i], x);
+      const uint2 codes = bs8_encode8<kE4m3>(x, now, inv);
+      *lo = codes.x;
+      *hi = codes.y;
     } else if (r < slot && grown) {
-      bs8_decode8<kE4m3>(*at, x);
+      bs8_decode8<kE4m3>(make_uint2(*lo, *hi), x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], old);
-      *at = bs8_encode8<kE4m3>(x, now);
+      const uint2 codes = bs8_encode8_exact<kE4m3>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], now);
+      *lo = codes.x;
+      *hi = codes.y;
     }
   }
 }
 
+// K and V of the runs that begin in the CTA's chunk of tokens.
 template <bool kE4m3>
-__global__ void __launch_bounds__(kWarps * 32) bs8_append_kernel(const Bs8AppendParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-
-  // K and V of the runs that begin in the chunk
+__device__ __forceinline__ void append_chunk(const Bs8AppendParams& p, int t0, int t1) {
+  const int warp = threadIdx.x >> 5;
   for (int t = t0; t < t1;) {
     const Place a = place_of(p, t);
     if (!a.live) break;
@@ -194,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32) bs8_append_kernel(const Bs8Append
     }
     const int slot = a.pos % PKV_PAGE_TOKENS;
     const int n = min(PKV_PAGE_TOKENS - slot, a.end - t);
-    if (t == __ldg(p.cu_new + a.seq) || slot == 0) {
+    if (a.first || slot == 0) {
       const int page = __ldg(p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS);
       if (page >= 0 && page < p.num_pages)
         append_run<kE4m3>(p, t, a.pos, n, page, warp >> 3, warp & 7);
@@ -203,12 +219,22 @@ __global__ void __launch_bounds__(kWarps * 32) bs8_append_kernel(const Bs8Append
     }
     t += n;
   }
+}
 
-  // q of the chunk's tokens, two heads per warp and step, 16 lanes of 4 dims
-  // each: one token by all warps, or one token by each warp
-  if (p.q_in == nullptr) return;
-  const int t = p.chunk == 1 ? t0 : t0 + warp;
-  if (t >= t1) return;
+// q of the chunk's tokens, four heads per warp and step: one token by 8 warps,
+// or one token by each warp, whose rows are loaded before its place is known.
+__device__ __forceinline__ void rotate_chunk(const Bs8AppendParams& p, int t0, int t1) {
+  static_assert(kChunkMany == kWarps && kWarps >= PKV_NUM_Q_HEADS / 4, "tokens and q heads over the warps");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
+  const bool many = p.chunk > 1;
+  const int t = many ? t0 + warp : t0;
+  if (t >= t1 || (!many && warp >= PKV_NUM_Q_HEADS / 4)) return;
+  constexpr int kSteps = PKV_NUM_Q_HEADS / 4;
+  uint4 raw[kSteps];
+  const uint16_t* src = p.q_in + (long long)t * p.q_stride;
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u)
+    if (many || u == 0) raw[u] = load_halves(src + ((many ? 4 * u : 4 * warp) + sub) * kRow, j);
   const Place a = place_of(p, t);
   if (!a.live) return;
   bool ok = a.ok;
@@ -216,38 +242,37 @@ __global__ void __launch_bounds__(kWarps * 32) bs8_append_kernel(const Bs8Append
     const int page = __ldg(p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS);
     ok = page >= 0 && page < p.num_pages;
   }
-  const int l16 = lane & 15;
-  const bool first = l16 < 8;  // dims 0..31: the pairs' first halves
   float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
   if (ok) {
-    const size_t row = (size_t)a.pos * PKV_ROPE_PAIRS + 4 * (l16 & 7);
+    const size_t row = (size_t)a.pos * PKV_ROPE_PAIRS + 4 * j;
     c = __ldg(reinterpret_cast<const float4*>(p.cos + row));
     s = __ldg(reinterpret_cast<const float4*>(p.sin + row));
   }
-  const int u0 = p.chunk == 1 ? warp : 0, u1 = p.chunk == 1 ? warp + 1 : kWarps;
-  static_assert(kWarps * 2 == PKV_NUM_Q_HEADS && kChunkMany == kWarps, "q heads and tokens over the warps");
-#pragma unroll 4
-  for (int u = u0; u < u1; ++u) {
-    const int head = 2 * u + (lane >> 4);
-    uint2 res = make_uint2(0, 0);
-    if (ok) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p.q_in + (long long)t * p.q_stride + head * kRow + 4 * l16);
-      const uint32_t mine[2] = {x.x, x.y};
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-      uint32_t w[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine[e], 8);
-        const uint32_t x0 = first ? mine[e] : other, x1 = first ? other : mine[e];
-        uint16_t lo0, lo1, hi0, hi1;
-        rope_pair((uint16_t)x0, (uint16_t)x1, cc[2 * e], ss[2 * e], lo0, lo1);
-        rope_pair((uint16_t)(x0 >> 16), (uint16_t)(x1 >> 16), cc[2 * e + 1], ss[2 * e + 1], hi0, hi1);
-        w[e] = first ? (uint32_t)lo0 | ((uint32_t)hi0 << 16) : (uint32_t)lo1 | ((uint32_t)hi1 << 16);
-      }
-      res = make_uint2(w[0], w[1]);
+  for (int u = 0; u < kSteps; ++u) {
+    if (!many && u) break;
+    uint16_t* dst = p.q_out + ((size_t)t * PKV_NUM_Q_HEADS + (many ? 4 * u : 4 * warp) + sub) * kRow;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (ok) {
+      float x[8];
+      widen8(raw[u], x);
+      rotate8(x, c, s);
+      res = narrow8(x);
     }
-    *reinterpret_cast<uint2*>(p.q_out + ((size_t)t * PKV_NUM_Q_HEADS + head) * kRow + 4 * l16) = res;
+    *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(res.x, res.y);
+    *reinterpret_cast<uint2*>(dst + 32 + 4 * j) = make_uint2(res.z, res.w);
   }
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kWarps * 32, 2) bs8_append_kernel(const Bs8AppendParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  if (blockIdx.y == 0)
+    append_chunk<kE4m3>(p, t0, t1);
+  else
+    rotate_chunk(p, t0, t1);
 }
 
 // out[i] = the page page_ids[i] as bf16: code * scale, rounded once.  One CTA
@@ -360,7 +385,7 @@ extern "C" int kv_append_rope_bs8(const void* k, long long k_stride, const void*
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)T + p.chunk - 1) / p.chunk));
+  cfg.gridDim = dim3((unsigned)(((long long)T + p.chunk - 1) / p.chunk), q_in ? 2 : 1);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;

@@ -23,9 +23,10 @@
 //     or k and v), for the shorter way through.
 //
 // Bound: memory.  A token moves 12 KiB (32 + 8 + 8 rows read and written)
-// and one table row.  With 16 contiguous bytes per lane and the partners
-// fetched by shuffles, and three warps per token, 32768 tokens took 131 us: 2450
-// instructions a token, half of the issue slots.
+// and one table row.  24 warps per SM (80 registers) keep 144 KB in flight;
+// with 16 warps 32768 tokens take 87 us, not 74.  With 16 contiguous bytes per
+// lane and the partners fetched by shuffles, and three warps per token, they
+// took 131 us: 2450 instructions a token, half of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -108,7 +109,7 @@ __device__ __forceinline__ void store_row(uint16_t* row, int lo, int hi, const u
 
 // kWhole: a warp has a whole token, else a part of it.
 template <int kLayout, bool kWhole, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_rope_kernel(const NormRopeParams p) {
   constexpr int kMine = kWhole ? kAllGroups : kGroups;
   __shared__ float rows[kLayout == kHalfAny ? kWarps : 1][4][kRow + 4];
   pdl_wait();
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopePa
       for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float r = __frsqrt_rn(fmaf(sum, 1.f / kRow, p.eps));
+      const float r = rsqrtf(fmaf(sum, 1.f / kRow, p.eps));
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e]);
     }
@@ -264,8 +265,9 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopePa
 }
 
 // Where one warp per token has enough warps to fill the GPU (about 16 on each
-// SM): 32768 tokens take 65 us whole and 80 us in parts, 257 tokens are 3.2 us
-// either way and 1 token 0.4 us less in parts.
+// SM): 32768 tokens take 74 us whole and 100 us in parts, 2432 tokens 7.6 and
+// 7.8 us; 257 tokens take 4.0 us whole and 3.1 us in parts, one token 3.6 and
+// 2.7 us.
 constexpr int kWholeTokensPerSm = 16;
 
 template <int kLayout>
