@@ -373,9 +373,10 @@ def _device_error(t, dev):
     _need(t, "d_err", _I32, dev)
 
 
-def _call(dev, stream, where, *args):
-    """The C call `where` with the stream appended: the given one, or the
-    current one of the tensors' device (made current for the call)."""
+def _call(dev, stream, where, args):
+    """The C call `where` of the tuple `args` with the stream appended: the
+    given one, or the current one of the tensors' device (made current for the
+    call)."""
     fn = getattr(_LIB or _L(), where)
     if stream is not None:
         st = fn(*args, stream.cuda_stream)
@@ -422,14 +423,18 @@ def _norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, r
         q_ptr, q_stride, _ = _rows(q, "q", NUM_Q_HEADS, dev, T)
     elif q_weight is not None:
         raise ValueError("q_weight needs q")
-    qo, ko = _opt(q_out, "q_out", _BF16, dev, T * _Q_ROW_ELEMS), _opt(k_out, "k_out", _BF16, dev, T * _KV_ROW_ELEMS)
+    qo = None if q_out is None else _vec(q_out, "q_out", _BF16, dev, T * _Q_ROW_ELEMS)
+    ko = None if k_out is None else _vec(k_out, "k_out", _BF16, dev, T * _KV_ROW_ELEMS)
     pos = _vec(positions, "positions", _I32, dev, T)
     if kv_pool is not None:
-        _need(kv_pool, "kv_pool", _BF16, dev, _PAGE)
-        pool, pages = kv_pool.data_ptr(), kv_pool.numel() // _PAGE_ELEMS
+        page = kv_pool.shape
+        if page[1:] != _PAGE:
+            raise ValueError(f"kv_pool must be [num_pages, {', '.join(map(str, _PAGE))}], got {tuple(page)}")
+        pages = page[0]
+        pool = _vec(kv_pool, "kv_pool", _BF16, dev, pages * _PAGE_ELEMS)
         v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
         bt, S, row = _block_rows(block_tables, dev)
-        seq = _opt(token_seq, "token_seq", _I32, dev, T)
+        seq = None if token_seq is None else _vec(token_seq, "token_seq", _I32, dev, T)
     shape = rope_cos.shape
     if len(shape) != 2 or not 1 <= shape[1] <= ROPE_PAIRS or rope_sin.shape != shape:
         raise ValueError("rope_cos and rope_sin must be [max_pos, pairs] with 1 to 32 pairs")
@@ -442,9 +447,9 @@ def _norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, r
     err = _device_error(d_err, dev)
     if T == 0:
         return
-    _call(dev, stream, "kv_append_norm_rope", q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, qw, kw,
-          1 if q_f32 or k_f32 else 0, eps, cos, sin, shape[0], shape[1], 1 if interleaved else 0, pos, seq, T,
-          bt, S, row, row if max_blocks is None else max_blocks, pool, pages, qo, ko, err)
+    _call(dev, stream, "kv_append_norm_rope", (q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, qw, kw,
+          1 if q_f32 or k_f32 else 0, float(eps), cos, sin, shape[0], shape[1], 1 if interleaved else 0, pos, seq, T,
+          bt, S, row, row if max_blocks is None else max_blocks, pool, pages, qo, ko, err))
 
 
 def kv_append_norm_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_sin, token_seq=None,
@@ -460,7 +465,8 @@ def kv_append_norm_rope(k, v, positions, block_tables, kv_pool, rope_cos, rope_s
     rope_cos/sin [max_pos, pairs] fp32 (rope_tables_scaled_device).  Weights
     [64] bf16 or fp32; None: not normalised.  Tokens and pages as for
     kv_append_rope; k_out [T, 8, 64], if given, gets the K rows as well."""
-    _on_device(kv_pool, "kv_pool")
+    if kv_pool is None:
+        raise ValueError("kv_pool must be given")
     _norm_rope(q_in, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, rope_sin, q_out, k_out,
                q_weight, k_weight, eps, interleaved, d_err, max_blocks, stream)
 
@@ -820,9 +826,9 @@ def kv_append_rope_bs8(k, v, cu_new, seq_lens, block_tables, kv_pool, kv_scales,
     err = _device_error(d_err, dev)
     if T == 0 or S == 0:
         return
-    _call(dev, stream, "kv_append_rope_bs8", k_ptr, k_stride, v_ptr, v_stride, cu, lens, T, bt, S, row,
+    _call(dev, stream, "kv_append_rope_bs8", (k_ptr, k_stride, v_ptr, v_stride, cu, lens, T, bt, S, row,
           row if max_blocks is None else max_blocks, pool, scales, pages, code, cos, sin, max_pos, q_ptr,
-          q_stride, q_dst, err)
+          q_stride, q_dst, err))
 
 
 def kv_read_bs8(kv_pool, kv_scales, page_ids, out=None, d_err=None, stream=None):
@@ -837,7 +843,7 @@ def kv_read_bs8(kv_pool, kv_scales, page_ids, out=None, d_err=None, stream=None)
     dst = _vec(out, "out", _BF16, dev, n * _PAGE_ELEMS)
     err = _device_error(d_err, dev)
     if n:
-        _call(dev, stream, "kv_read_bs8", pool, scales, pages, code, ids, n, dst, err)
+        _call(dev, stream, "kv_read_bs8", (pool, scales, pages, code, ids, n, dst, err))
     return out
 
 
@@ -876,9 +882,9 @@ def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, sca
     if workspace is None:
         workspace = alloc_bs8_workspace(S, dev, stream)
     size = workspace.numel()
-    _call(dev, stream, "paged_gqa_decode_bs8", q_ptr, pool, scales, pages, code, bt, row, mb, lens, S,
-          PAGE_TOKENS * mb if max_seq_len is None else max_seq_len, dst, scale,
-          _vec(workspace, "workspace", torch.uint8, dev, size), size, err)
+    _call(dev, stream, "paged_gqa_decode_bs8", (q_ptr, pool, scales, pages, code, bt, row, mb, lens, S,
+          PAGE_TOKENS * mb if max_seq_len is None else int(max_seq_len), dst, float(scale),
+          _vec(workspace, "workspace", torch.uint8, dev, size), size, err))
 
 
 def paged_gqa_decode_append(q, k_new, v_new, kv_pool, block_tables, seq_lens, out, rope_cos,
@@ -1144,9 +1150,9 @@ def process_logits(logits, out=None, ids=None, history=None, history_lens=None, 
         mask = _vec(allow_mask, "allow_mask", _I32, dev, rows * mask_stride)
     if rows == 0:
         return ids
-    _call(dev, stream, "pkv_process_logits", logits.data_ptr(), dtype, rows, vocab,
+    _call(dev, stream, "pkv_process_logits", (logits.data_ptr(), dtype, rows, vocab,
           stride[0] if rows > 1 else vocab, dst, out_stride, id_ptr, hist, H, h_lens, p_lens, rep, pres, freq,
-          b_ids, b_vals, B, mask, mask_stride)
+          b_ids, b_vals, B, mask, mask_stride))
     return ids
 
 

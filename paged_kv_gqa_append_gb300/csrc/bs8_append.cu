@@ -268,8 +268,10 @@ template <bool kE4m3>
 __global__ void __launch_bounds__(kWarps * 32, 2) bs8_append_kernel(const Bs8AppendParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  if (blockIdx.y == 0)
+  // with q, the two kinds of CTA take turns, so that both kinds are on every SM
+  const int kinds = p.q_in ? 2 : 1;
+  const int t0 = blockIdx.x / kinds * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  if (blockIdx.x % kinds == 0)
     append_chunk<kE4m3>(p, t0, t1);
   else
     rotate_chunk(p, t0, t1);
@@ -351,7 +353,7 @@ extern "C" int kv_append_rope_bs8(const void* k, long long k_stride, const void*
        reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(kv_scales) |
        reinterpret_cast<uintptr_t>(d_err)) & 3u)
     return PKV_ERR_MISALIGNED;
-  if (T > (1 << 30) || num_seqs > (1 << 30) || max_blocks > (1 << 26))
+  if (T > (1 << 29) || num_seqs > (1 << 30) || max_blocks > (1 << 26))
     return PKV_ERR_UNSUPPORTED_SHAPE;
   int dev = 0;
   const int rc = bind_stream_device(stream, &dev);
@@ -385,7 +387,7 @@ extern "C" int kv_append_rope_bs8(const void* k, long long k_stride, const void*
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)T + p.chunk - 1) / p.chunk), q_in ? 2 : 1);
+  cfg.gridDim = dim3((unsigned)(((long long)T + p.chunk - 1) / p.chunk) * (q_in ? 2 : 1));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;

@@ -187,15 +187,17 @@ struct Head {  // a consumer's state for one segment
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = 0.f;
     }
-    float amax = 0.f;
+    uint32_t bits = 0;  // of the largest finite |q|: magnitudes order as their bits
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-    // 2^up brings the largest |q| into [2^14, 2^15); none for 0, infinities and
-    // (through fmaxf, which drops them) rows of NaN alone.  up lies in
-    // [-113, 141]: two factors keep each a normal number.
-    int up = 0;
-    if (bits != 0 && bits < 0x7F800000u) up = 14 - max((int)(bits >> 23) - 127, -127);
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+      bits = max(bits, b < 0x7F800000u ? b : 0u);
+    }
+    bits = __reduce_max_sync(0xffffffffu, bits);
+    // 2^up brings it into [2^14, 2^15), unless it is 0; infinities and NaN stay
+    // what they are, in their own head.  up lies in [-113, 141]: two factors
+    // keep each a normal number.
+    const int up = bits ? 14 - ((int)(bits >> 23) - 127) : 0;
     const float f0 = __uint_as_float((uint32_t)(127 + up / 2) << 23);
     const float f1 = __uint_as_float((uint32_t)(127 + up - up / 2) << 23);
     const float d0 = __uint_as_float((uint32_t)(127 - up / 2) << 23);

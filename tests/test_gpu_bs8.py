@@ -317,6 +317,43 @@ def test_decode_values(lib, cuda_device, kind, what):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_infinite_and_nan_queries_stay_in_their_head(lib, cuda_device, kind):
+    lens = [150, 20]
+    codes, scales = random_pages(55, 14, kind)
+    bt = tables_for(56, lens, 14)
+    q = rows(57, 2, 32, 64, scale=1e-3)
+    ref = O8.attend(q, codes, scales, bt, lens, 0.125, kind)
+    bad = q.copy()
+    bad[0, 5, 3], bad[1, 30, 63] = 0x7F80, 0x7FC0          # inf, NaN
+    out, code = decode(lib, cuda_device, kind, bad, codes, scales, bt, lens)
+    assert code == 0
+    keep = np.ones((2, 32), bool)
+    keep[0, 5] = keep[1, 30] = False
+    assert torch.isnan(out[1, 30].float()).all()
+    out[0, 5], out[1, 30] = 0, 0
+    close(out * torch.from_numpy(keep).to(out)[..., None], *[r * keep[..., None] for r in ref], lens)
+
+
+def test_pages_behind_4_gib(lib, cuda_device, tables):
+    """Offsets into a pool pass 32 bits: the last pages of 4.5 GB of codes."""
+    dev, pages, n = cuda_device, 275000, 100
+    pool, sc = lib.new_bs8_pool(pages, dev)
+    bt = np.arange(pages - 7, pages, dtype=np.int32)[None, ::-1].copy()
+    k, v, q = rows(58, n, 8, 64), rows(59, n, 8, 64), rows(60, 1, 32, 64)
+    small = O8.append(np.zeros((7, 2, 8, 16, 64), np.uint8), np.zeros((7, 2, 8), np.float32), k, v, [0, n], [n],
+                      np.arange(6, -1, -1, dtype=np.int32)[None], "int8")
+    btd, lens = to_dev_i32(bt, dev), to_dev_i32([n], dev)
+    lib.kv_append_rope_bs8(to_dev_bf16(k, dev), to_dev_bf16(v, dev), to_dev_i32([0, n], dev), lens, btd, pool, sc)
+    assert np.array_equal(pool_bytes(pool[-7:]), small[0]) and np.array_equal(sc[-7:].cpu().numpy(), small[1])
+    assert int((sc != 0).sum()) == int((small[1] != 0).sum())
+    out = torch.empty(1, 32, 64, dtype=torch.bfloat16, device=dev)
+    lib.paged_gqa_decode_bs8(to_dev_bf16(q, dev), pool, sc, btd, lens, out, 0.125)
+    close(out, *O8.attend(q, small[0], small[1], np.arange(6, -1, -1, dtype=np.int32)[None], [n], 0.125, "int8"), [n])
+    wide = lib.kv_read_bs8(pool, sc, to_dev_i32([pages - 1], dev))
+    assert np.array_equal(bits(wide)[0], OB.from_f32_rne(O8.values(small[0][6], small[1][6], "int8").astype(np.float32)))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_decode_refuses_bad_sequences_alone(lib, cuda_device, kind):
     lens = [40, 300, -1, 7000, 2 ** 31 - 1, 500, 33, 20]
     codes, scales = random_pages(39, 60, kind)

@@ -60,7 +60,8 @@ def run(lib, dev, c, names, out=True, **kw):
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
 @pytest.mark.parametrize("rows,vocab,hist,bias", [(1, 1, 1, 1), (3, 7, 5, 2), (2, 31, 40, 0), (5, 257, 64, 9),
-                                                  (4, 1000, 3, 700), (33, 4099, 129, 33), (2, 128256, 2048, 300)])
+                                                  (4, 1000, 3, 700), (33, 4099, 129, 33), (2, 128256, 2048, 300),
+                                                  (61, 4099, 129, 33), (150, 1003, 2500, 7)])
 def test_everything(lib, cuda_device, dtype, rows, vocab, hist, bias):
     c = case(rows + vocab, rows, vocab, hist, bias, dtype)
     run(lib, cuda_device, c, NAMES)
@@ -84,6 +85,15 @@ def test_more_changed_tokens_than_a_pass_holds(lib, cuda_device, dtype, vocab, h
     c["history_lens"][:] = [hist, hist // 2, hist]
     run(lib, cuda_device, c, NAMES)
     run(lib, cuda_device, c, NAMES, out=None)
+    many = {n: np.concatenate([a] * 17) for n, a in c.items() if n not in ("x", "wide")}     # CTAs of the other shape
+    many["x"], many["wide"] = c["x"].repeat(17, 1), np.concatenate([c["wide"]] * 17)
+    many["repetition"][3:] += 0.25
+    dev = cuda_device
+    got = lib.process_logits(many["x"].to(dev), **{("allow_mask" if n == "mask" else n): torch.from_numpy(many[n]).to(dev)
+                                                    for n in NAMES if n in many}).cpu().numpy()
+    sub = [0, 1, 2, 30, 31, 50]
+    _, want = OL.process(many["wide"][sub], **{n: many[n][sub] for n in NAMES if n in many})
+    assert np.array_equal(got[sub], want)
 
 
 def test_large_vocabulary(lib, cuda_device):
@@ -115,7 +125,8 @@ def test_strided_unaligned_rows_and_in_place(lib, cuda_device):
     assert np.array_equal(ids.cpu().numpy(), want_ids) and np.array_equal(out[:, 2:].cpu().numpy(), want, equal_nan=True)
 
 
-def test_rows_with_nothing_left(lib, cuda_device):
+@pytest.mark.parametrize("copies", [1, 12])
+def test_rows_with_nothing_left(lib, cuda_device, copies):
     dev = cuda_device
     x = torch.randn(4, 100, device=dev)
     x[1] = float("nan")
@@ -124,9 +135,23 @@ def test_rows_with_nothing_left(lib, cuda_device):
     mask[0] = 0
     mask[3] = 0
     mask[3, 3] = 1 << 30                                   # a bit behind the vocabulary: token 126
+    x, mask = x.repeat(copies, 1), mask.repeat(copies, 1)
     out = torch.empty_like(x)
     ids = lib.process_logits(x, out=out, allow_mask=mask)
-    assert ids.tolist() == [-1, -1, 0, -1]
+    assert ids.tolist() == [-1, -1, 0, -1] * copies
+    # everything is -inf but for what the history makes of it: a penalty cannot raise it, a bias can
+    low = torch.full((4 * copies, 100), float("-inf"), device=dev)
+    hist = torch.full((4 * copies, 2), 7, dtype=torch.int32, device=dev)
+    lens = torch.full((4 * copies,), 2, dtype=torch.int32, device=dev)
+    bias = torch.full((4 * copies, 1), 40, dtype=torch.int32, device=dev)
+    up = torch.full((4 * copies, 1), float("inf"), device=dev)
+    first = lib.process_logits(low, history=hist, history_lens=lens)
+    assert first.tolist() == [0] * (4 * copies)
+    first = lib.process_logits(low, bias_ids=bias, bias_values=up)                 # -inf + inf is NaN: never chosen
+    assert first.tolist() == [0] * (4 * copies)
+    only = torch.zeros((4 * copies, 4), dtype=torch.int32, device=dev)
+    only[:, 0] = 1 << 7
+    assert lib.process_logits(low, history=hist, history_lens=lens, allow_mask=only).tolist() == [7] * (4 * copies)
     assert torch.isinf(out[0]).all() and torch.isnan(out[1]).all()
 
 

@@ -163,6 +163,35 @@ def test_bad_tokens_are_skipped(lib, cuda_device):
     assert (qo[1:3] == 0).all() and (qo[3:].float().abs().sum((1, 2)) > 0).all()
 
 
+def test_many_tokens_equal_few(lib, cuda_device):
+    """The form for many tokens (one warp per token) gives the bits of the one for few, in every layout, and
+    reaches pages behind 4 GiB of the pool."""
+    dev, T = cuda_device, 5000
+    g = torch.Generator(dev).manual_seed(0)
+    qkv = torch.randn(T, 48, 64, generator=g, device=dev).bfloat16()
+    w = torch.randn(64, generator=g, device=dev)
+    pool = torch.zeros((140000, 2, 8, 16, 64), dtype=torch.bfloat16, device=dev)     # 4.6 GB
+    bt = torch.arange(140000 - 313, 140000, dtype=torch.int32, device=dev)[None]
+    pos, seq = torch.arange(T, dtype=torch.int32, device=dev), torch.zeros(T, dtype=torch.int32, device=dev)
+    for pairs, inter in ((32, False), (20, False), (9, False), (32, True), (13, True)):
+        cos, sin, _ = tables(lib, dev, pairs, T)
+        got = []
+        for step in (T, 500):
+            pool[-313:] = 0
+            qo, ko = torch.zeros(T, 32, 64, dtype=torch.bfloat16, device=dev), torch.zeros(T, 8, 64, dtype=torch.bfloat16, device=dev)
+            for t in range(0, T, step):
+                x = qkv[t:t + step]
+                lib.kv_append_norm_rope(x[:, 32:40], x[:, 40:], pos[t:t + step], bt, pool, cos, sin, token_seq=seq[t:t + step],
+                                        q_in=x[:, :32], q_out=qo[t:t + step], k_out=ko[t:t + step], q_weight=w, k_weight=w,
+                                        interleaved=inter)
+            got.append((qo, ko, pool[-313:].clone()))
+        for a, b in zip(*got):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        k = got[0][2].transpose(2, 3).reshape(313, 2, 16, 8, 64).transpose(0, 1).reshape(2, -1, 8, 64)[:, :T]
+        assert torch.equal(k[0], got[0][1]) and torch.equal(k[1], qkv[:, 40:])
+    assert not pool[:-313].any()
+
+
 def test_zero_rows_and_no_tokens(lib, cuda_device):
     dev = cuda_device
     cos, sin, _ = tables(lib, dev, 32, 16)

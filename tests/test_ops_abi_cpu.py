@@ -111,7 +111,7 @@ def _checks():
     for bad in (dict(k=odd), dict(v=odd), dict(q=odd), dict(qo=odd), dict(pool=odd), dict(cos=odd), dict(cu=odd),
                 dict(sc=odd), dict(ks=513), dict(qs=2052), dict(err=odd)):
         assert ap(**bad) == 2, bad
-    assert ap(mb=(1 << 26) + 1, row=(1 << 26) + 1) == 3
+    assert ap(mb=(1 << 26) + 1, row=(1 << 26) + 1) == 3 and ap(T=(1 << 29) + 1) == 3
 
     def rd(**kw):
         a = dict(pool=f, sc=f, pages=8, code=1, ids=f, n=3, out=f, err=none)
