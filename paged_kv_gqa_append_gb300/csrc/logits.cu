@@ -66,13 +66,13 @@ constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's ot
 
 // How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
 // filled while others stream (256 x 128256 fp32 with penalties, biases and
-// output 68 us, with 2 x 512 threads 81 us).  When all CTAs fit on the GPU at
+// output 62 us, with 2 x 512 threads 81 us).  When all CTAs fit on the GPU at
 // once there is nothing else to overlap with, and more threads shorten both
 // parts (32 x 128256 bf16 13.0 us, with 256 threads 16.0 us).
 struct Many {
   static constexpr int kThreads = 256, kResident = 4;
   static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
-  static constexpr int kIds = 8;    // ids in flight per thread, at most 8 (3 bits of the queue)
+  static constexpr int kIds = 4;    // ids in flight per thread, at most 8 (3 bits of the queue); 8 spill: 68 us
 };
 struct Few {
   static constexpr int kThreads = 512, kResident = 2;
