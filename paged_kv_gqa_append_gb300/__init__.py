@@ -5,7 +5,11 @@ dtypes, devices and shapes of torch tensors, pass raw pointers, sizes and the
 current CUDA stream to the library, and raise ``PkvError`` on a non-zero
 status.  Every step of the computation runs in the library's sm_103a kernels;
 there is no fallback: the first call raises when libpkv.so is missing (build
-it with ``python -m paged_kv_gqa_append_gb300.build``).
+it with ``python -m paged_kv_gqa_append_gb300.build``).  The calls that are
+small enough for the host's time to count go through _calls.so first
+(binding/calls.cpp), which does the same checks on the tensors in C++ and makes
+the same C call; whatever it does not take as it is comes back to the functions
+here, which say what is wrong or make the call.
 
 Tensor layouts (see include/pkv.h):
     kv_pool       [num_pages, 2, 8, 16, 64] bf16   (K = 0, V = 1), 32 KiB/page
@@ -16,6 +20,7 @@ Tensor layouts (see include/pkv.h):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -23,6 +28,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 
 NUM_Q_HEADS = 32
 NUM_KV_HEADS = 8
@@ -139,6 +145,23 @@ def _L():
             fn.argtypes = args
         _LIB = lib
     return _LIB
+
+
+_CALLS = None
+
+
+def _load_calls():
+    """The module of binding/calls.cpp (it needs the torch that is imported here)."""
+    global _CALLS
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"_calls.so not found at {CALLS_PATH}; build it with "
+                           "`python -m paged_kv_gqa_append_gb300.build`")
+    _L()
+    spec = importlib.util.spec_from_file_location(__name__ + "._calls", CALLS_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _CALLS = module
+    return module
 
 
 def __getattr__(name):
@@ -300,9 +323,9 @@ _PAGE = (2, NUM_KV_HEADS, PAGE_TOKENS, HEAD_DIM)
 _PAGE_ELEMS = 2 * NUM_KV_HEADS * PAGE_TOKENS * HEAD_DIM
 
 
-# The checks below cost about 0.1 us per attribute of a tensor, which is what
-# a small call's host time is made of: each attribute is read once, and the
-# error messages are made only when a check fails (_need says what is wrong).
+# The checks of the calls that _calls.so did not take: each attribute of a
+# tensor is read once (about 0.1 us each), and the error messages are made only
+# when a check fails (_need says what is wrong).
 
 def _on_device(t, name):
     """The CUDA device of `t`."""
@@ -413,6 +436,12 @@ def _weight(w, name, dev):
 
 def _norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos, rope_sin, q_out, k_out,
                q_weight, k_weight, eps, interleaved, d_err, max_blocks, stream):
+    if stream is None:
+        st = (_CALLS or _load_calls()).norm_rope(q, k, v, positions, token_seq, block_tables, kv_pool, rope_cos,
+                                                 rope_sin, q_out, k_out, q_weight, k_weight, eps, interleaved, d_err,
+                                                 max_blocks)
+        if st >= 0:
+            return _check(st, "kv_append_norm_rope")
     dev = _on_device(k, "k")
     k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
     q_ptr = v_ptr = bt = pool = seq = None
@@ -798,6 +827,11 @@ def kv_append_rope_bs8(k, v, cu_new, seq_lens, block_tables, kv_pool, kv_scales,
     set its scale together, and a block whose scale grows has its held codes
     written again (pkv.h).  k, v [T, 8, 64], q_in [T, 32, 64] bf16 with any
     token stride that is a multiple of 8."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).append_bs8(kv_pool, kv_scales, k, v, cu_new, seq_lens, block_tables, rope_cos,
+                                                  rope_sin, q_in, q_out, d_err, max_blocks)
+        if st >= 0:
+            return _check(st, "kv_append_rope_bs8")
     dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
     k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
     v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
@@ -835,6 +869,11 @@ def kv_read_bs8(kv_pool, kv_scales, page_ids, out=None, d_err=None, stream=None)
     """Pages page_ids of a block-scaled pool as bf16 pages
     [len(page_ids), 2, 8, 16, 64] (a bf16 pool, e.g. for paged_gqa_prefill over
     a cached prefix with block table 0 .. n - 1)."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).read_bs8(kv_pool, kv_scales, page_ids, out, d_err)
+        if st >= 0:
+            _check(st, "kv_read_bs8")
+            return out
     dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
     n = page_ids.numel()
     ids = _vec(page_ids, "page_ids", _I32, dev, n)
@@ -866,6 +905,11 @@ def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, sca
     """paged_gqa_decode over block-scaled 8-bit pages (new_bs8_pool): q, out
     [num_seqs, 32, 64] bf16, q rotated.  workspace: alloc_bs8_workspace, one
     for each stream or captured graph that may run at the same time."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).decode_bs8(kv_pool, kv_scales, q, block_tables, seq_lens, out, scale, workspace,
+                                                  max_seq_len, d_err, max_blocks)
+        if st >= 0:
+            return _check(st, "paged_gqa_decode_bs8")
     dev, pool, scales, pages, code = _bs8_pool(kv_pool, kv_scales)
     shape = q.shape
     if shape[-2:] != _Q_ROW:
@@ -1096,6 +1140,14 @@ def process_logits(logits, out=None, ids=None, history=None, history_lens=None, 
     bias_values [rows, B] int32 / fp32; ids outside the vocabulary are padding.
     allow_mask [rows, >= ceil(vocab / 32)] int32, bit i % 32 of word i / 32 set:
     token i is allowed."""
+    if stream is None:
+        if ids is None and isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2:
+            ids = torch.empty(logits.shape[0], dtype=_I32, device=logits.device)
+        st = (_CALLS or _load_calls()).process_logits(logits, out, ids, history, history_lens, prompt_lens, repetition,
+                                                      presence, frequency, bias_ids, bias_values, allow_mask)
+        if st >= 0:
+            _check(st, "pkv_process_logits")
+            return ids
     dev = _on_device(logits, "logits")
     shape, stride, dtype = logits.shape, logits.stride(), LOGITS_DTYPES.get(logits.dtype)
     if dtype is None or len(shape) != 2:

@@ -5,16 +5,21 @@
 Translation units compile in parallel; objects go to ``_build/`` at the repo
 root and the shared library to ``paged_kv_gqa_append_gb300/libpkv.so``.
 The CUDA runtime is linked statically, so the library loads on a machine
-without a GPU driver (calls then fail with PKV_ERR_CUDA).
+without a GPU driver (calls then fail with PKV_ERR_CUDA).  The Python binding's
+marshalling of the small calls (binding/calls.cpp) is compiled against the
+installed torch into ``paged_kv_gqa_append_gb300/_calls.so``; libpkv.so itself
+needs neither Python nor torch.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +27,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
+BINDING = os.path.join(PKG, "binding", "calls.cpp")
+BINDING_LIB = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 HOST_FLAGS = "-fPIC,-ffp-contract=off,-O2"
@@ -43,13 +50,13 @@ def sources():
 def _inputs():
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return sources() + headers + [os.path.abspath(__file__)]
+    return sources() + headers + [BINDING, os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
@@ -64,14 +71,41 @@ def _compile(src: str, ptxas_verbose: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD, "calls.cpp.o")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING, "-o", obj,
+           "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str):
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-lpkv", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _calls.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
     """Compile every translation unit and link libpkv.so; returns its path."""
     if not force and not ptxas_verbose and not is_stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
+        binding_obj = binding.result()
     objs = [o for o, _ in results]
     logs = "".join(e for _, e in results)
     if ptxas_verbose:
@@ -83,6 +117,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if not quiet:
         print(f"built {LIB}")
         if ptxas_verbose:

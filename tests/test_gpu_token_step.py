@@ -113,3 +113,46 @@ def test_prefill_over_a_cached_prefix_read_back(lib, cuda_device):
     for i in range(9):
         ref, bad = OP.decode(bits(qr[i:i + 1]), bits(wide), np.arange(4, dtype=np.int32)[None], [41 + i], 0.125)
         check_close(bf16_to_f64(out[i:i + 1]), ref, f"row {i}")
+
+
+def test_usual_calls_are_marshalled_natively_and_equal_the_others(lib, cuda_device, monkeypatch):
+    """The calls of a step never reach the ctypes way; through it (a stream
+    given) they give the same bits."""
+    dev, S = cuda_device, 5
+    cos, sin = lib.rope_tables_device(dev, 64)
+    qkv = to_dev_bf16(rows(20, S, 48, 64), dev)
+    q, k, v = qkv[:, :32], qkv[:, 32:40], qkv[:, 40:]
+    w = torch.ones(64, device=dev)
+    bt = to_dev_i32(np.arange(S * 2).reshape(S, 2), dev)
+    pos, lens, cu = (to_dev_i32(x, dev) for x in ([3, 16, 0, 31, 7], [4, 17, 1, 32, 8], np.arange(S + 1)))
+    logits = torch.randn(S, 500, generator=torch.Generator("cpu").manual_seed(1)).to(dev)
+    hist, hl = to_dev_i32(np.arange(S * 4).reshape(S, 4), dev), to_dev_i32([4] * S, dev)
+    seen = []
+    real = lib._call
+    monkeypatch.setattr(lib, "_call", lambda dev, stream, where, args: (seen.append(where), real(dev, stream, where, args)))
+    got = []
+    for stream in (None, torch.cuda.current_stream(dev)):
+        pool16 = torch.zeros((S * 2, 2, 8, 16, 64), dtype=torch.bfloat16, device=dev)
+        pool, sc = lib.new_bs8_pool(S * 2, dev, torch.float8_e4m3fn)
+        qo, ko, out = (torch.zeros(S, n, 64, dtype=torch.bfloat16, device=dev) for n in (32, 8, 32))
+        ws = lib.alloc_bs8_workspace(S, dev)
+        err = torch.zeros(1, dtype=torch.int32, device=dev)
+        lib.kv_append_norm_rope(k, v, pos, bt, pool16, cos, sin, q_in=q, q_out=qo, q_weight=w, k_weight=w, d_err=err, stream=stream)
+        lib.qk_norm_rope(q, k, pos, cos, sin, qo, ko, q_weight=w, d_err=err, stream=stream)
+        lib.kv_append_rope_bs8(k, v, cu, lens, bt, pool, sc, cos, sin, q, qo, err, stream=stream)
+        wide = lib.kv_read_bs8(pool, sc, bt[0].contiguous(), torch.empty((2, 2, 8, 16, 64), dtype=torch.bfloat16, device=dev), err, stream=stream)
+        lib.paged_gqa_decode_bs8(qo, pool, sc, bt, lens, out, 0.125, workspace=ws, max_seq_len=32, d_err=err, stream=stream)
+        ids = lib.process_logits(logits, history=hist, history_lens=hl, frequency=torch.ones(S, device=dev), stream=stream)
+        torch.cuda.synchronize(dev)
+        assert lib.pkv_read_device_error(err) == 0
+        got.append([pool16, qo, ko, pool.view(torch.int8), sc, wide, out, ids])
+        assert len(seen) == (0 if stream is None else 6), seen
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # what is refused is refused by the Python checks, with their words
+    with pytest.raises(ValueError, match="positions must have 5 elements"):
+        lib.qk_norm_rope(q, k, pos[:3], cos, sin, qo, ko)
+    with pytest.raises(ValueError, match="num_seqs"):
+        lib.paged_gqa_decode_bs8(qo, pool, sc, bt[:3], lens, out, 0.125)
+    with pytest.raises(lib.PkvError, match="WORKSPACE"):
+        lib.paged_gqa_decode_bs8(qo, pool, sc, bt, lens, out, 0.125, workspace=ws[:16])
