@@ -131,6 +131,19 @@ __device__ __forceinline__ void take(float v, int i, float& bv, int& bi) {
   }
 }
 
+// Logits as whole numbers in the same order, -0 equal to 0, above 0 = none.
+__device__ __forceinline__ uint32_t order_of(float v, int i) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return i < 0 ? 0u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The warp's largest, and the lowest id among its equals (0xFFFFFFFF: none).
+__device__ __forceinline__ void best_of_warp(uint32_t& top, uint32_t& id) {
+  const uint32_t most = __reduce_max_sync(0xffffffffu, top);
+  id = __reduce_min_sync(0xffffffffu, top == most ? id : 0xFFFFFFFFu);
+  top = most;
+}
+
 // 8 bytes into the shared memory of the cluster's first CTA, counted on its
 // barrier; both addresses as they are in this CTA's own window.
 __device__ __forceinline__ void send8(uint32_t dst, uint32_t bar, uint64_t value) {
@@ -192,11 +205,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
   constexpr int N = 16 / (int)sizeof(T);  // tokens per 16 bytes
   // the table: token of the pass, its count (then its finished logit), its bias entry + 1
   __shared__ __align__(16) uint32_t key[kSlots], count[kSlots], entry[kSlots];
-  __shared__ float best_v[kThreads / 32];
-  __shared__ int best_i[kThreads / 32];
-  __shared__ uint64_t best_of[kCtas], arrived;  // of the cluster's first CTA: (id, value bits) of all
+  __shared__ uint2 best[kThreads / 32];
+  __shared__ uint64_t best_of[kCtas], arrived;  // of the cluster's first CTA: (id, order) of all
   __shared__ uint32_t allow[kMostTokens / 32];  // the stream's tokens, a bit per token of the pass
   __shared__ uint16_t list[kList];
+  __shared__ float list_x[kList];
   __shared__ uint32_t queue[kThreads / 32][kIds * 32];  // token of the pass, and which id of the round it is
   __shared__ int listed;
   cg::cluster_group cluster = cg::this_cluster();
@@ -285,8 +298,10 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
           for (int i0 = 0; i0 < packed; i0 += 32) {
             bool entered = false;
             int slot = -1;
+            float v = 0.f;
             if (i0 + lane < packed) {
               const uint32_t e = queue[warp][i0 + lane];
+              v = load1(x + first + (e >> 8));  // needed if the token is new; under way meanwhile
               slot = slot_of((int)(e >> 8), entered);
               if (slot >= 0) f(slot, k0 + (int)(e & 31u) + (int)(e >> 5 & 7u) * kThreads);
             }
@@ -295,7 +310,10 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
               int where = 0;
               if (lane == 0) where = atomicAdd(&listed, __popc(fresh));
               where = __shfl_sync(0xffffffffu, where, 0) + __popc(fresh & ((1u << lane) - 1));
-              if (entered && where < kList) list[where] = (uint16_t)slot;
+              if (entered && where < kList) {
+                list[where] = (uint16_t)slot;
+                list_x[where] = v;
+              }
             }
           }
         }
@@ -327,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
       }
       for (int i = threadIdx.x; i < listed; i += kThreads) {
         const int slot = list[i], at = (int)key[slot];
-        const float v = change(load1(x + first + at), count[slot], entry[slot], r);
+        const float v = change(list_x[i], count[slot], entry[slot], r);
         // out of the stream's hands; one that was masked out before stays -inf
         const bool was = atomicAnd(allow + (at >> 5), ~(1u << (at & 31))) >> (at & 31) & 1u;
         count[slot] = was ? (v != v ? 0x7FFFFFFFu : __float_as_uint(v)) : kMaskedBits;
@@ -406,37 +424,27 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
     if (base < p.part) __syncthreads();  // the next pass uses the table again
   }
 
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float ov = __shfl_down_sync(0xffffffffu, bv, o);
-    const int oi = __shfl_down_sync(0xffffffffu, bi, o);
-    take(ov, oi, bv, bi);
-  }
-  if (lane == 0) {
-    best_v[warp] = bv;
-    best_i[warp] = bi;
-  }
+  uint32_t top = order_of(bv, bi), id = (uint32_t)bi;
+  best_of_warp(top, id);
+  if (lane == 0) best[warp] = make_uint2(top, id);
   __syncthreads();
   cluster.barrier_wait();  // every CTA of the cluster has started
+  if (!p.ids) return;
   if (warp == 0) {
-    bv = lane < kThreads / 32 ? best_v[lane] : 0.f;
-    bi = lane < kThreads / 32 ? best_i[lane] : -1;
-#pragma unroll
-    for (int o = kThreads / 64; o > 0; o >>= 1) {
-      const float ov = __shfl_down_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_down_sync(0xffffffffu, bi, o);
-      take(ov, oi, bv, bi);
+    const uint2 w = lane < kThreads / 32 ? best[lane] : make_uint2(0u, 0xFFFFFFFFu);
+    top = w.x;
+    id = w.y;
+    best_of_warp(top, id);
+    if (lane == 0) send8(smem_u32(&best_of[rank]), smem_u32(&arrived), (uint64_t)id << 32 | top);
+    if (rank == 0) {
+      const bool all = wait_cluster(smem_u32(&arrived));
+      const uint64_t e = all && lane < kCtas ? best_of[lane] : 0xFFFFFFFFull << 32;
+      top = (uint32_t)e;
+      id = (uint32_t)(e >> 32);
+      best_of_warp(top, id);
+      if (lane == 0) p.ids[row] = (int)id;
     }
-    if (lane == 0 && p.ids)
-      send8(smem_u32(&best_of[rank]), smem_u32(&arrived),
-            (uint64_t)(uint32_t)bi << 32 | (uint64_t)__float_as_uint(bv));
   }
-  if (rank != 0 || threadIdx.x != 0 || !p.ids) return;
-  float v = 0.f;
-  int i = -1;
-  if (wait_cluster(smem_u32(&arrived)))
-    for (int k = 0; k < kCtas; ++k) take(__uint_as_float((uint32_t)best_of[k]), (int)(best_of[k] >> 32), v, i);
-  p.ids[row] = i;
 }
 
 template <typename T, typename Shape>
