@@ -26,7 +26,8 @@
 // and one table row.  24 warps per SM (80 registers) keep 144 KB in flight;
 // with 16 warps 32768 tokens take 87 us, not 74.  With 16 contiguous bytes per
 // lane and the partners fetched by shuffles, and three warps per token, they
-// took 131 us: 2450 instructions a token, half of the issue slots.
+// took 131 us: 2450 instructions a token, half of the issue slots; with two
+// 16-byte loads per lane and four lanes per row, 79 us.  Interleaved pairs: 68 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -133,6 +134,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_ro
   bool turned;
   places<kLayout>(j, p.pairs, lo, hi, turned);
 
+  // the way to the table and page entries starts first, then everything else is under way
+  const int pos = __ldg(p.positions + t);
+  const int row = p.pool && p.token_seq ? __ldg(p.token_seq + t) : t;
   uint4 raw[kMine];
   const uint16_t* q = p.q + (long long)t * p.q_stride;
   const uint16_t* k = p.k + (long long)t * p.k_stride;
@@ -142,14 +146,12 @@ __global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_ro
     if (!is_v(g) || p.pool)
       raw[g] = load_row<kLayout>((is_q(g) ? q : is_v(g) ? v : k) + head_of(g) * kRow, lo, hi);
 
-  const int pos = __ldg(p.positions + t);
   bool ok = pos >= 0 && pos < p.max_pos;
   int page = -1;
   if (p.pool) {
-    const int s = p.token_seq ? __ldg(p.token_seq + t) : t;
-    ok = ok && s >= 0 && s < p.num_seqs && pos / PKV_PAGE_TOKENS < p.max_blocks;
+    ok = ok && row >= 0 && row < p.num_seqs && pos / PKV_PAGE_TOKENS < p.max_blocks;
     if (ok) {
-      page = __ldg(p.block_tables + (size_t)s * p.bt_stride + pos / PKV_PAGE_TOKENS);
+      page = __ldg(p.block_tables + (size_t)row * p.bt_stride + pos / PKV_PAGE_TOKENS);
       ok = page >= 0 && page < p.num_pages;
     }
   }
