@@ -30,7 +30,13 @@
 // division and are rounded to fp16 for the product (half a step is 2^-12 of
 // one, against 2^-9 of the bf16 result); their sum is over the unrounded ones.
 //
-// Bound: memory, 1 KiB + 4 B of scales per token.
+// Bound: memory, 1 KiB + 4 B of scales per token.  Of 32 sequences of 2048 tokens
+// (19.4 us, 51 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
+// us go by before the first copy is issued (lengths, their sums, the table
+// entries: loads that wait for one another), 3 us at the end, where SMs of larger
+// GPCs get less bandwidth each and finish their equal shares later, and 2.8 us
+// for the merge.  97 sequences of up to 8191 tokens run at 81 %.  A page holds
+// one warp for about 150 instructions; the tensor pipe is busy 27 % of the time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
