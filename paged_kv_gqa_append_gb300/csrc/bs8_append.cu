@@ -20,9 +20,10 @@
 //
 // Bound: memory, 3 KiB per token for K and V, and 8 KiB for q.  Codes without a
 // division per value (bs8.cuh) and rotations without shuffles took 14400 tokens
-// of eight prompts from 65 us to 35 us.  A step of few tokens is latency: the
-// sequence search (one round of a 32-way search for up to 1023 sequences), the
-// table entry, the rows, the old scale.
+// of eight prompts from 65 us to 33 us.  A step of few tokens is latency: the
+// token's place (without a search where a step has one token per sequence; else
+// one round of a 32-way search for up to 1023 sequences), then the table entry,
+// the rows and the rotations together, then the old scale.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -77,15 +78,28 @@ struct Place {
 
 __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
   Place a{-1, 0, t + 1, false, false, false};
-  a.seq = find_sequence(p.cu_new, p.num_seqs, t);
-  if (a.seq >= p.num_seqs) {  // rows behind the last sequence are left alone
-    a.end = p.T;
-    return a;
+  int lo = 0, hi = 0, len = 0;
+  bool found = false;
+  if (p.T == p.num_seqs) {  // a step of one token each, most likely: row t is sequence t's
+    lo = __ldg(p.cu_new + t);
+    hi = __ldg(p.cu_new + t + 1);
+    len = __ldg(p.seq_lens + t);
+    found = lo == t && hi == t + 1;
+    a.seq = t;
+  }
+  if (!found) {
+    a.seq = find_sequence(p.cu_new, p.num_seqs, t);
+    if (a.seq >= p.num_seqs) {  // rows behind the last sequence are left alone
+      a.end = p.T;
+      return a;
+    }
+    a.live = true;
+    if (a.seq < 0) return a;
+    lo = __ldg(p.cu_new + a.seq);
+    hi = __ldg(p.cu_new + a.seq + 1);
+    len = __ldg(p.seq_lens + a.seq);
   }
   a.live = true;
-  if (a.seq < 0) return a;
-  const int lo = __ldg(p.cu_new + a.seq), hi = __ldg(p.cu_new + a.seq + 1);
-  const int len = __ldg(p.seq_lens + a.seq);
   const int fresh = hi - lo;
   if (hi <= t || hi > p.T || lo < 0) return a;  // not ascending, or beyond the rows given
   a.end = hi;
@@ -126,17 +140,17 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
-// K (kv = 0) or V rows of one head of a run: slots [slot, slot + n) of the page.
+// K (kv = 0) or V rows of one head of a run: slots [slot, slot + n) of the page
+// that `entry` of the block table names.  The page is needed last: its entry, the
+// rows and the rotations are under way together.
 template <bool kE4m3>
-__device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int pos, int n, int page, int kv,
-                                           int head) {
+__device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int pos, int n, const int32_t* entry,
+                                           int kv, int head) {
   const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
   const int slot = pos % PKV_PAGE_TOKENS;
   const uint16_t* src = kv ? p.v : p.k;
   const long long stride = kv ? p.v_stride : p.k_stride;
-  uint8_t* block = p.pool + ((size_t)page * 2 + kv) * (PKV_NUM_KV_HEADS * kBs8BlockBytes) +
-                   (size_t)head * kBs8BlockBytes;
-  float* scale = p.scales + ((size_t)page * 2 + kv) * PKV_NUM_KV_HEADS + head;
+  const int page = __ldg(entry);
 
   uint4 raw[4];
 #pragma unroll
@@ -145,17 +159,32 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
     raw[i] = make_uint4(0, 0, 0, 0);
     if (r >= 0 && r < n) raw[i] = load_halves(src + (long long)(t + r) * stride + head * kRow, j);
   }
-  float old = 0.f;
-  if (slot && lane == 0) old = *scale;
-  if (kv == 0 && p.cos) {
+  const bool turn = kv == 0 && p.cos;
+  float4 c[4], s[4];  // rows beside the run (of zeros) take its first entry
+  if (turn) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * i + sub - slot;
-      if (r < 0 || r >= n) continue;
-      const size_t row = (size_t)(pos + r) * PKV_ROPE_PAIRS + 4 * j;
+      const size_t row = (size_t)(r >= 0 && r < n ? pos + r : pos) * PKV_ROPE_PAIRS + 4 * j;
+      c[i] = __ldg(reinterpret_cast<const float4*>(p.cos + row));
+      s[i] = __ldg(reinterpret_cast<const float4*>(p.sin + row));
+    }
+  }
+  if (page < 0 || page >= p.num_pages) {
+    if (threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+    return;
+  }
+  uint8_t* block = p.pool + ((size_t)page * 2 + kv) * (PKV_NUM_KV_HEADS * kBs8BlockBytes) +
+                   (size_t)head * kBs8BlockBytes;
+  float* scale = p.scales + ((size_t)page * 2 + kv) * PKV_NUM_KV_HEADS + head;
+  float old = 0.f;
+  if (slot && lane == 0) old = *scale;
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       float x[8];
       widen8(raw[i], x);
-      rotate8(x, __ldg(reinterpret_cast<const float4*>(p.cos + row)), __ldg(reinterpret_cast<const float4*>(p.sin + row)));
+      rotate8(x, c[i], s[i]);
       raw[i] = narrow8(x);
     }
   }
@@ -165,9 +194,9 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
   for (int i = 0; i < 4; ++i) {
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
   }
-  const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, max(top & 0xFFFF0000u, top << 16)));
   old = __shfl_sync(0xffffffffu, old, 0);
   const float fresh = __fdiv_rn(amax, kE4m3 ? 448.f : 127.f);
   const bool grown = slot > 0 && fresh > old;
@@ -210,13 +239,9 @@ __device__ __forceinline__ void append_chunk(const Bs8AppendParams& p, int t0, i
     }
     const int slot = a.pos % PKV_PAGE_TOKENS;
     const int n = min(PKV_PAGE_TOKENS - slot, a.end - t);
-    if (a.first || slot == 0) {
-      const int page = __ldg(p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS);
-      if (page >= 0 && page < p.num_pages)
-        append_run<kE4m3>(p, t, a.pos, n, page, warp >> 3, warp & 7);
-      else if (threadIdx.x == 0)
-        report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
-    }
+    if (a.first || slot == 0)  // else it began in an earlier chunk
+      append_run<kE4m3>(p, t, a.pos, n, p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS,
+                        warp >> 3, warp & 7);
     t += n;
   }
 }
@@ -238,15 +263,13 @@ __device__ __forceinline__ void rotate_chunk(const Bs8AppendParams& p, int t0, i
   const Place a = place_of(p, t);
   if (!a.live) return;
   bool ok = a.ok;
-  if (ok) {
-    const int page = __ldg(p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS);
-    ok = page >= 0 && page < p.num_pages;
-  }
   float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
   if (ok) {
+    const int page = __ldg(p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS);
     const size_t row = (size_t)a.pos * PKV_ROPE_PAIRS + 4 * j;
     c = __ldg(reinterpret_cast<const float4*>(p.cos + row));
     s = __ldg(reinterpret_cast<const float4*>(p.sin + row));
+    ok = page >= 0 && page < p.num_pages;
   }
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
@@ -279,9 +302,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) bs8_append_kernel(const Bs8App
 
 // out[i] = the page page_ids[i] as bf16: code * scale, rounded once.  One CTA
 // per page, 16 codes per thread and step; bound by memory (16 KiB read,
-// 32 KiB written per page).
-template <bool kE4m3>
-__global__ void __launch_bounds__(256) bs8_read_kernel(const uint8_t* __restrict__ pool,
+// 32 KiB written per page) and, for the usual few hundred pages, by its start and
+// end: 906 pages take 9.8 us with 512 threads and 11.9 us with 256, 32 pages 2.6
+// and 2.4 us, so that a grid of one CTA per SM at most takes 256.
+template <bool kE4m3, int kReadThreads>
+__global__ void __launch_bounds__(kReadThreads) bs8_read_kernel(const uint8_t* __restrict__ pool,
                                                        const float* __restrict__ scales, int num_pages,
                                                        const int32_t* __restrict__ page_ids,
                                                        uint16_t* __restrict__ out, int* d_err) {
@@ -292,12 +317,12 @@ __global__ void __launch_bounds__(256) bs8_read_kernel(const uint8_t* __restrict
   if (!ok && threadIdx.x == 0) report_error(d_err, PKV_ERR_DEVICE_INDEX);
   uint16_t* dst = out + (size_t)blockIdx.x * kBs8PageBytes;
   const uint8_t* src = pool + (size_t)(ok ? page : 0) * kBs8PageBytes;
-  constexpr int kSteps = kBs8PageBytes / (256 * 16);
+  constexpr int kSteps = kBs8PageBytes / (kReadThreads * 16);
   uint4 raw[kSteps];
   float scale[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int at = (i * 256 + threadIdx.x) * 16;
+    const int at = (i * kReadThreads + threadIdx.x) * 16;
     raw[i] = make_uint4(0, 0, 0, 0);
     scale[i] = 0.f;
     if (ok) {
@@ -307,7 +332,7 @@ __global__ void __launch_bounds__(256) bs8_read_kernel(const uint8_t* __restrict
   }
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int at = (i * 256 + threadIdx.x) * 16;
+    const int at = (i * kReadThreads + threadIdx.x) * 16;
     const uint2 half[2] = {make_uint2(raw[i].x, raw[i].y), make_uint2(raw[i].z, raw[i].w)};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -415,15 +440,14 @@ extern "C" int kv_read_bs8(const void* kv_pool, const float* kv_scales, int num_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)count);
-  cfg.blockDim = dim3(256);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const uint8_t* pool = static_cast<const uint8_t*>(kv_pool);
-  uint16_t* dst = static_cast<uint16_t*>(out);
-  return cuda_status(
-      code_type == PKV_BS8_E4M3
-          ? cudaLaunchKernelEx(&cfg, bs8_read_kernel<true>, pool, kv_scales, num_pages, page_ids, dst, d_err)
-          : cudaLaunchKernelEx(&cfg, bs8_read_kernel<false>, pool, kv_scales, num_pages, page_ids, dst, d_err),
-      "cudaLaunchKernelEx(read bs8)");
+  const bool few = count <= sm_count(dev);
+  cfg.blockDim = dim3(few ? 256 : 512);
+  auto* kernel = code_type == PKV_BS8_E4M3 ? (few ? bs8_read_kernel<true, 256> : bs8_read_kernel<true, 512>)
+                                           : (few ? bs8_read_kernel<false, 256> : bs8_read_kernel<false, 512>);
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint8_t*>(kv_pool), kv_scales, num_pages, page_ids,
+                                        static_cast<uint16_t*>(out), d_err),
+                     "cudaLaunchKernelEx(read bs8)");
 }

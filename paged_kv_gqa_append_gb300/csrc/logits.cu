@@ -508,7 +508,8 @@ extern "C" int pkv_process_logits(const void* logits, int dtype, int rows, int v
                           reinterpret_cast<uintptr_t>(allow_mask);
   if ((words & 3u) || (reinterpret_cast<uintptr_t>(logits) & (dtype == PKV_LOGITS_F32 ? 3u : 1u)))
     return PKV_ERR_MISALIGNED;
-  if (rows > (1 << 27) || vocab > (1 << 30) || history_stride > (1ll << 30)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  if (rows > (1 << 27) || vocab > (1 << 30) || history_stride > (1ll << 30) || bias_count > (1 << 30))
+    return PKV_ERR_UNSUPPORTED_SHAPE;
   int dev = 0;
   const int rc = bind_stream_device(stream, &dev);
   if (rc != PKV_OK) return rc;

@@ -149,3 +149,4 @@ def _checks():
                 dict(out=odd, os=100)):
         assert lg(**bad) == 2, bad
     assert lg(vocab=(1 << 30) + 1, stride=1 << 31, ms=1 << 30) == 3
+    assert lg(B=(1 << 30) + 1) == 3 and lg(hs=(1 << 30) + 1) == 3
