@@ -31,11 +31,11 @@
 // one, against 2^-9 of the bf16 result); their sum is over the unrounded ones.
 //
 // Bound: memory, 1 KiB + 4 B of scales per token.  Of 32 sequences of 2048 tokens
-// (19.4 us, 51 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
+// (19.0 us, 52 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
 // us go by before the first copy is issued (lengths, their sums, the table
 // entries: loads that wait for one another), 3 us at the end, where SMs of larger
 // GPCs get less bandwidth each and finish their equal shares later, and 2.8 us
-// for the merge.  97 sequences of up to 8191 tokens run at 81 %.  A page holds
+// for the merge.  97 sequences of up to 8191 tokens run at 80 %.  A page holds
 // one warp for about 150 instructions; the tensor pipe is busy 27 % of the time.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -63,13 +63,18 @@ constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + kStagePages * kScaleB
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxSeqsBs8 = 4096;
 constexpr int kMinPages = 4;                            // least share of a CTA
+// Up to this many sequences the merge looks at every sequence; beyond it at every
+// CTA, in each of which one split sequence begins at most (4096 sequences of 64
+// tokens: 67 us, by sequence 107 us; 256 of 2048: 99 and 105 us; 97 mixed ones:
+// 75.5 and 74 us).
+constexpr int kBySequence = 128;
 constexpr uint32_t kWaitUs = 2000000;                   // limit of every wait
 constexpr float kLift = 14.f;                           // probabilities carry 2^14
 constexpr float kNothing = -1.f;                        // l of a part with a bad page
 
 // Workspace: per CTA two parts (of a sequence begun in an earlier CTA, and of
 // one that goes on in the next) of 32 heads, o [64] then (m, l) pairs; then
-// per sequence its first and last CTA.
+// which CTAs a split sequence lies in, by sequence or by CTA.
 constexpr int kPartFloats = PKV_NUM_Q_HEADS * (PKV_HEAD_DIM + 2);
 
 struct Bs8DecodeParams {
@@ -78,10 +83,11 @@ struct Bs8DecodeParams {
   const int32_t *block_tables, *seq_lens;
   uint16_t* out;
   float* parts;
-  int2* span;  // [num_seqs] first and last CTA of a split sequence, or (-1, -1)
+  int2* span;  // by sequence: first and last CTA of a split one; by CTA: the split sequence that begins
+               // there and its last CTA; else (-1, -1)
   int* d_err;
   float scale;
-  int num_pages, bt_stride, max_blocks, num_seqs, min_pages;
+  int num_pages, bt_stride, max_blocks, num_seqs, min_pages, by_cta;
 };
 
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
@@ -159,7 +165,7 @@ __device__ __forceinline__ void codes_by_dim(uint32_t w, uint32_t& d0, uint32_t&
 __device__ __forceinline__ int pages_of(const Bs8DecodeParams& p, int s, bool& refused) {
   const int n = __ldg(p.seq_lens + s);
   refused = n < 0 || n > (long long)p.max_blocks * PKV_PAGE_TOKENS;
-  return refused ? 0 : (n + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
+  return refused ? 0 : (int)(((unsigned)n + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS);
 }
 
 struct Smem {
@@ -176,22 +182,29 @@ struct Head {  // a consumer's state for one segment
   float o[4][4];          // O^T: dims 16 c + 2 g (+ 1), heads 2 t, 2 t + 1
   float m, l, unit;       // running maximum and this lane's sum of head g; scale of the scores
 
-  __device__ void start(const Bs8DecodeParams& p, int seq, int head) {
+  // q of a sequence as this lane will need it: 16 dims of head g, zeros in rows 4..7
+  struct Q {
+    uint4 a, b;
+  };
+  __device__ static Q fetch(const Bs8DecodeParams& p, int seq, int head) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float x[16];
+    Q q{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (g < PKV_GROUP) {
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + g) * PKV_HEAD_DIM + 16 * t);
-      const uint4 a = src[0], b = src[1];
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      q.a = src[0];
+      q.b = src[1];
+    }
+    return q;
+  }
+
+  __device__ void start(const Bs8DecodeParams& p, const Q& q) {
+    float x[16];
+    const uint32_t w[8] = {q.a.x, q.a.y, q.a.z, q.a.w, q.b.x, q.b.y, q.b.z, q.b.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[2 * e] = bf16lo_to_f32(w[e]);
-        x[2 * e + 1] = bf16hi_to_f32(w[e]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      x[2 * e] = bf16lo_to_f32(w[e]);
+      x[2 * e + 1] = bf16hi_to_f32(w[e]);
     }
     uint32_t bits = 0;  // of the largest finite |q|: magnitudes order as their bits
 #pragma unroll
@@ -370,19 +383,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   // Where this CTA's share of the list of pages (below 2^30 of them) begins: `before` pages and
   // `seq` sequences are in front of the one it begins in.
   int begin, end, seq, page;
+  unsigned share;
   const auto shares = [&](int total) {
-    int share = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
-    share = max(share + (share & 1), p.min_pages);
-    begin = (int)min((unsigned)total, (unsigned)share * blockIdx.x);
-    end = min(total, begin + share);
-    return (unsigned)share;
+    share = ((unsigned)total + gridDim.x - 1) / gridDim.x;
+    share = max(share + (share & 1u), (unsigned)p.min_pages);
+    begin = (int)min((unsigned)total, share * blockIdx.x);
+    end = min(total, begin + (int)share);
   };
-  // Which CTAs share sequence s, whose n pages begin at `at`, and the rows of one with nothing to
-  // read: written by one CTA for each sequence, while the producer is under way already.
-  const auto record = [&](int s, int at, int n, bool refused, unsigned share) {
+  // Which CTAs share sequence s, whose n pages begin at `at` (unless every CTA says so itself), and
+  // the rows of one with nothing to read: written by one CTA for each sequence, while the producer is
+  // under way already.
+  const auto record = [&](int s, int at, int n, bool refused) {
     if (s % (int)gridDim.x != (int)blockIdx.x) return;
-    const int c0 = (int)((unsigned)at / share), c1 = n ? (int)((unsigned)(at + n - 1) / share) : c0;
-    p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
+    if (!p.by_cta) {
+      const int c0 = (int)((unsigned)at / share), c1 = n ? (int)((unsigned)(at + n - 1) / share) : c0;
+      p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
+    }
     if (n == 0) {
       uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
       for (int i = 0; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
@@ -398,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       const int v = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += v;
     }
-    const unsigned share = shares(__shfl_sync(0xffffffffu, run, 31));
+    shares(__shfl_sync(0xffffffffu, run, 31));
     const int before = run - n;
     const uint32_t here = __ballot_sync(0xffffffffu, before <= begin && begin < run);
     seq = here ? __ffs(here) - 1 : 0;
     page = begin - __shfl_sync(0xffffffffu, before, seq);
     pdl_launch_dependents();
-    if (warp == 0 && lane < p.num_seqs) record(lane, before, n, refused, share);
+    if (warp == 0 && lane < p.num_seqs) record(lane, before, n, refused);
   } else {  // a consumer thread's sequences, then the sums over all
     const int per = (p.num_seqs + kConsumers * 32 - 1) / (kConsumers * 32);
     const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
@@ -427,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       if (w < warp) before += sh.sum[w];
       total += sh.sum[w];
     }
-    const unsigned share = shares(total);
+    shares(total);
     if (before <= begin && begin < before + mine) {
       int at = before;
       for (int s = s0; s < s1; ++s) {
@@ -448,11 +464,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
     for (int s = s0; s < s1; ++s) {
       bool refused;
       const int n = pages_of(p, s, refused);
-      record(s, at, n, refused, share);
+      record(s, at, n, refused);
       at += n;
     }
   }
-  if (begin >= end) return;
+  if (begin >= end) {
+    if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = make_int2(-1, -1);
+    return;
+  }
 
   int at = begin;
   int stage = 0;
@@ -520,12 +539,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   const int head = warp;
   Head<kE4m3> st;
   bool alive = true;
+  int2 split = make_int2(-1, -1);  // the sequence that begins here and goes on, and the last CTA that has a part of it
+  bool refused;
+  int pages = pages_of(p, seq, refused);
+  auto q = Head<kE4m3>::fetch(p, seq, head);
   while (at < end && alive) {
-    bool refused;
-    const int pages = pages_of(p, seq, refused);
     const int len = __ldg(p.seq_lens + seq);
     const int todo = min(pages - page, end - at);
-    st.start(p, seq, head);
+    st.start(p, q);
+    // the next sequence, and its q under way while this one is worked on
+    int next = seq + 1, next_pages = 0;
+    if (at + todo < end) {
+      while (next < p.num_seqs && (next_pages = pages_of(p, next, refused)) == 0) ++next;
+      if (next < p.num_seqs) q = Head<kE4m3>::fetch(p, next, head);
+    }
     bool bad = false;
     for (int i = 0; i < todo; i += kStagePages) {
       if (!mbar_wait_bounded(smem_u32(&sh.full[stage]), phase, kWaitUs)) {
@@ -548,11 +575,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
     // a part: of a sequence that began in an earlier CTA (slot 0) or begins here (slot 1)
     float* part = whole ? nullptr : p.parts + ((size_t)blockIdx.x * 2 + (page > 0 ? 0 : 1)) * kPartFloats;
     st.finish(p, seq, head, bad, part);
+    if (!whole && page == 0) split = make_int2(seq, (int)((unsigned)(at + pages - 1) / share));
     at += todo;
     page = 0;
-    ++seq;
-    while (at < end && seq < p.num_seqs && pages_of(p, seq, refused) == 0) ++seq;
+    seq = next;
+    pages = next_pages;
   }
+  if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = split;
   if (!alive && lane == 0) report_error(p.d_err, PKV_ERR_TIMEOUT);
 }
 
@@ -571,15 +600,17 @@ constexpr int kMergeThreads = 512;
 constexpr int kMergeBatch = 8;  // parts in flight per thread
 constexpr int kKept = 4;        // of all parts' (m, l): those that a lane has in flight and keeps
 
-template <bool kOneHead>
-__global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* parts, const int2* span,
-                                                                  uint16_t* out, int heads) {
+// kPerSm: 1 has the registers for everything in flight (90), where one wave is
+// enough; else two at a time matter more.
+template <bool kOneHead, int kPerSm>
+__global__ void __launch_bounds__(kMergeThreads, kPerSm) bs8_merge_kernel(const float* parts, const int2* span,
+                                                                  uint16_t* out, int heads, int by_cta) {
   extern __shared__ float weights[];  // one head: of all parts
   __shared__ float4 sums[kMergeThreads / 32][16];
   __shared__ float tops[kMergeThreads / 32], dens[kMergeThreads / 32];
   if (kOneHead) heads = 1;
   const int ctas = PKV_NUM_Q_HEADS / heads;
-  const int seq = blockIdx.x / ctas;
+  const int item = blockIdx.x / ctas;
   const int per = kMergeThreads / heads;  // threads of a head
   const int head = (blockIdx.x % ctas) * heads + threadIdx.x / per;
   const int group = (threadIdx.x % per) >> 4, groups = per >> 4;
@@ -587,8 +618,10 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
   const int dims = head * PKV_HEAD_DIM + 4 * sub, ml = PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * head;
   pdl_wait();
   pdl_launch_dependents();
-  const int2 c = span[seq];
+  int2 c = span[item];
   if (c.x < 0) return;
+  const int seq = by_cta ? c.x : item;
+  if (by_cta) c.x = item;
   const int n = c.y - c.x + 1;
   // the sequence begins in its first CTA (slot 1) and continues in the others (slot 0)
   const float* base = parts + (size_t)c.x * 2 * kPartFloats;
@@ -703,6 +736,10 @@ __global__ void __launch_bounds__(kMergeThreads) bs8_merge_kernel(const float* p
 
 size_t parts_bytes(int sms) { return (size_t)sms * kCtasPerSm * 2 * kPartFloats * sizeof(float); }
 
+size_t span_bytes(int sms, int num_seqs) {
+  return sizeof(int2) * (size_t)(num_seqs > kBySequence ? sms * kCtasPerSm : num_seqs > 0 ? num_seqs : 1);
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -717,7 +754,7 @@ extern "C" size_t paged_gqa_decode_bs8_workspace_bytes(int num_seqs) {
   }
   const int sms = sm_count(dev);
   if (sms <= 0) return 0;
-  return parts_bytes(sms) + (size_t)(num_seqs > 0 ? num_seqs : 1) * sizeof(int2);
+  return parts_bytes(sms) + span_bytes(sms, num_seqs);
 }
 
 extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_scales, int num_pages,
@@ -741,7 +778,7 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   if (rc != PKV_OK) return rc;
   const int sms = sm_count(dev);
   if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
-  if (workspace_bytes < parts_bytes(sms) + (size_t)num_seqs * sizeof(int2)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < parts_bytes(sms) + span_bytes(sms, num_seqs)) return PKV_ERR_WORKSPACE_TOO_SMALL;
 
   Bs8DecodeParams p;
   p.q = static_cast<const uint16_t*>(q);
@@ -758,6 +795,7 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   p.max_blocks = max_blocks;
   p.num_seqs = num_seqs;
   p.min_pages = kMinPages;
+  p.by_cta = num_seqs > kBySequence;
 
   CUtensorMap map;
   rc = make_bs8_map(&map, kv_pool, num_pages);
@@ -790,13 +828,14 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
                         : cudaLaunchKernelEx(&cfg, bs8_decode_kernel<false>, map, p),
                    "cudaLaunchKernelEx(decode bs8)");
   if (rc != PKV_OK || ctas == 1) return rc;  // one CTA splits nothing
-  const int heads = num_seqs <= 8 ? 1 : num_seqs <= 64 ? 8 : 16;
-  cfg.gridDim = dim3((unsigned)(num_seqs * (PKV_NUM_Q_HEADS / heads)));
+  const int heads = num_seqs <= 8 ? 1 : num_seqs * 4 <= sms ? 8 : 16;
+  const long long items = p.by_cta ? ctas - 1 : num_seqs;  // nothing goes on behind the last CTA
+  cfg.gridDim = dim3((unsigned)(items * (PKV_NUM_Q_HEADS / heads)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = heads == 1 ? (size_t)ctas * sizeof(float) : 0;
   const float* parts = p.parts;
   const int2* span = p.span;
-  return cuda_status(heads == 1 ? cudaLaunchKernelEx(&cfg, bs8_merge_kernel<true>, parts, span, p.out, heads)
-                                : cudaLaunchKernelEx(&cfg, bs8_merge_kernel<false>, parts, span, p.out, heads),
-                     "cudaLaunchKernelEx(merge bs8)");
+  auto* merge = heads == 1 ? bs8_merge_kernel<true, 2>
+                : (int)cfg.gridDim.x > sms ? bs8_merge_kernel<false, 2> : bs8_merge_kernel<false, 1>;
+  return cuda_status(cudaLaunchKernelEx(&cfg, merge, parts, span, p.out, heads, p.by_cta), "cudaLaunchKernelEx(merge bs8)");
 }

@@ -371,6 +371,30 @@ def test_decode_refuses_bad_sequences_alone(lib, cuda_device, kind):
     close(out[good], *ref, np.array(lens)[good])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("S", [128, 129, 300])
+def test_decode_many_sequences_long_short_empty_and_bad(lib, cuda_device, kind, S):
+    """Sequences over many CTAs between ones that share a CTA, with all that is refused."""
+    g = np.random.default_rng(60 + S)
+    lens = g.integers(0, 500, S)
+    lens[g.permutation(S)[:S // 3]] = g.integers(0, 18, S // 3)
+    lens[[5, S - 2]] = 9001, 6007
+    lens[[0, S - 1]] = 0, 700
+    pages = int(sum(-(-n // 16) for n in lens)) + 1
+    codes, scales = random_pages(61, pages, kind)
+    bt = tables_for(62, lens, pages)
+    q = rows(63, S, 32, 64)
+    check_decode(lib, cuda_device, kind, q, codes, scales, bt, lens)
+    bad = [5, 17, 18, 40, S - 1]
+    lens[[17, 18, 40]] = -3, bt.shape[1] * 16 + 1, 480
+    bt[5, 300], bt[S - 1, 43], bt[40, :30] = pages, -1, -1
+    out, code = decode(lib, cuda_device, kind, q, codes, scales, bt, lens)
+    assert code == lib.ERR_DEVICE_INDEX
+    assert (out[bad] == 0).all()
+    good = np.setdiff1d(np.arange(S), bad)
+    close(out[good], *O8.attend(q[good], codes, scales, bt[good], lens[good], 0.125, kind), lens[good])
+
+
 def test_decode_largest_batch_and_page_order(lib, cuda_device):
     S = 4096
     lens = np.random.default_rng(42).integers(0, 20, S).astype(np.int32)
