@@ -91,6 +91,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// `bytes` at `src` on their way into the L2; both multiples of 16.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // L2 policy under which the copied lines are evicted first: for data that a
 // call reads once and that is larger than the L2 (K/V pages of a large
 // batch), so that the small inputs read by every CTA stay resident.
