@@ -16,32 +16,36 @@
 // history and bias list (from L2) and keeps those of its part in a hash table in
 // shared memory -- open addressing, 2048 slots, at most about half of them used
 // -- with how often a token was generated, whether it was seen at all, and its
-// last bias entry.  A warp first packs the ids of its share that are in the part
-// (an eighth, on average), so that the slower entering runs with full warps.
+// last bias entry.  All warps first queue the ids that are in the part (an
+// eighth, on average) and take their tokens out of the bitmap of those that the
+// stream is to handle, which starts as the mask.  Then half of the warps enter
+// the queue into the table, 32 ids at a time, and finish the tokens, while the
+// other half streams already (256 rows of 128256 fp32 with everything kept 55 us;
+// all warps first at the table, then at the stream 56.5 us, a quarter 57.7 us).
 // Integer atomics give the same numbers in any order, wherever a token's slot
-// is.  Whoever enters a token lists its slot, and the listed ones are then
-// finished, one thread each, and taken out of the bitmap of the tokens that the
-// stream is to handle, which starts as the mask.
+// is.  Whoever enters a token lists its slot, and the listed ones are finished
+// one thread each.
 // A part with more than 1024 such tokens is done in passes over smaller ranges,
 // halved until one fits (a range of 1024 tokens always does).
 //
-// The stream over the part (16 bytes per load) tests a few bits per load and
-// treats what is not its own as -inf; the finished tokens are written over that,
-// and compete, behind it (looking them up from the stream made it five times as
-// long: some lane of a warp nearly always has one).  The table is
-// small on purpose: what shared memory takes from the L1 is missing as room for
-// loads in flight (a word per token of the part, 64 KiB a CTA, took 85 us for
-// 256 rows of 128256 with penalties and biases).  The ids and the stream's first
-// batch are loaded ahead, so that memory is busy while the table is filled.  A
-// thread keeps its largest value and its id; warp shuffles and shared memory reduce
-// them under a total order, and every CTA sends its best to the cluster's first
-// one, which alone waits for them (a closing cluster barrier kept all 8 until
-// the last had drained its stores).
+// The stream over the part (16 bytes per load, units of a few loads per warp,
+// claimed by whoever is free) tests a few bits per load and treats what is not
+// its own as -inf; the finished tokens are written over that, and compete, behind
+// it (looking them up from the stream made it five times as long: some lane of a
+// warp nearly always has one).  Logits changed in place are read for the table
+// before the stream starts.  The table is small on purpose: what shared memory
+// takes from the L1 is missing as room for loads in flight (a word per token of
+// the part, 64 KiB a CTA, took 85 us for 256 rows of 128256 with penalties and
+// biases).  The ids and a warp's first unit are loaded ahead, so that memory is
+// busy while the ids are queued.  A thread keeps its largest value and its id; warp
+// shuffles and shared memory reduce them under a total order, and every CTA sends
+// its best to the cluster's first one, which alone waits for them (a closing
+// cluster barrier kept all 8 until the last had drained its stores).
 //
 // Bound: memory, the logits read (and written, when they are kept): 256 rows of
-// 128256 fp32 logits take 25.5 us for the ids alone (77 % of the measured copy
-// rate), 43.5 us with the logits written, 53.7 us with penalties and biases.  One
-// row is latency: 3.0 us, 5.5 us with everything.
+// 128256 fp32 logits take 24.6 us for the ids alone (79 % of the measured copy
+// rate), 42.4 us with the logits written, 51.0 us with penalties and biases.  One
+// row is latency: 3.1 us, 5.5 us with everything.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -63,26 +67,28 @@ constexpr int kMostTokens = 16384;  // of a pass: the bitmaps
 constexpr int kSlots = 2048;        // of the table
 constexpr int kList = 1024;         // tokens entered; a CTA's threads more may be before all see that it is full
 constexpr uint32_t kSeen = 1u << 31;
+constexpr uint32_t kAllowed = 1u << 15;                            // of a listed slot: the mask leaves it
+constexpr uint32_t kBias = 1u << 14, kPrompt = 2u << 14, kWhat = 3u << 14;  // of a queued id; else generated
+constexpr int kEnterShare = 2;  // 1 of so many warps enters tokens while the others stream
 constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr uint32_t kMaskedBits = 0xFFFFDEADu;  // a NaN that stands for "masked out" in the table
 constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's other CTAs
 
 // How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
 // filled while others stream (256 x 128256 fp32 with penalties, biases and
-// output 58 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
+// output 55 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
 // once there is nothing else to overlap with, and more threads shorten both
-// parts (32 x 128256 bf16 12.2 us, with 256 threads 3 us more).
+// parts (32 x 128256 bf16 12.1 us, with 256 threads 3 us more).
 struct Many {
   static constexpr int kThreads = 256, kResident = 4;
   static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
-  static constexpr int kIds = 4;    // ids in flight per thread, at most 8 (3 bits of the queue); 8 spill: 68 us
+  static constexpr int kIds = 4;    // ids in flight per thread
 };
 struct Few {
   static constexpr int kThreads = 512, kResident = 2;
   static constexpr int kBatch = 2;
   static constexpr int kIds = 4;
 };
-
 
 struct LogitsParams {
   const void* logits;
@@ -204,19 +210,22 @@ __device__ __forceinline__ void load_ids(const int32_t* ids, int k0, int count, 
 
 template <typename T, int kThreads, int kResident, int kBatch, int kIds>
 __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const LogitsParams p) {
-  static_assert(kList + kThreads <= kSlots * 3 / 4 && kIds <= 8, "the table never fills up; the queue's bits");
   constexpr int N = 16 / (int)sizeof(T);  // tokens per 16 bytes
+  constexpr int kWarps = kThreads / 32, kEnterWarps = kWarps / kEnterShare;
+  constexpr int kRound = kIds * kThreads;          // ids at a time
+  constexpr int kQueue = kRound + (kRound > 1024 ? 512 : kRound);  // ids of the part that wait for the table (48 KB in all)
+  static_assert(kList + kThreads <= kSlots * 3 / 4, "the table never fills up");
+  static_assert(kMostTokens <= 1 << 14 && 65536 % kRound == 0, "the bits of the queue");
   // the table: token of the pass, its count (then its finished logit), its bias entry + 1
   __shared__ __align__(16) uint32_t key[kSlots], count[kSlots], entry[kSlots];
-  __shared__ uint2 best[kThreads / 32];
+  __shared__ uint2 best[kWarps];
   __shared__ uint64_t best_of[kCtas], arrived;  // of the cluster's first CTA: (id, order) of all
   __shared__ uint32_t allow[kMostTokens / 32];  // the stream's tokens, a bit per token of the pass
-  __shared__ uint16_t list[kList];
+  __shared__ uint16_t list[kList];              // slot, and kAllowed
   __shared__ float list_x[kList];
-  __shared__ uint32_t queue[kThreads / 32][kIds * 32];  // token of the pass, and which id of the round it is
-  __shared__ int listed;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  __shared__ uint32_t queue[kQueue];  // token of the pass, what it is (kBias and so on), low 16 bits of the bias entry
+  __shared__ int listed, queued, next_unit;
+  const int rank = (int)cg::this_cluster().block_rank();
   const int row = blockIdx.x / kCtas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (rank == 0 && threadIdx.x == 0) {
@@ -224,7 +233,9 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
     fence_mbar_init();
     mbar_arrive_expect_tx(smem_u32(&arrived), kCtas * 8);
   }
-  cluster.barrier_arrive();  // waited for before the first write into another CTA's shared memory
+  __syncwarp();
+  // waited for before the first write into another CTA's shared memory
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   pdl_launch_dependents();
 
@@ -255,15 +266,16 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
     const bool bits = mask || p.history || p.bias_count > 0;
     if (bits)
       for (int i = threadIdx.x; i < (n + 31) / 32; i += kThreads) allow[i] = mask ? __ldg(mask + (first >> 5) + i) : 0xFFFFFFFFu;
+    // a unit of the stream: kBatch loads of a warp; the first is its own in any case
+    int unit = warp;
+    const auto vec_of = [&](int which, int u) { return (which * kBatch + u) * 32 + lane; };
     uint4 raw[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if ((int)threadIdx.x + u * kThreads < vecs) raw[u] = __ldcs(src + threadIdx.x + u * kThreads);
+      if (vec_of(unit, u) < vecs) raw[u] = __ldcs(src + vec_of(unit, u));
 
     const bool tables = hist > 0 || p.bias_count > 0;
     if (tables) {
-      // padding (negative, or behind the vocabulary) is in no part
-      const auto mine = [&](int id) { return id >= 0 && (unsigned)(id - first) < (unsigned)n; };
       // the slot of token `at`, entered if it is new; -1 once the list is full
       const auto slot_of = [&](int at, bool& entered) {
         uint32_t i = first_slot(at);
@@ -278,46 +290,90 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
         }
         return -1;
       };
-      // f(slot, index in the list) for every id of the part: a warp packs its share's ids, then
-      // enters them with full warps
-      const auto enter = [&](const int32_t* ids, int total, const int (&head)[kIds], auto&& f) {
-        for (int k0 = threadIdx.x & ~31; k0 < total; k0 += kIds * kThreads) {
-          int id[kIds], packed = 0;
-          if (k0 < kThreads) {
-#pragma unroll
-            for (int u = 0; u < kIds; ++u) id[u] = k0 + lane + u * kThreads < total ? head[u] : -1;
-          } else {
-            load_ids<kThreads>(ids, k0 + lane, total, id);
+      // the first `total` of the queue into the table, by the first `threads` threads; `high`: of the bias entries
+      const auto enter = [&](int threads, int total, uint32_t high) {
+        for (int i0 = threadIdx.x & ~31; i0 < total; i0 += threads) {
+          bool entered = false;
+          int slot = -1;
+          float v = 0.f;
+          uint32_t word = 0xFFFFFFFFu;
+          if (i0 + lane < total) {
+            const uint32_t e = queue[i0 + lane];
+            const int at = (int)(e & 0x3FFFu);
+            v = load1(x + first + at);  // needed if the token is new; under way meanwhile
+            if (mask) word = __ldg(mask + ((first + at) >> 5)) >> (at & 31);
+            slot = slot_of(at, entered);
+            if (slot >= 0) {
+              const uint32_t what = e & kWhat;
+              if (what == kBias)
+                atomicMax(entry + slot, (high | e >> 16) + 1u);
+              else if (what == kPrompt)
+                atomicOr(count + slot, kSeen);
+              else
+                atomicAdd(count + slot, 1u);
+            }
           }
-          __syncwarp();  // the last round's queue has been read
+          const uint32_t fresh = __ballot_sync(0xffffffffu, entered);
+          if (fresh) {
+            int where = 0;
+            if (lane == 0) where = atomicAdd(&listed, __popc(fresh));
+            where = __shfl_sync(0xffffffffu, where, 0) + __popc(fresh & ((1u << lane) - 1));
+            if (entered && where < kList) {
+              list[where] = (uint16_t)(slot | (word & 1u ? kAllowed : 0u));
+              list_x[where] = v;
+            }
+          }
+        }
+      };
+      int room = kQueue, done = 0;  // ids that still fit in any case; those that are in the table
+      uint32_t high = 0;
+      // ids of the part into the queue, their tokens out of the stream's hands
+      const auto collect = [&](const int32_t* ids, int total, const int (&head)[kIds], bool biases) {
+        for (int k0 = 0; k0 < total; k0 += kRound) {
+          const bool turn = biases && (uint32_t)k0 >> 16 << 16 != high;
+          const int most = min(kRound, total - k0);
+          if (turn || room < most) {
+            __syncthreads();
+            const int waiting = queued;
+            __syncthreads();
+            room = kQueue - waiting;
+            if (turn || room < most) {
+              enter(kThreads, waiting, high);
+              done += waiting;
+              room = kQueue;
+              if (threadIdx.x == 0) queued = 0;
+              __syncthreads();
+            }
+            if (biases) high = (uint32_t)k0 >> 16 << 16;
+          }
+          room -= most;
+          int id[kIds], packed = 0;
+          if (k0 == 0) {
+#pragma unroll
+            for (int u = 0; u < kIds; ++u) id[u] = (int)threadIdx.x + u * kThreads < total ? head[u] : -1;
+          } else {
+            load_ids<kThreads>(ids, k0 + threadIdx.x, total, id);
+          }
+          // padding (negative, or behind the vocabulary) is in no part
+          uint32_t in[kIds];
 #pragma unroll
           for (int u = 0; u < kIds; ++u) {
-            const bool in = mine(id[u]);
-            const uint32_t all = __ballot_sync(0xffffffffu, in);
-            if (in) queue[warp][packed + __popc(all & ((1u << lane) - 1))] = (uint32_t)(id[u] - first) << 8 | (uint32_t)(u << 5 | lane);
-            packed += __popc(all);
+            in[u] = __ballot_sync(0xffffffffu, id[u] >= 0 && (unsigned)(id[u] - first) < (unsigned)n);
+            packed += __popc(in[u]);
           }
-          __syncwarp();
-          for (int i0 = 0; i0 < packed; i0 += 32) {
-            bool entered = false;
-            int slot = -1;
-            float v = 0.f;
-            if (i0 + lane < packed) {
-              const uint32_t e = queue[warp][i0 + lane];
-              v = load1(x + first + (e >> 8));  // needed if the token is new; under way meanwhile
-              slot = slot_of((int)(e >> 8), entered);
-              if (slot >= 0) f(slot, k0 + (int)(e & 31u) + (int)(e >> 5 & 7u) * kThreads);
+          if (packed == 0) continue;
+          int where = 0;
+          if (lane == 0) where = atomicAdd(&queued, packed);
+          where = __shfl_sync(0xffffffffu, where, 0);
+#pragma unroll
+          for (int u = 0; u < kIds; ++u) {
+            if (in[u] >> lane & 1u) {
+              const int at = id[u] - first, k = k0 + (int)threadIdx.x + u * kThreads;
+              queue[where + __popc(in[u] & ((1u << lane) - 1))] =
+                  (uint32_t)at | (biases ? kBias | (uint32_t)k << 16 : k < prompt ? kPrompt : 0u);
+              atomicAnd(allow + (at >> 5), ~(1u << (at & 31)));
             }
-            const uint32_t fresh = __ballot_sync(0xffffffffu, entered);
-            if (fresh) {
-              int where = 0;
-              if (lane == 0) where = atomicAdd(&listed, __popc(fresh));
-              where = __shfl_sync(0xffffffffu, where, 0) + __popc(fresh & ((1u << lane) - 1));
-              if (entered && where < kList) {
-                list[where] = (uint16_t)slot;
-                list_x[where] = v;
-              }
-            }
+            where += __popc(in[u]);
           }
         }
       };
@@ -330,45 +386,56 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
         reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4*>(entry)[i] = make_uint4(0, 0, 0, 0);
       }
-      if (threadIdx.x == 0) listed = 0;
-      __syncthreads();
-      if (p.bias_count > 0)
-        enter(bias_ids, p.bias_count, bias_id, [&](int slot, int k) { atomicMax(entry + slot, (uint32_t)k + 1u); });
-      enter(history, hist, hist_id, [&](int slot, int k) {
-        if (k < prompt)
-          atomicOr(count + slot, kSeen);
-        else
-          atomicAdd(count + slot, 1u);
-      });
-      __syncthreads();
-      if (listed >= kList && n > kList) {  // it may be incomplete: a smaller range
-        span = max(kList, ((n + 1) / 2 + 31) & ~31);
-        __syncthreads();
-        continue;
+      if (threadIdx.x == 0) {
+        listed = queued = 0;
+        next_unit = kWarps;
       }
-      for (int i = threadIdx.x; i < listed; i += kThreads) {
-        const int slot = list[i], at = (int)key[slot];
-        const float v = change(list_x[i], count[slot], entry[slot], r);
-        // out of the stream's hands; one that was masked out before stays -inf
-        const bool was = atomicAnd(allow + (at >> 5), ~(1u << (at & 31))) >> (at & 31) & 1u;
-        count[slot] = was ? (v != v ? 0x7FFFFFFFu : __float_as_uint(v)) : kMaskedBits;
+      __syncthreads();
+      if (p.bias_count > 0) collect(bias_ids, p.bias_count, bias_id, true);
+      collect(history, hist, hist_id, false);
+      __syncthreads();
+      const int waiting = queued;
+      // Some warps do the rest while the others stream -- unless the list may overflow, which has to
+      // be known first, or the stream writes over the logits that are needed here.
+      const bool apart = done + waiting <= kList && static_cast<const void*>(out) != static_cast<const void*>(x);
+      const int threads = apart ? kEnterWarps * 32 : kThreads;
+      if ((int)threadIdx.x < threads) {
+        enter(threads, waiting, high);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        if (listed >= kList && n > kList && !apart) {  // it may be incomplete: a smaller range
+          span = max(kList, ((n + 1) / 2 + 31) & ~31);
+          __syncthreads();
+          continue;
+        }
+        for (int i = threadIdx.x; i < listed; i += threads) {
+          const uint32_t e = list[i], slot = e & (kSlots - 1);
+          const float v = change(list_x[i], count[slot], entry[slot], r);
+          count[slot] = !(e & kAllowed) ? kMaskedBits : v != v ? 0x7FFFFFFFu : __float_as_uint(v);
+        }
       }
+    } else if (bits) {
+      __syncthreads();
     }
-    if (bits) __syncthreads();
 
-    // Whole batches have no branch inside, so that their tests and loads overlap; a thread's ids
+    // Whole units have no branch inside, so that their tests and loads overlap; a thread's ids
     // ascend, so of equal values the first stands.
-    for (int k0 = threadIdx.x; k0 < vecs; k0 += kBatch * kThreads) {
+    while (unit * (kBatch * 32) < vecs) {
+      int next = unit + kWarps;
+      if (tables) {  // not all warps began at the same time
+        if (lane == 0) next = atomicAdd(&next_unit, 1);
+        next = __shfl_sync(0xffffffffu, next, 0);
+      }
       uint32_t allowed[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + u * kThreads;
+        const int k = vec_of(unit, u);
         allowed[u] = 0;
         if (k < vecs) allowed[u] = (bits ? allow[N * k >> 5] >> (N * k & 31) : 0xFFu) & ((1u << N) - 1);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + u * kThreads;
+        const int k = vec_of(unit, u);
         float v[N];
         widen(raw[u], v, (const T*)nullptr);
 #pragma unroll
@@ -386,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
           for (int e = 0; e < N; e += 4)
             __stcs(reinterpret_cast<float4*>(out + first + N * k + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
         }
-        const int next = k + kBatch * kThreads;
-        if (next < vecs) raw[u] = __ldcs(src + next);
+        if (vec_of(next, u) < vecs) raw[u] = __ldcs(src + vec_of(next, u));
       }
+      unit = next;
     }
     const auto single = [&](int k, bool& can) {
       can = !bits || ((allow[k >> 5] >> (k & 31)) & 1u);
@@ -406,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
     if (tables) {
       __syncthreads();  // the stream has written its -inf
       for (int i = threadIdx.x; i < listed; i += kThreads) {
-        const int slot = list[i], id = first + (int)key[slot];
+        const int slot = list[i] & (kSlots - 1), id = first + (int)key[slot];
         const uint32_t value = count[slot];
         if (value != kMaskedBits) take(__uint_as_float(value), id, bv, bi);
         if (out) out[id] = value != kMaskedBits ? __uint_as_float(value) : -INFINITY;
@@ -431,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
   best_of_warp(top, id);
   if (lane == 0) best[warp] = make_uint2(top, id);
   __syncthreads();
-  cluster.barrier_wait();  // every CTA of the cluster has started
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
   if (!p.ids) return;
   if (warp == 0) {
     const uint2 w = lane < kThreads / 32 ? best[lane] : make_uint2(0u, 0xFFFFFFFFu);

@@ -96,6 +96,30 @@ def test_more_changed_tokens_than_a_pass_holds(lib, cuda_device, dtype, vocab, h
     assert np.array_equal(got[sub], want)
 
 
+@pytest.mark.parametrize("rows", [2, 80])
+@pytest.mark.parametrize("hist,bias,distinct", [(9000, 0, 40), (2500, 1500, 900), (700, 131200, 300), (5, 66000, 2400)])
+def test_long_lists_of_few_tokens(lib, cuda_device, rows, hist, bias, distinct):
+    """Lists far longer than what is entered at a time, of tokens of one part;
+    a bias entry's number needs more than 16 bits."""
+    c = case(rows, rows, 20011, hist, bias)
+    g = np.random.default_rng(rows + distinct)
+    some = np.sort(g.permutation(2500)[:distinct]).astype(np.int32)     # one CTA's tokens
+    c["history"] = some[g.integers(0, distinct, c["history"].shape)]
+    c["history_lens"] = np.full(rows, hist, np.int32)
+    if bias:
+        c["bias_ids"] = some[g.integers(0, distinct, c["bias_ids"].shape)]
+        c["bias_ids"][:, 65530:65540] = 19999                           # beside the 2^16th entry, in the last part
+    run(lib, cuda_device, c, NAMES)
+    x = c["x"].to(cuda_device)
+    run(lib, cuda_device, dict(c, x=x), NAMES, out=None)
+    put = {("allow_mask" if n == "mask" else n): torch.from_numpy(c[n]).to(cuda_device) for n in NAMES if n in c}
+    other = torch.empty_like(x)
+    ids = lib.process_logits(x, out=other, **put)
+    same = x.clone()
+    assert torch.equal(lib.process_logits(same, out=same, **put), ids)
+    assert torch.equal(same.view(torch.int32), other.view(torch.int32))
+
+
 def test_large_vocabulary(lib, cuda_device):
     """Over 8 x 16384 tokens the parts go in passes; the last one is ragged."""
     c = case(7, 2, 300001, 500, 50)
