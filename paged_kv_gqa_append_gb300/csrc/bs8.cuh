@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "pkv.h"
+#include "ptx.cuh"
 
 namespace pkv {
 
@@ -46,41 +47,31 @@ __device__ __noinline__ uint2 bs8_encode8_exact(float x0, float x1, float x2, fl
   return make_uint2(lo, hi);
 }
 
-// The codes of four products x * inv, unclamped (|x * inv| stays below 128 or
-// saturates): adding 1.5 * 2^23 rounds the exact product to the nearest even
+// Eight codes of bf16 values |x| <= top * scale without divisions, inv = 1 / scale
+// rounded: the quotient from the product x * inv, its remainder and one correction
+// (Markstein's, IBM J. Res. Dev. 34, 1990).  With 8-bit significands of x it equals
+// the IEEE quotient beside every point where a code changes, for all 2^23
+// significands of the scale; the scale is in [2^-100, 2^100], so that nothing that
+// a code depends on underflows.  Adding 1.5 * 2^23 rounds to the nearest even
 // integer in the low bits.
 template <bool kE4m3>
-__device__ __forceinline__ uint32_t bs8_round4(const float* x, float inv) {
-  if (kE4m3) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
+__device__ __forceinline__ uint2 bs8_encode8(const float2 (&x)[4], float scale, float inv) {
+  const float2 s = make_float2(-scale, -scale), v = make_float2(inv, inv);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 q = mul2(x[e], v);
+    q = fma2(fma2(q, s, x[e]), v, q);
+    if (kE4m3) {
+      w[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    } else {
+      const float2 r = add2(q, make_float2(12582912.f, 12582912.f));
+      w[e] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x0040);
+    }
   }
-  constexpr float kRound = 12582912.f;
-  const uint32_t a = __byte_perm(__float_as_uint(fmaf(x[0], inv, kRound)), __float_as_uint(fmaf(x[1], inv, kRound)), 0x0040);
-  const uint32_t b = __byte_perm(__float_as_uint(fmaf(x[2], inv, kRound)), __float_as_uint(fmaf(x[3], inv, kRound)), 0x0040);
-  return __byte_perm(a, b, 0x5410);
+  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
-
-// The codes of |x| <= top * scale without 32 divisions: a quotient lies between
-// x * inv (1 - 2^-21) and x * inv (1 + 2^-21), with inv = 1 / scale rounded; where
-// both give the same codes (rounding is monotonic) they are the quotients', and
-// elsewhere -- one value in about 10^4 -- the divisions are done.
-struct Bs8Inverse {
-  float lo, hi;  // 0: no short way (scale 0 or near the subnormals)
-};
-__device__ __forceinline__ Bs8Inverse bs8_inverse(float scale) {
-  if (!(scale > 7.9e-31f && scale < 1e30f)) return {0.f, 0.f};  // 2^-100 .. 2^100
-  const float inv = __frcp_rn(scale);
-  return {inv * (1.f - 4.76837158203125e-7f), inv * (1.f + 4.76837158203125e-7f)};
-}
-template <bool kE4m3>
-__device__ __forceinline__ uint2 bs8_encode8(const float (&x)[8], float scale, Bs8Inverse inv) {
-  const uint2 a = make_uint2(bs8_round4<kE4m3>(x, inv.lo), bs8_round4<kE4m3>(x + 4, inv.lo));
-  const uint2 b = make_uint2(bs8_round4<kE4m3>(x, inv.hi), bs8_round4<kE4m3>(x + 4, inv.hi));
-  if (a.x == b.x && a.y == b.y && inv.lo > 0.f) return a;
-  return bs8_encode8_exact<kE4m3>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], scale);
-}
+__device__ __forceinline__ bool bs8_has_inverse(float scale) { return scale > 7.9e-31f && scale < 1e30f; }
 
 template <bool kE4m3>
 __device__ __forceinline__ void bs8_decode8(uint2 u, float (&x)[8]) {

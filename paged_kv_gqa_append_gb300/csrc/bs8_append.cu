@@ -19,8 +19,8 @@
 // that neither waits for the other.
 //
 // Bound: memory, 3 KiB per token for K and V, and 8 KiB for q.  Codes without a
-// division per value (bs8.cuh) and rotations without shuffles took 14400 tokens
-// of eight prompts from 65 us to 33 us.  A step of few tokens is latency: the
+// division per value (bs8.cuh), rotations without shuffles and products by pairs
+// took 14400 tokens of eight prompts from 65 us to 31 us (K and V alone 13 us).  A step of few tokens is latency: the
 // token's place (without a search where a step has one token per sequence; else
 // one round of a 32-way search for up to 1023 sequences), then the table entry,
 // the rows and the rotations together, then the old scale.
@@ -111,14 +111,17 @@ __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
 }
 
 // Four dims and their partners rotated in place, in kv_append_rope's order of
-// operations: x[0 .. 3] with x[4 .. 7].
-__device__ __forceinline__ void rotate8(float (&x)[8], const float4& c4, const float4& s4) {
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+// operations: x[0], x[1] with x[2], x[3].
+__device__ __forceinline__ void rotate8(float2 (&x)[4], const float4& c4, const float4& s4) {
+  const float2 c[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+  const float2 s[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float a = x[e], b = x[e + 4];
-    x[e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-    x[e + 4] = __fadd_rn(__fmul_rn(a, s[e]), __fmul_rn(b, c[e]));
+  for (int e = 0; e < 2; ++e) {
+    const float2 a = x[e], b = x[e + 2];
+    // (each product and each sum rounded: mul2 with add2 would not do)
+    const float2 ac = mul2(a, c[e]), bs = mul2(b, s[e]), as = mul2(a, s[e]), bc = mul2(b, c[e]);
+    x[e] = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
+    x[e + 2] = make_float2(__fadd_rn(as.x, bc.x), __fadd_rn(as.y, bc.y));
   }
 }
 
@@ -128,16 +131,14 @@ __device__ __forceinline__ uint4 load_halves(const uint16_t* row, int j) {
   const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + 32 + 4 * j));
   return make_uint4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ void widen8(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void widen8(const uint4& u, float2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = bf16lo_to_f32(w[e]);
-    x[2 * e + 1] = bf16hi_to_f32(w[e]);
-  }
+  for (int e = 0; e < 4; ++e) x[e] = make_float2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
 }
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const float2 (&x)[4]) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                    pack_bf16x2(x[3].x, x[3].y));
 }
 
 // K (kv = 0) or V rows of one head of a run: slots [slot, slot + n) of the page
@@ -182,7 +183,8 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
   if (turn) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x[8];
+      if (4 * i + 4 <= slot || 4 * i >= slot + n) continue;  // none of the warp's four rows
+      float2 x[4];
       widen8(raw[i], x);
       rotate8(x, c[i], s[i]);
       raw[i] = narrow8(x);
@@ -202,25 +204,33 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
   const bool grown = slot > 0 && fresh > old;
   const float now = slot == 0 || grown ? fresh : old;
   if (lane == 0 && (slot == 0 || grown)) *scale = now;
-  const Bs8Inverse inv = bs8_inverse(now);
+  const auto write = [&](int r, const uint2& codes) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(block + r * kRow + 4 * j);
+    to[0] = codes.x;
+    to[8] = codes.y;
+  };
+  const bool by_inverse = bs8_has_inverse(now);
+  const float inv = by_inverse ? __frcp_rn(now) : 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * i + sub;
-    uint32_t* lo = reinterpret_cast<uint32_t*>(block + r * kRow + 4 * j);
-    uint32_t* hi = lo + 32 / 4;
-    float x[8];
-    if (r >= slot && r < slot + n) {
-      widen8(raw[i], x);
-      const uint2 codes = bs8_encode8<kE4m3>(x, now, inv);
-      *lo = codes.x;
-      *hi = codes.y;
-    } else if (r < slot && grown) {
-      bs8_decode8<kE4m3>(make_uint2(*lo, *hi), x);
+    if (4 * i + 4 <= slot || 4 * i >= slot + n) continue;
+    float2 x[4];
+    widen8(raw[i], x);
+    const uint2 codes = by_inverse ? bs8_encode8<kE4m3>(x, now, inv)
+                                   : bs8_encode8_exact<kE4m3>(x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x,
+                                                              x[3].y, now);
+    if (r >= slot && r < slot + n) write(r, codes);
+  }
+  if (grown) {
+#pragma unroll 1
+    for (int r = sub; r < slot; r += 4) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(block + r * kRow + 4 * j);
+      float x[8];
+      bs8_decode8<kE4m3>(make_uint2(from[0], from[8]), x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], old);
-      const uint2 codes = bs8_encode8_exact<kE4m3>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], now);
-      *lo = codes.x;
-      *hi = codes.y;
+      write(r, bs8_encode8_exact<kE4m3>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], now));
     }
   }
 }
@@ -229,12 +239,13 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
 template <bool kE4m3>
 __device__ __forceinline__ void append_chunk(const Bs8AppendParams& p, int t0, int t1) {
   const int warp = threadIdx.x >> 5;
+  Place a = place_of(p, t0);
   for (int t = t0; t < t1;) {
-    const Place a = place_of(p, t);
     if (!a.live) break;
     if (!a.ok) {
       if (threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
       t = max(t + 1, min(a.end, t1));
+      if (t < t1) a = place_of(p, t);
       continue;
     }
     const int slot = a.pos % PKV_PAGE_TOKENS;
@@ -243,6 +254,12 @@ __device__ __forceinline__ void append_chunk(const Bs8AppendParams& p, int t0, i
       append_run<kE4m3>(p, t, a.pos, n, p.block_tables + (size_t)a.seq * p.bt_stride + a.pos / PKV_PAGE_TOKENS,
                         warp >> 3, warp & 7);
     t += n;
+    if (t < a.end) {  // the same sequence's next page
+      a.pos += n;
+      a.first = false;
+    } else if (t < t1) {
+      a = place_of(p, t);
+    }
   }
 }
 
@@ -277,7 +294,7 @@ __device__ __forceinline__ void rotate_chunk(const Bs8AppendParams& p, int t0, i
     uint16_t* dst = p.q_out + ((size_t)t * PKV_NUM_Q_HEADS + (many ? 4 * u : 4 * warp) + sub) * kRow;
     uint4 res = make_uint4(0, 0, 0, 0);
     if (ok) {
-      float x[8];
+      float2 x[4];
       widen8(raw[u], x);
       rotate8(x, c, s);
       res = narrow8(x);

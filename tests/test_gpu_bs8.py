@@ -158,6 +158,33 @@ def test_append_zero_and_extreme_rows(lib, cuda_device, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_append_values_where_a_code_changes(lib, cuda_device, kind):
+    """Quotients at and beside the middle between two codes, the tie itself among
+    them, under scales of many significands and exponents."""
+    pages = 24
+    g = np.random.default_rng(71)
+    amax = np.ldexp(1 + g.integers(0, 128, (pages, 2, 8)) / 128, g.integers(-90, 90, (pages, 2, 8))).astype(np.float32)
+    top = np.float32(127 if kind == "int8" else 448)
+    scale = (amax / top).astype(np.float64)
+    if kind == "int8":
+        middle = np.arange(127) + 0.5
+    else:
+        middle = (16 + np.arange(16)) / 16 * 2.0 ** np.arange(-10, 9)[:, None]
+        middle = middle[(middle < 448)].ravel()
+    at = g.choice(middle, (pages, 2, 8, 16, 64)) * scale[..., None, None]
+    x = ((at.astype(np.float32).view(np.uint32) >> 16).astype(np.int64) + g.integers(-1, 3, at.shape)).astype(np.uint16)
+    x |= (g.integers(0, 2, x.shape) << 15).astype(np.uint16)
+    big = np.abs(OB.to_f64(x)) > amax[..., None, None]
+    x[big] = 0
+    x[:, :, :, 5, 7] = amax.view(np.uint32) >> 16                       # the block's largest, exactly
+    rows_of = x.transpose(1, 0, 3, 2, 4).reshape(2, pages * 16, 8, 64)
+    bt = g.permutation(pages).astype(np.int32)[None]
+    codes, scales = np.zeros((pages, 2, 8, 16, 64), np.uint8), np.zeros((pages, 2, 8), np.float32)
+    n = pages * 16
+    check_append(lib, cuda_device, kind, codes, scales, rows_of[0], rows_of[1], [0, n], [n], bt)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_append_bad_sequences_are_skipped(lib, cuda_device, tables, kind):
     codes, scales = random_pages(10, 6, kind)
     k, v, q = rows(11, 60, 8, 64), rows(12, 60, 8, 64), rows(13, 60, 32, 64)
