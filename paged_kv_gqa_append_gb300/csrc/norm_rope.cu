@@ -24,10 +24,12 @@
 //
 // Bound: memory.  A token moves 12 KiB (32 + 8 + 8 rows read and written)
 // and one table row.  24 warps per SM (80 registers) keep 144 KB in flight;
-// with 16 warps 32768 tokens take 87 us, not 74.  With 16 contiguous bytes per
+// with 16 warps 32768 tokens took 87 us, not 74.  With 16 contiguous bytes per
 // lane and the partners fetched by shuffles, and three warps per token, they
 // took 131 us: 2450 instructions a token, half of the issue slots; with two
-// 16-byte loads per lane and four lanes per row, 79 us.  Interleaved pairs: 68 us.
+// 16-byte loads per lane and four lanes per row, 79 us.  With later rows on their
+// way into the L2 they take 67.7 us (89 % of the measured copy rate), interleaved
+// pairs 63.8 us, the layouts through the row buffer 100 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -275,12 +277,12 @@ __global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_ro
 }
 
 // Where one warp per token has enough warps to fill the GPU (about 16 on each
-// SM): 32768 tokens take 74 us whole and 100 us in parts, 2432 tokens 7.6 and
+// SM): 32768 tokens take 68 us whole and 100 us in parts, 2432 tokens 7.6 and
 // 7.8 us; 257 tokens take 4.0 us whole and 3.1 us in parts, one token 3.6 and
 // 2.7 us.
 constexpr int kWholeTokensPerSm = 16;
 // A warp fetches the rows half a wave behind its own into the L2: 32768 tokens
-// 68.9 us, without 75.6 us; 6, 24 and 36 tokens per SM ahead 69.7, 69.9 and 73.2 us.
+// 67.7 us, without 75.6 us; 6, 24 and 36 tokens per SM ahead take 0.8, 1 and 4 us more.
 constexpr int kAheadPerSm = 12;
 
 template <int kLayout>
