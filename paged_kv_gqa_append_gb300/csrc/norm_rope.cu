@@ -29,7 +29,7 @@
 // took 131 us: 2450 instructions a token, half of the issue slots; with two
 // 16-byte loads per lane and four lanes per row, 79 us.  With later rows on their
 // way into the L2 they take 67.7 us (89 % of the measured copy rate), interleaved
-// pairs 63.8 us, the layouts through the row buffer 100 us.
+// pairs 63.8 us, the layouts through the row buffer 80.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -196,6 +196,16 @@ __global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_ro
       }
     }
   }
+  const auto row_of = [](int d) { return d + 4 * (d >> 5); };
+  int partner[kTab];  // any half layout: where the other dim of each pair is; s gets its sign
+  if (kLayout == kHalfAny) {
+#pragma unroll
+    for (int e = 0; e < kTab; ++e) {
+      const int d = 8 * j + e;
+      partner[e] = row_of(d < p.pairs ? d + p.pairs : d < 2 * p.pairs ? d - p.pairs : d);
+      if (d < p.pairs) s[e] = -s[e];
+    }
+  }
   const auto load_weights = [&](const void* weight, float (&w)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -244,18 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32, kWhole ? 24 / kWarps : 1) norm_ro
       }
     } else {
       float* buf = rows[warp][sub];
-      const auto at = [](int d) { return d + 4 * (d >> 5); };
 #pragma unroll
-      for (int e = 0; e < 8; ++e) buf[at(8 * j) + e] = x[e];
+      for (int e = 0; e < 8; ++e) buf[row_of(8 * j) + e] = x[e];
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int d = 8 * j + e;
-        const bool first = d < p.pairs, in = d < 2 * p.pairs;
-        const float b = buf[at(first ? d + p.pairs : in ? d - p.pairs : d)];
-        const float xc = __fmul_rn(x[e], c[e]), bs = __fmul_rn(b, s[e]);
-        // first half: a c - b s; second half (x is the pair's b, b its a): a s + b c
-        y[e] = !in ? x[e] : first ? __fsub_rn(xc, bs) : __fadd_rn(bs, xc);
+        // a c + b (-s) in the first half; in the second x is the pair's b, and its a is multiplied by s
+        const float turned_e = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(buf[partner[e]], s[e]));
+        y[e] = 8 * j + e < 2 * p.pairs ? turned_e : x[e];
       }
       __syncwarp();  // the next group writes the buffer again
     }
