@@ -47,25 +47,30 @@ __device__ __noinline__ uint2 bs8_encode8_exact(float x0, float x1, float x2, fl
   return make_uint2(lo, hi);
 }
 
-// Eight codes of bf16 values |x| <= top * scale without divisions, inv = 1 / scale
-// rounded: the quotient from the product x * inv, its remainder and one correction
-// (Markstein's, IBM J. Res. Dev. 34, 1990).  With 8-bit significands of x it equals
-// the IEEE quotient beside every point where a code changes, for all 2^23
-// significands of the scale; the scale is in [2^-100, 2^100], so that nothing that
-// a code depends on underflows.  Adding 1.5 * 2^23 rounds to the nearest even
-// integer in the low bits.
-template <bool kE4m3>
+// Eight codes of values |x| <= top * scale without divisions, inv = 1 / scale
+// rounded: the quotient from the product x * inv by corrections with its remainder
+// (Markstein, IBM J. Res. Dev. 34, 1990).  A second one makes any quotient the IEEE
+// one, the first having brought it within a unit in the last place.  For bf16
+// values one is enough: with their 8-bit significands it equals the IEEE quotient
+// beside every point where a code changes, for all 2^23 significands of the scale.
+// The scale is in [2^-100, 2^100], so that nothing that a code depends on
+// underflows.  The remainder is taken as q * scale - x: -0 stays -0.  Adding
+// 1.5 * 2^23 rounds to the nearest even integer in the low bits.
+// kAny: values of codes held before, which also may be -128.
+template <bool kE4m3, bool kAny = false>
 __device__ __forceinline__ uint2 bs8_encode8(const float2 (&x)[4], float scale, float inv) {
-  const float2 s = make_float2(-scale, -scale), v = make_float2(inv, inv);
+  const float2 s = make_float2(scale, scale), v = make_float2(inv, inv), minus = make_float2(-inv, -inv);
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float2 q = mul2(x[e], v);
-    q = fma2(fma2(q, s, x[e]), v, q);
+#pragma unroll
+    for (int c = 0; c < (kAny ? 2 : 1); ++c) q = fma2(fma2(q, s, make_float2(-x[e].x, -x[e].y)), minus, q);
     if (kE4m3) {
       w[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
     } else {
-      const float2 r = add2(q, make_float2(12582912.f, 12582912.f));
+      float2 r = add2(q, make_float2(12582912.f, 12582912.f));
+      if (kAny) r = make_float2(fmaxf(r.x, 12582785.f), fmaxf(r.y, 12582785.f));
       w[e] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x0040);
     }
   }

@@ -185,6 +185,19 @@ def test_append_values_where_a_code_changes(lib, cuda_device, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_append_zeros_of_both_signs(lib, cuda_device, tables, kind):
+    k, v, q = rows(73, 40, 8, 64), rows(74, 40, 8, 64), rows(75, 40, 32, 64)
+    for x in (k, v, q):
+        x[:, :, ::3] = 0x8000
+        x[::7] = 0
+        x[1::7] = 0x8000
+    codes, scales = random_pages(76, 8, kind)
+    bt = np.array([[3, 0, 5], [1, 7, 2]], np.int32)
+    for rope in (None, tables):
+        check_append(lib, cuda_device, kind, codes, scales, k, v, [0, 23, 40], [30, 17], bt, rope, None if rope is None else q)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_append_bad_sequences_are_skipped(lib, cuda_device, tables, kind):
     codes, scales = random_pages(10, 6, kind)
     k, v, q = rows(11, 60, 8, 64), rows(12, 60, 8, 64), rows(13, 60, 32, 64)
