@@ -9,9 +9,9 @@
 // four scores and its finished P V product, and the codes themselves enter
 // the MMAs.
 //
-// Work: the pages of all sequences, one after another, are one long list;
-// every CTA takes an equal share of it (an even number of pages), whatever
-// the lengths.  A share that ends inside a sequence leaves a partial (o, m, l)
+// Work: sequences that are short by the caller's bound have a CTA each.  Else the
+// pages of all sequences, one after another, are one long list; every CTA takes an
+// equal share of it (an even number of pages), whatever the lengths.  A share that ends inside a sequence leaves a partial (o, m, l)
 // in the workspace, and a second kernel merges the parts of such sequences.
 // One CTA is a producer warp and 8 consumer warps, one per KV head: the
 // producer copies whole pages -- 16 KiB, all heads, one TMA box each -- into a
@@ -41,6 +41,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -63,10 +64,16 @@ constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + kStagePages * kScaleB
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxSeqsBs8 = 4096;
 constexpr int kMinPages = 4;                            // least share of a CTA
+// Short sequences stay whole, one CTA's each: nothing to merge, nothing to add up
+// first.  Short is up to 8 pages, and one more per 8 sequences up to 24: one
+// sequence of 8 pages takes 6.5 us, by shares 6.9 us, of 12 pages 8.0 and 6.8 us; 64
+// of 16 pages 10.1 and 9.2 us (ragged 9.9 and 11.6 us), of 24 pages 13.4 and 10.6 us;
+// 152 of 24 pages 16.2 and 22.2 us; 1000 ragged ones to 24 pages 52 and 51 us.
+constexpr int kWholePages = 8, kWholePagesMost = 24;
 // Up to this many sequences the merge looks at every sequence; beyond it at every
 // CTA, in each of which one split sequence begins at most (4096 sequences of 64
-// tokens: 67 us, by sequence 107 us; 256 of 2048: 99 and 105 us; 97 mixed ones:
-// 75.5 and 74 us).
+// tokens in shares: 67 us, by sequence 107 us; 256 of 2048: 99 and 105 us; 97 mixed
+// ones: 75.5 and 74 us).
 constexpr int kBySequence = 128;
 constexpr uint32_t kWaitUs = 2000000;                   // limit of every wait
 constexpr float kLift = 14.f;                           // probabilities carry 2^14
@@ -361,7 +368,7 @@ struct Head {  // a consumer's state for one segment
   }
 };
 
-template <bool kE4m3>
+template <bool kE4m3, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const __grid_constant__ CUtensorMap map,
                                                                           const Bs8DecodeParams p) {
   extern __shared__ uint8_t dyn[];
@@ -390,6 +397,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
     begin = (int)min((unsigned)total, share * blockIdx.x);
     end = min(total, begin + (int)share);
   };
+  const auto nothing = [&](int s, bool refused) {  // the rows of a sequence with nothing to read
+    uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
+    for (int i = 0; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+    if (refused) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+  };
   // Which CTAs share sequence s, whose n pages begin at `at` (unless every CTA says so itself), and
   // the rows of one with nothing to read: written by one CTA for each sequence, while the producer is
   // under way already.
@@ -399,13 +411,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       const int c0 = (int)((unsigned)at / share), c1 = n ? (int)((unsigned)(at + n - 1) / share) : c0;
       p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
     }
-    if (n == 0) {
-      uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
-      for (int i = 0; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
-      if (refused) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
-    }
+    if (n == 0) nothing(s, refused);
   };
-  if (p.num_seqs <= 32) {  // every warp finds out by itself, without a barrier (0.2 us less)
+  const int hop = kWhole ? (int)gridDim.x : 1;  // from one of the CTA's sequences to its next
+  if (kWhole) {
+    pdl_launch_dependents();
+    begin = page = share = 0;
+    end = INT_MAX;
+    bool refused;
+    for (seq = blockIdx.x; seq < p.num_seqs && pages_of(p, seq, refused) == 0;) seq += hop;
+    for (int s = blockIdx.x + (int)threadIdx.x * hop; s < p.num_seqs; s += kThreads * hop)
+      if (pages_of(p, s, refused) == 0) nothing(s, refused);
+    __syncwarp();
+  } else if (p.num_seqs <= 32) {  // every warp finds out by itself, without a barrier (0.2 us less)
     bool refused = false;
     const int n = lane < p.num_seqs ? pages_of(p, lane, refused) : 0;
     int run = n;
@@ -468,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       at += n;
     }
   }
-  if (begin >= end) {
+  if (kWhole ? seq >= p.num_seqs : begin >= end) {
     if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = make_int2(-1, -1);
     return;
   }
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   if (warp == kConsumers) {  // producer
     bool alive = true;
     int filled = 0;
-    while (at < end && alive) {
+    while ((kWhole ? seq < p.num_seqs : at < end) && alive) {
       bool refused;
       const int pages = pages_of(p, seq, refused);
       const int todo = min(pages - page, end - at);
@@ -521,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
       }
       at += todo;
       page = 0;
-      ++seq;
-      while (at < end && seq < p.num_seqs && pages_of(p, seq, refused) == 0) ++seq;
+      seq += hop;
+      while (at < end && seq < p.num_seqs && pages_of(p, seq, refused) == 0) seq += hop;
     }
     if (!alive) {  // every copy in flight lands before the CTA's shared memory goes
       if (lane == 0) {
@@ -543,14 +561,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bs8_decode_kernel(const 
   bool refused;
   int pages = pages_of(p, seq, refused);
   auto q = Head<kE4m3>::fetch(p, seq, head);
-  while (at < end && alive) {
+  while ((kWhole ? seq < p.num_seqs : at < end) && alive) {
     const int len = __ldg(p.seq_lens + seq);
     const int todo = min(pages - page, end - at);
     st.start(p, q);
     // the next sequence, and its q under way while this one is worked on
-    int next = seq + 1, next_pages = 0;
+    int next = seq + hop, next_pages = 0;
     if (at + todo < end) {
-      while (next < p.num_seqs && (next_pages = pages_of(p, next, refused)) == 0) ++next;
+      while (next < p.num_seqs && (next_pages = pages_of(p, next, refused)) == 0) next += hop;
       if (next < p.num_seqs) q = Head<kE4m3>::fetch(p, next, head);
     }
     bool bad = false;
@@ -795,23 +813,17 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   p.max_blocks = max_blocks;
   p.num_seqs = num_seqs;
   p.min_pages = kMinPages;
-  p.by_cta = num_seqs > kBySequence;
 
   CUtensorMap map;
   rc = make_bs8_map(&map, kv_pool, num_pages);
   if (rc != PKV_OK) return rc;
   const bool e4m3 = code_type == PKV_BS8_E4M3;
-  rc = cuda_status(e4m3 ? cudaFuncSetAttribute(bs8_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemBytes)
-                        : cudaFuncSetAttribute(bs8_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemBytes),
-                   "cudaFuncSetAttribute(decode bs8)");
-  if (rc != PKV_OK) return rc;
-
   // no more CTAs than the length bound can give work to (the shares follow the actual lengths)
   const long long longest = max_seq_len > 0 ? max_seq_len : (long long)max_blocks * PKV_PAGE_TOKENS;
-  const long long most = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS * num_seqs;
-  long long ctas = (most + kMinPages - 1) / kMinPages;
+  const long long most_pages = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
+  const bool whole = most_pages <= (num_seqs < 8 * (kWholePagesMost - kWholePages) ? kWholePages + num_seqs / 8 : kWholePagesMost);
+  p.by_cta = !whole && num_seqs > kBySequence;
+  long long ctas = whole ? num_seqs : (most_pages * num_seqs + kMinPages - 1) / kMinPages;
   if (ctas > (long long)sms * kCtasPerSm) ctas = (long long)sms * kCtasPerSm;
   if (ctas < 1) ctas = 1;
   cudaLaunchAttribute attr[1];
@@ -824,10 +836,13 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  rc = cuda_status(e4m3 ? cudaLaunchKernelEx(&cfg, bs8_decode_kernel<true>, map, p)
-                        : cudaLaunchKernelEx(&cfg, bs8_decode_kernel<false>, map, p),
-                   "cudaLaunchKernelEx(decode bs8)");
-  if (rc != PKV_OK || ctas == 1) return rc;  // one CTA splits nothing
+  auto* decode = e4m3 ? (whole ? bs8_decode_kernel<true, true> : bs8_decode_kernel<true, false>)
+                      : (whole ? bs8_decode_kernel<false, true> : bs8_decode_kernel<false, false>);
+  rc = cuda_status(cudaFuncSetAttribute(decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
+                   "cudaFuncSetAttribute(decode bs8)");
+  if (rc != PKV_OK) return rc;
+  rc = cuda_status(cudaLaunchKernelEx(&cfg, decode, map, p), "cudaLaunchKernelEx(decode bs8)");
+  if (rc != PKV_OK || ctas == 1 || whole) return rc;  // one CTA splits nothing
   const int heads = num_seqs <= 8 ? 1 : num_seqs * 4 <= sms ? 8 : 16;
   const long long items = p.by_cta ? ctas - 1 : num_seqs;  // nothing goes on behind the last CTA
   cfg.gridDim = dim3((unsigned)(items * (PKV_NUM_Q_HEADS / heads)));

@@ -435,6 +435,29 @@ def test_decode_many_sequences_long_short_empty_and_bad(lib, cuda_device, kind, 
     close(out[good], *O8.attend(q[good], codes, scales, bt[good], lens[good], 0.125, kind), lens[good])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("S,bound", [(5, 64), (70, 128), (700, 64), (700, 384), (700, 400)])
+def test_decode_short_by_the_bound(lib, cuda_device, kind, S, bound):
+    """Whole sequences per CTA or shares, by the bound alone; lengths beyond it, empty
+    and bad sequences among them."""
+    g = np.random.default_rng(80 + S)
+    lens = g.integers(0, bound, S)
+    lens[g.permutation(S)[:S // 2]] = g.integers(0, 3, S // 2)
+    lens[[0, S // 2, S - 1]] = 0, bound + 37, 700
+    pages = int(sum(-(-n // 16) for n in lens)) + 1
+    codes, scales = random_pages(81, pages, kind)
+    bt = tables_for(82, lens, pages)
+    q = rows(83, S, 32, 64)
+    out = check_decode(lib, cuda_device, kind, q, codes, scales, bt, lens, max_seq_len=bound)
+    assert (out[lens == 0] == 0).all()
+    lens[[1, 3]] = -5, bt.shape[1] * 16 + 1
+    bt[S - 1, 20], bad = -1, [1, 3, S - 1]
+    out, code = decode(lib, cuda_device, kind, q, codes, scales, bt, lens, max_seq_len=bound)
+    assert code == lib.ERR_DEVICE_INDEX and (out[bad] == 0).all()
+    good = np.setdiff1d(np.arange(S), bad)
+    close(out[good], *O8.attend(q[good], codes, scales, bt[good], lens[good], 0.125, kind), lens[good])
+
+
 def test_decode_largest_batch_and_page_order(lib, cuda_device):
     S = 4096
     lens = np.random.default_rng(42).integers(0, 20, S).astype(np.int32)
