@@ -728,7 +728,7 @@ int pkv_argmax_f32(const float* logits, int rows, int vocab, long long row_strid
  *                 outside [0, vocab) are padding; unused with bias_count 0
  *   allow_mask    device uint32 [rows][mask_stride] or NULL, mask_stride >=
  *                 ceil(vocab / 32)
- * One cluster of 8 CTAs per row; deterministic.  Host-side checks only.
+ * One cluster of up to 8 CTAs per row; deterministic.  Host-side checks only.
  * ---------------------------------------------------------------------- */
 #define PKV_LOGITS_F32 0
 #define PKV_LOGITS_BF16 1

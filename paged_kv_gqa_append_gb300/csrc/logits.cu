@@ -10,17 +10,16 @@
 // and the id chosen is the first of the largest non-NaN x among the tokens
 // that the mask leaves, -1 if there is none.
 //
-// A cluster of 8 CTAs handles a row, each a contiguous eighth of the
+// A cluster of up to 8 CTAs handles a row, each a contiguous part of the
 // vocabulary (a multiple of 32 tokens, one mask word).  The tokens that steps 1
 // to 3 change are few, so they are worked out first: a CTA reads the row's whole
 // history and bias list (from L2) and keeps those of its part in a hash table in
 // shared memory -- open addressing, 2048 slots, at most about half of them used
 // -- with how often a token was generated, whether it was seen at all, and its
-// last bias entry.  All warps first queue the ids that are in the part (an
-// eighth, on average) and take their tokens out of the bitmap of those that the
+// last bias entry.  All warps first queue the ids that are in the part and take their tokens out of the bitmap of those that the
 // stream is to handle, which starts as the mask.  Then half of the warps enter
 // the queue into the table, 32 ids at a time, and finish the tokens, while the
-// other half streams already (256 rows of 128256 fp32 with everything kept 55 us;
+// other half streams already (256 rows of 128256 fp32 with everything kept 55.0 us;
 // all warps first at the table, then at the stream 56.5 us, a quarter 57.7 us).
 // Integer atomics give the same numbers in any order, wherever a token's slot
 // is.  Whoever enters a token lists its slot, and the listed ones are finished
@@ -28,9 +27,10 @@
 // A part with more than 1024 such tokens is done in passes over smaller ranges,
 // halved until one fits (a range of 1024 tokens always does).
 //
-// The stream over the part (16 bytes per load, units of a few loads per warp,
-// claimed by whoever is free) tests a few bits per load and treats what is not
-// its own as -inf; the finished tokens are written over that, and compete, behind
+// The stream over the part (16 bytes per load, from the first 16-byte boundary on:
+// 160 rows of 68906 bf16 20 us, by single values 36 us; units of a few loads per
+// warp, claimed by whoever is free) tests a few bits per load and treats what is
+// not its own as -inf; the finished tokens are written over that, and compete, behind
 // it (looking them up from the stream made it five times as long: some lane of a
 // warp nearly always has one).  Logits changed in place are read for the table
 // before the stream starts.  The table is small on purpose: what shared memory
@@ -43,9 +43,9 @@
 // cluster barrier kept all 8 until the last had drained its stores).
 //
 // Bound: memory, the logits read (and written, when they are kept): 256 rows of
-// 128256 fp32 logits take 24.6 us for the ids alone (79 % of the measured copy
-// rate), 42.4 us with the logits written, 51.0 us with penalties and biases.  One
-// row is latency: 3.1 us, 5.5 us with everything.
+// 128256 fp32 logits take 25.0 us for the ids alone (77 % of the measured copy
+// rate), 42.5 us with the logits written, 52 us with penalties and biases.  One
+// row is latency: 3.5 us, 5.8 us with penalties and a mask.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,15 +70,18 @@ constexpr uint32_t kSeen = 1u << 31;
 constexpr uint32_t kAllowed = 1u << 15;                            // of a listed slot: the mask leaves it
 constexpr uint32_t kBias = 1u << 14, kPrompt = 2u << 14, kWhat = 3u << 14;  // of a queued id; else generated
 constexpr int kEnterShare = 2;  // 1 of so many warps enters tokens while the others stream
+// Where more wait in the queue, all warps enter them first: the stream would be over
+// before (184 rows of 15603 with 1200 ids 15.2 us, 17.3 us apart).
+constexpr int kEnterApart = 256;
 constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr uint32_t kMaskedBits = 0xFFFFDEADu;  // a NaN that stands for "masked out" in the table
 constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's other CTAs
 
 // How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
 // filled while others stream (256 x 128256 fp32 with penalties, biases and
-// output 55 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
+// output 56 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
 // once there is nothing else to overlap with, and more threads shorten both
-// parts (32 x 128256 bf16 12.1 us, with 256 threads 3 us more).
+// parts (32 x 128256 bf16 11.5 us, with 256 threads 3 us more).
 struct Many {
   static constexpr int kThreads = 256, kResident = 4;
   static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
@@ -100,7 +103,7 @@ struct LogitsParams {
   const int32_t* bias_ids;
   const float* bias_values;
   const uint32_t* mask;
-  int vocab, part, bias_count;  // part: tokens per CTA
+  int vocab, ctas, part, bias_count;  // ctas: per row; part: tokens per CTA
 };
 
 // 16 bytes of logits in fp32
@@ -208,7 +211,7 @@ __device__ __forceinline__ void load_ids(const int32_t* ids, int k0, int count, 
   for (int u = 0; u < kIds; ++u) id[u] = k0 + u * kThreads < count ? __ldg(ids + k0 + u * kThreads) : -1;
 }
 
-template <typename T, int kThreads, int kResident, int kBatch, int kIds>
+template <typename T, bool kAligned, int kThreads, int kResident, int kBatch, int kIds>
 __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const LogitsParams p) {
   constexpr int N = 16 / (int)sizeof(T);  // tokens per 16 bytes
   constexpr int kWarps = kThreads / 32, kEnterWarps = kWarps / kEnterShare;
@@ -220,18 +223,18 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
   __shared__ __align__(16) uint32_t key[kSlots], count[kSlots], entry[kSlots];
   __shared__ uint2 best[kWarps];
   __shared__ uint64_t best_of[kCtas], arrived;  // of the cluster's first CTA: (id, order) of all
-  __shared__ uint32_t allow[kMostTokens / 32];  // the stream's tokens, a bit per token of the pass
+  __shared__ uint32_t allow[kMostTokens / 32 + 1];  // the stream's tokens, a bit per token of the pass
   __shared__ uint16_t list[kList];              // slot, and kAllowed
   __shared__ float list_x[kList];
   __shared__ uint32_t queue[kQueue];  // token of the pass, what it is (kBias and so on), low 16 bits of the bias entry
   __shared__ int listed, queued, next_unit;
   const int rank = (int)cg::this_cluster().block_rank();
-  const int row = blockIdx.x / kCtas;
+  const int row = blockIdx.x / p.ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (rank == 0 && threadIdx.x == 0) {
     mbar_init(smem_u32(&arrived), 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(smem_u32(&arrived), kCtas * 8);
+    mbar_arrive_expect_tx(smem_u32(&arrived), p.ctas * 8);
   }
   __syncwarp();
   // waited for before the first write into another CTA's shared memory
@@ -252,9 +255,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
   for (int base = 0; base < p.part;) {
     const int first = min(p.vocab, (int)min((long long)rank * p.part + base, (long long)p.vocab));
     const int n = min(min(span, p.part - base), p.vocab - first);  // tokens of this pass
-    const bool wide = ((reinterpret_cast<uintptr_t>(x + first) | (out ? reinterpret_cast<uintptr_t>(out + first) : 0)) & 15u) == 0;
-    const int vecs = wide ? n / N : 0;
-    const uint4* src = reinterpret_cast<const uint4*>(x + first);
+    // the stream begins behind `skip` tokens, on a 16-byte boundary
+    const int skip = kAligned ? 0 : min(n, (int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(x + first) & 15u)) % 16u / sizeof(T)));
+    const int vecs = (n - skip) / N;
+    const uint4* src = reinterpret_cast<const uint4*>(x + first + skip);
+    const bool out_wide = kAligned || (reinterpret_cast<uintptr_t>(out + first + skip) & 15u) == 0;
     int hist = 0, prompt = 0;
     int hist_id[kIds], bias_id[kIds];  // the first of both lists
     load_ids<kThreads>(history, threadIdx.x, (int)p.hist_stride, hist_id);
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
       // Some warps do the rest while the others stream -- unless the list may overflow, which has to
       // be known first, or the stream writes over the logits that are needed here.
       const bool apart = done + waiting <= kList && static_cast<const void*>(out) != static_cast<const void*>(x);
-      const int threads = apart ? kEnterWarps * 32 : kThreads;
+      const int threads = apart && waiting <= kEnterApart ? kEnterWarps * 32 : kThreads;
       if ((int)threadIdx.x < threads) {
         enter(threads, waiting, high);
         __syncwarp();
@@ -431,7 +436,12 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
       for (int u = 0; u < kBatch; ++u) {
         const int k = vec_of(unit, u);
         allowed[u] = 0;
-        if (k < vecs) allowed[u] = (bits ? allow[N * k >> 5] >> (N * k & 31) : 0xFFu) & ((1u << N) - 1);
+        if (k < vecs) {
+          const int at = skip + N * k;
+          uint32_t w = 0xFFu;
+          if (bits) w = skip % N ? __funnelshift_r(allow[at >> 5], allow[(at >> 5) + 1], at & 31) : allow[at >> 5] >> (at & 31);
+          allowed[u] = w & ((1u << N) - 1);
+        }
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -447,11 +457,17 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
         for (int e = N - 2; e >= 0; --e) at = v[e] == top ? e : at;
         const bool better = top > bv;
         bv = better ? top : bv;
-        bi = better ? first + N * k + at : bi;
+        bi = better ? first + skip + N * k + at : bi;
         if (out && k < vecs) {
+          float* to = out + first + skip + N * k;
+          if (out_wide) {
 #pragma unroll
-          for (int e = 0; e < N; e += 4)
-            __stcs(reinterpret_cast<float4*>(out + first + N * k + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+            for (int e = 0; e < N; e += 4)
+              __stcs(reinterpret_cast<float4*>(to + e), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) __stcs(to + e, v[e]);
+          }
         }
         if (vec_of(next, u) < vecs) raw[u] = __ldcs(src + vec_of(next, u));
       }
@@ -461,10 +477,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
       can = !bits || ((allow[k >> 5] >> (k & 31)) & 1u);
       return can ? load1(x + first + k) : -INFINITY;
     };
-    for (int k = N * vecs + threadIdx.x; k < n; k += kThreads) {
+    for (int i = threadIdx.x; i < n - N * vecs; i += kThreads) {  // in front of the stream and behind it
+      const int k = i < skip ? i : i + N * vecs;
       bool can;
       const float v = single(k, can);
-      if (can && v > bv) {
+      if (can && (v > bv || (v == bv && first + k < bi))) {
         bv = v;
         bi = first + k;
       }
@@ -508,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
     if (lane == 0) send8(smem_u32(&best_of[rank]), smem_u32(&arrived), (uint64_t)id << 32 | top);
     if (rank == 0) {
       const bool all = wait_cluster(smem_u32(&arrived));
-      const uint64_t e = all && lane < kCtas ? best_of[lane] : 0xFFFFFFFFull << 32;
+      const uint64_t e = all && lane < p.ctas ? best_of[lane] : 0xFFFFFFFFull << 32;
       top = (uint32_t)e;
       id = (uint32_t)(e >> 32);
       best_of_warp(top, id);
@@ -518,28 +535,42 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
 }
 
 template <typename T, typename Shape>
-int launch_logits(const LogitsParams& p, int rows, cudaStream_t stream) {
+int launch_logits(LogitsParams& p, int rows, int ctas, cudaStream_t stream) {
+  p.ctas = ctas;
+  p.part = ((p.vocab + ctas - 1) / ctas + 31) & ~31;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)rows * kCtas);
+  cfg.gridDim = dim3((unsigned)rows * ctas);
   cfg.blockDim = dim3(Shape::kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, logits_kernel<T, Shape::kThreads, Shape::kResident, Shape::kBatch, Shape::kIds>, p),
-                     "cudaLaunchKernelEx(logits)");
+  // every row on a 16-byte boundary, read and written
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | reinterpret_cast<uintptr_t>(p.out) |
+                       (rows > 1 ? (uintptr_t)p.stride * sizeof(T) | (p.out ? (uintptr_t)p.out_stride * 4 : 0) : 0);
+  auto* kernel = (at & 15u) == 0
+                     ? logits_kernel<T, true, Shape::kThreads, Shape::kResident, Shape::kBatch, Shape::kIds>
+                     : logits_kernel<T, false, Shape::kThreads, Shape::kResident, Shape::kBatch, Shape::kIds>;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(logits)");
 }
 
 template <typename T>
-int launch_logits(const LogitsParams& p, int rows, int sms, cudaStream_t stream) {
-  return (long long)rows * kCtas <= (long long)sms * Few::kResident ? launch_logits<T, Few>(p, rows, stream)
-                                                                   : launch_logits<T, Many>(p, rows, stream);
+int launch_logits(LogitsParams& p, int rows, int sms, cudaStream_t stream) {
+  if ((long long)rows * kCtas <= (long long)sms * Few::kResident) return launch_logits<T, Few>(p, rows, kCtas, stream);
+  // As many CTAs per row as run at once, but parts that one pass holds, and lists that leave a
+  // part's tokens few (184 rows of 15603 bf16 with 1231 ids and a mask: eight per row 21.5 us,
+  // four 16.2 us).
+  int ctas = 1;
+  while (ctas < kCtas && ((long long)rows * ctas * 2 <= (long long)sms * Many::kResident || (p.vocab + ctas - 1) / ctas > kMostTokens ||
+                          (p.hist_stride + p.bias_count) / ctas > kList / 2))
+    ctas *= 2;
+  return launch_logits<T, Many>(p, rows, ctas, stream);
 }
 
 }  // namespace
@@ -601,7 +632,6 @@ extern "C" int pkv_process_logits(const void* logits, int dtype, int rows, int v
   p.mask = allow_mask;
   p.vocab = vocab;
   p.bias_count = bias_count;
-  p.part = ((vocab + kCtas - 1) / kCtas + 31) & ~31;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PKV_LOGITS_F32) return launch_logits<float>(p, rows, sm_count(dev), st);
   if (dtype == PKV_LOGITS_BF16) return launch_logits<__nv_bfloat16>(p, rows, sm_count(dev), st);

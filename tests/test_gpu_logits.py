@@ -96,6 +96,37 @@ def test_more_changed_tokens_than_a_pass_holds(lib, cuda_device, dtype, vocab, h
     assert np.array_equal(got[sub], want)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab,hist,bias", [(160, 1777, 30, 3), (320, 1001, 40, 5), (700, 515, 900, 2), (700, 16500, 5, 0),
+                                                  (310, 2048, 3000, 40)])
+def test_many_rows(lib, cuda_device, dtype, rows, vocab, hist, bias):
+    """Fewer CTAs per row, and more of them again where lists are long."""
+    c = case(vocab, rows, vocab, hist, bias, dtype)
+    run(lib, cuda_device, c, NAMES)
+    run(lib, cuda_device, c, ["mask"], out=None)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("vocab,at", [(1, 0), (9, 1), (4099, 3), (20011, 5), (257, 7)])
+def test_equal_logits_at_any_alignment(lib, cuda_device, dtype, vocab, at):
+    """The first of equal logits, wherever 16-byte loads begin; -0 equals 0."""
+    x = torch.zeros((9, vocab + at), dtype=getattr(torch, dtype))
+    x[:, ::2] = -0.0
+    x = x.to(cuda_device)[:, at:]
+    assert (lib.process_logits(x).cpu() == 0).all()
+    mask = torch.zeros((9, (vocab + 31) // 32), dtype=torch.int32)
+    last = vocab - 1
+    mask[:, last // 32] = -2 ** 31 if last % 32 == 31 else 1 << (last % 32)
+    mask[:, 0] |= 1 << min(4, last)
+    out = torch.full((9, vocab + 3), 5.0, device=cuda_device)
+    ids = lib.process_logits(x, out=out[:, 1:vocab + 1], allow_mask=mask.to(cuda_device))
+    assert (ids.cpu() == min(4, last)).all()
+    got = out.cpu().numpy()
+    want = np.full((9, vocab), -np.inf, np.float32)
+    want[:, [min(4, last), last]] = 0
+    assert np.array_equal(got[:, 1:vocab + 1], want) and (got[:, 0] == 5).all() and (got[:, vocab + 1:] == 5).all()
+
+
 @pytest.mark.parametrize("rows", [2, 80])
 @pytest.mark.parametrize("hist,bias,distinct", [(9000, 0, 40), (2500, 1500, 900), (700, 131200, 300), (5, 66000, 2400)])
 def test_long_lists_of_few_tokens(lib, cuda_device, rows, hist, bias, distinct):
