@@ -624,9 +624,11 @@ int kv_read_bs8(const void* kv_pool, const float* kv_scales, int num_pages, int 
 /* paged_gqa_decode over bs8 pages: attention over the values the codes stand
  * for, scores and sums in fp32, output rounded to bf16; lengths of zero, bad
  * lengths and bad page ids as paged_gqa_decode.
- * Codes enter fp16 tensor-core MMAs exactly; q is scaled by a power of two per
- * (sequence, KV head) so that its largest |value| lies in [2^14, 2^15); the
- * probabilities are rounded to fp16 (relative 2^-12) for the P V product.
+ * Codes enter fp16 tensor-core MMAs exactly.  Each q head is scaled by the
+ * power of two that brings its largest |value| into [2^14, 2^15) and is exact in
+ * fp16 but for values below 2^-31 of that one, which are off by at most 2^-39 of
+ * it.  A probability enters the P V product as two fp16 values, off by 2^-22 of
+ * it and by no less than 2^-39 of the largest one.
  *   kv_scales    16-byte aligned
  *   max_seq_len  host upper bound of seq_lens (sizes the grid; a larger
  *                actual length is still handled; 0: 16 max_blocks)

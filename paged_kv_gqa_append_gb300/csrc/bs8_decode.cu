@@ -19,16 +19,18 @@
 // reads its head's 2 KiB of each page from there.
 //
 // A consumer's page: S = q K^T as m16n8k16 with the four query heads in rows
-// 0..3 (two n-tiles of 8 tokens, four k-steps), whose accumulator layout is
-// the B operand's of O^T = V^T P^T, so the probabilities never leave their
-// lanes; V^T is loaded by ldmatrix.trans on byte pairs, which puts the codes
+// 0..3 and again in 4..7 (two n-tiles of 8 tokens, four k-steps), whose
+// accumulator layout is the B operand's of O^T = V^T P^T, so the probabilities
+// never leave their lanes.  fp16 holds 11 bits of a probability: columns 0..3 of
+// P^T are p rounded, columns 4..7 what the rounding left of it, in products that
+// the tile has room for, and their sums are added at the end.  V^T is loaded by ldmatrix.trans on byte pairs, which puts the codes
 // of two tokens and two dims into one register.  Codes become fp16 exactly:
 // e4m3 by conversion, int8 by placing code + 128 into the mantissa of 1024
-// and subtracting 1152.  q is scaled per (sequence, KV head) by the power of
-// two that brings its largest value into [2^14, 2^15): exact in fp16 unless
-// smaller by 2^-31.  Probabilities carry a factor 2^14 that cancels in the
-// division and are rounded to fp16 for the product (half a step is 2^-12 of
-// one, against 2^-9 of the bf16 result); their sum is over the unrounded ones.
+// and subtracting 1152.  A head's q is scaled by the power of two that brings its
+// largest value into [2^14, 2^15): exact in fp16 unless smaller by 2^-31.
+// Probabilities carry a factor 2^14 that cancels in the division; the two
+// columns together are within 2^-22 of one, and within 2^-39 of the largest for
+// the smallest of them.  Their sum is over the unrounded ones.
 //
 // Bound: memory, 1 KiB + 4 B of scales per token.  Of 32 sequences of 2048 tokens
 // (19.0 us, 52 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
@@ -186,23 +188,19 @@ struct Smem {
 template <bool kE4m3>
 struct Head {  // a consumer's state for one segment
   uint32_t qa[4], qb[4];  // q fragments: dims 16 t + 4 i, + 1 and + 2, + 3
-  float o[4][4];          // O^T: dims 16 c + 2 g (+ 1), heads 2 t, 2 t + 1
-  float m, l, unit;       // running maximum and this lane's sum of head g; scale of the scores
+  float o[4][4];          // O^T: dims 16 c + 2 g (+ 1), heads 2 t, 2 t + 1 (their second columns for t > 1)
+  float m, l, unit;       // running maximum and this lane's sum of head g % 4; scale of the scores
 
-  // q of a sequence as this lane will need it: 16 dims of head g, zeros in rows 4..7
+  // q of a sequence as this lane will need it: 16 dims of head g % 4
   struct Q {
     uint4 a, b;
   };
   __device__ static Q fetch(const Bs8DecodeParams& p, int seq, int head) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    Q q{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (g < PKV_GROUP) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + g) * PKV_HEAD_DIM + 16 * t);
-      q.a = src[0];
-      q.b = src[1];
-    }
-    return q;
+    static_assert(PKV_GROUP == 4, "two columns for each head of a group");
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + (g & 3)) * PKV_HEAD_DIM + 16 * t);
+    return Q{src[0], src[1]};
   }
 
   __device__ void start(const Bs8DecodeParams& p, const Q& q) {
@@ -219,7 +217,8 @@ struct Head {  // a consumer's state for one segment
       const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
       bits = max(bits, b < 0x7F800000u ? b : 0u);
     }
-    bits = __reduce_max_sync(0xffffffffu, bits);
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
     // 2^up brings it into [2^14, 2^15), unless it is 0; infinities and NaN stay
     // what they are, in their own head.  up lies in [-113, 141]: two factors
     // keep each a normal number.
@@ -240,6 +239,13 @@ struct Head {  // a consumer's state for one segment
       for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
     m = -INFINITY;
     l = 0.f;
+  }
+
+  // Two probabilities in fp16: rounded (first = 0), or what the rounding leaves (-1).
+  __device__ __forceinline__ static uint32_t column(float p0, float p1, float first) {
+    const uint32_t near = pack_f16x2(p0, p1);
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&near));
+    return pack_f16x2(fmaf(r.x, first, p0), fmaf(r.y, first, p1));
   }
 
   // Two pages in shared memory at `pages`, scales at `scales`; `live` tokens of
@@ -295,7 +301,7 @@ struct Head {  // a consumer's state for one segment
       l *= keep;
       m = now;
     }
-    const float shift = m - kLift;
+    const float shift = m - kLift, first = g < PKV_GROUP ? 0.f : -1.f;
 #pragma unroll
     for (int u = 0; u < kStagePages; ++u) {
       // a page that the last stage does not have: whatever shared memory holds is no scale
@@ -304,7 +310,7 @@ struct Head {  // a consumer's state for one segment
 #pragma unroll
       for (int e = 0; e < 4; ++e) pr[e] = exp2_approx(x[u][e] - shift);
       l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-      const uint32_t b0 = pack_f16x2(pr[0], pr[1]), b1 = pack_f16x2(pr[2], pr[3]);
+      const uint32_t b0 = column(pr[0], pr[1], first), b1 = column(pr[2], pr[3], first);
       // V^T: matrices of 8 tokens x 16 bytes, (chunk, tokens 0..7), (chunk, 8..15), and the next chunk's
       const int row = lane & 15;
       const uint32_t base = pages + u * kBs8PageBytes + (kHeads + head) * kBs8BlockBytes + row * 64;
@@ -340,6 +346,10 @@ struct Head {  // a consumer's state for one segment
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float sum = l + __shfl_xor_sync(0xffffffffu, l, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] += __shfl_xor_sync(0xffffffffu, o[c][e], 2);  // a head's two columns
     if (part) {
       if (g < PKV_GROUP && t == 0)
         *reinterpret_cast<float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * (head * PKV_GROUP + g)) =
