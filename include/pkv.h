@@ -628,7 +628,9 @@ int kv_read_bs8(const void* kv_pool, const float* kv_scales, int num_pages, int 
  * power of two that brings its largest |value| into [2^14, 2^15) and is exact in
  * fp16 but for values below 2^-31 of that one, which are off by at most 2^-39 of
  * it.  A probability enters the P V product as two fp16 values, off by 2^-22 of
- * it and by no less than 2^-39 of the largest one.
+ * it and by no less than 2^-39 of the largest one.  The sums p v are kept 2^20
+ * times smaller than they are: 2^20 values next to fp32's largest do not
+ * overflow.
  *   kv_scales    16-byte aligned
  *   max_seq_len  host upper bound of seq_lens (sizes the grid; a larger
  *                actual length is still handled; 0: 16 max_blocks)

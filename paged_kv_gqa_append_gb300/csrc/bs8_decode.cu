@@ -30,7 +30,9 @@
 // largest value into [2^14, 2^15): exact in fp16 unless smaller by 2^-31.
 // Probabilities carry a factor 2^14 that cancels in the division; the two
 // columns together are within 2^-22 of one, and within 2^-39 of the largest for
-// the smallest of them.  Their sum is over the unrounded ones.
+// the smallest of them.  Their sum is over the unrounded ones.  The output's sums
+// are kept 2^20 times smaller than they are, so that a million values next to
+// fp32's largest do not overflow.
 //
 // Bound: memory, 1 KiB + 4 B of scales per token.  Of 32 sequences of 2048 tokens
 // (19.0 us, 52 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
@@ -79,6 +81,10 @@ constexpr int kWholePages = 8, kWholePagesMost = 24;
 constexpr int kBySequence = 128;
 constexpr uint32_t kWaitUs = 2000000;                   // limit of every wait
 constexpr float kLift = 14.f;                           // probabilities carry 2^14
+// 2^-34 on a page's product, with them, to the output's sums (in the page's scale it would
+// cost bits where values are below 1e-27).
+constexpr float kLower = 0x1p-34f;
+constexpr float kRaise = 0x1p34f;                       // with the final division
 constexpr float kNothing = -1.f;                        // l of a part with a bad page
 
 // Workspace: per CTA two parts (of a sequence begun in an earlier CTA, and of
@@ -335,7 +341,7 @@ struct Head {  // a consumer's state for one segment
           float d[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16(d, a0, a1, a2, a3, b0, b1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[2 * c2 + h][e] = fmaf(vs, d[e], o[2 * c2 + h][e]);
+          for (int e = 0; e < 4; ++e) o[2 * c2 + h][e] = fmaf(vs, d[e] * kLower, o[2 * c2 + h][e]);
         }
       }
     }
@@ -368,7 +374,7 @@ struct Head {  // a consumer's state for one segment
     if (t < 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float inv = bad ? 0.f : 1.f / (h ? s1 : s0);
+        const float inv = bad ? 0.f : kRaise * (1.f / (h ? s1 : s0));
         uint16_t* dst = p.out + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + 2 * t + h) * PKV_HEAD_DIM + 2 * g;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(kMergeThreads, kPerSm) bs8_merge_kernel(const 
     acc.z += e.z;
     acc.w += e.w;
   }
-  const float inv = 1.f / sum;
+  const float inv = kRaise * (1.f / sum);
   *reinterpret_cast<uint2*>(out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM + dims) =
       bad ? make_uint2(0, 0)
           : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

@@ -114,3 +114,17 @@ def test_heads_of_a_group_with_queries_of_different_sizes(lib, cuda_device, kind
     q[:, 1::4] *= 2.0 ** 44
     q[:, 2::4] *= 2.0 ** -44
     check(lib, cuda_device, kind, OB.from_f32_rne(q.astype(np.float32)), codes, scales, bt, lens)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [2.0 ** 127.9, 2.0 ** 110, 2.0 ** -70, 2.0 ** -100])
+def test_values_next_to_the_ends_of_the_range(lib, cuda_device, kind, size):
+    """V as large as bf16 goes, of one sign so that the sums grow with the length, and V
+    whose sums come near the smallest numbers; in one CTA and over many."""
+    lens = [3, 1500, 8000]
+    codes, scales, bt = pages(5, lens, kind)
+    codes[:, 1, :, :, ::2] &= 0x7F                     # every second dim of one sign
+    top = 127 if kind == "int8" else 448
+    scales[:, 1] = np.float32(size / top) * np.random.default_rng(6).uniform(0.5, 0.99, scales[:, 1].shape)
+    scales[:, 0] *= np.float32(0.05)
+    check(lib, cuda_device, kind, rows(7, 3, 32, 64), codes, scales, bt, lens)
