@@ -195,7 +195,8 @@ template <bool kE4m3>
 struct Head {  // a consumer's state for one segment
   uint32_t qa[4], qb[4];  // q fragments: dims 16 t + 4 i, + 1 and + 2, + 3
   float o[4][4];          // O^T: dims 16 c + 2 g (+ 1), heads 2 t, 2 t + 1 (their second columns for t > 1)
-  float m, l, unit;       // running maximum and this lane's sum of head g % 4; scale of the scores
+  float m, l;             // running maximum and this lane's sum of head g % 4
+  float unit, unit2;      // scale of the scores, in two factors: their product may be too small for a float
 
   // q of a sequence as this lane will need it: 16 dims of head g % 4
   struct Q {
@@ -238,7 +239,8 @@ struct Head {  // a consumer's state for one segment
       qa[i] = pack_f16x2(x[4 * i] * f0 * f1, x[4 * i + 1] * f0 * f1);
       qb[i] = pack_f16x2(x[4 * i + 2] * f0 * f1, x[4 * i + 3] * f0 * f1);
     }
-    unit = p.scale * 1.4426950408889634f * d0 * d1;
+    unit = p.scale * 1.4426950408889634f * d0;
+    unit2 = d1;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -261,7 +263,7 @@ struct Head {  // a consumer's state for one segment
     float x[2][4];
 #pragma unroll
     for (int u = 0; u < kStagePages; ++u) {
-      const float ks = scales[u * 2 * kHeads + head] * unit;
+      const float ks = scales[u * 2 * kHeads + head] * unit * unit2;
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile) {
         // K rows of 64 bytes, 16-byte chunks swizzled by (row / 2) % 4

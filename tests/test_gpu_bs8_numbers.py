@@ -128,3 +128,14 @@ def test_values_next_to_the_ends_of_the_range(lib, cuda_device, kind, size):
     scales[:, 1] = np.float32(size / top) * np.random.default_rng(6).uniform(0.5, 0.99, scales[:, 1].shape)
     scales[:, 0] *= np.float32(0.05)
     check(lib, cuda_device, kind, rows(7, 3, 32, 64), codes, scales, bt, lens)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("up", [-124, -110, 60, 110])
+def test_queries_and_keys_at_opposite_ends_of_the_range(lib, cuda_device, kind, up):
+    """Scores of ordinary size from q about 2^up and K about 2^-up."""
+    lens = [33, 900]
+    codes, scales, bt = pages(8, lens, kind)
+    scales[:, 0] = np.ldexp(np.random.default_rng(9).uniform(0.5, 1, scales[:, 0].shape), -up - (7 if kind == "int8" else 9))
+    q = OB.to_f64(rows(10, 2, 32, 64)) * 2.0 ** up
+    check(lib, cuda_device, kind, OB.from_f32_rne(q.astype(np.float32)), codes, scales, bt, lens)
