@@ -54,6 +54,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "logits_table.cuh"
 #include "pkv.h"
 #include "ptx.cuh"
 
@@ -64,8 +65,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kCtas = 8;
 constexpr int kMostTokens = 16384;  // of a pass: the bitmaps
-constexpr int kSlots = 2048;        // of the table
-constexpr int kList = 1024;         // tokens entered; a CTA's threads more may be before all see that it is full
 constexpr uint32_t kSeen = 1u << 31;
 constexpr uint32_t kAllowed = 1u << 15;                            // of a listed slot: the mask leaves it
 constexpr uint32_t kBias = 1u << 14, kPrompt = 2u << 14, kWhat = 3u << 14;  // of a queued id; else generated
@@ -73,7 +72,6 @@ constexpr int kEnterShare = 2;  // 1 of so many warps enters tokens while the ot
 // Where more wait in the queue, all warps enter them first: the stream would be over
 // before (184 rows of 15603 with 1200 ids 15.2 us, 17.3 us apart).
 constexpr int kEnterApart = 256;
-constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr uint32_t kMaskedBits = 0xFFFFDEADu;  // a NaN that stands for "masked out" in the table
 constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's other CTAs
 
@@ -201,8 +199,14 @@ __device__ __forceinline__ float change(float x, uint32_t count, uint32_t entry,
   return x;
 }
 
-__device__ __forceinline__ uint32_t first_slot(int at) { return ((uint32_t)at * 2654435769u) >> 21; }
-static_assert(kSlots == 1 << 11, "first_slot");
+// The table in shared memory (logits_table.cuh).
+struct SharedTable {
+  uint32_t* keys;
+  int* listed;
+  __device__ __forceinline__ uint32_t key(uint32_t i) const { return *(volatile uint32_t*)(keys + i); }
+  __device__ __forceinline__ uint32_t claim(uint32_t i, uint32_t at) const { return atomicCAS(keys + i, kEmpty, at); }
+  __device__ __forceinline__ bool full() const { return *(volatile int*)listed >= kList; }
+};
 
 // A thread's share of a list of ids, kIds at a time (-1: none).
 template <int kThreads, int kIds>
@@ -281,20 +285,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
 
     const bool tables = hist > 0 || p.bias_count > 0;
     if (tables) {
-      // the slot of token `at`, entered if it is new; -1 once the list is full
-      const auto slot_of = [&](int at, bool& entered) {
-        uint32_t i = first_slot(at);
-        for (int tries = 0; tries < kSlots; ++tries, i = (i + 1) & (kSlots - 1)) {
-          uint32_t k = *(volatile uint32_t*)(key + i);
-          if (k == (uint32_t)at) return (int)i;
-          if (k != kEmpty) continue;
-          if (*(volatile int*)&listed >= kList) return -1;
-          k = atomicCAS(key + i, kEmpty, (uint32_t)at);
-          entered = k == kEmpty;
-          if (entered || k == (uint32_t)at) return (int)i;
-        }
-        return -1;
-      };
+      const SharedTable table{key, &listed};
+      const bool may_overflow = n > kList;
       // the first `total` of the queue into the table, by the first `threads` threads; `high`: of the bias entries
       const auto enter = [&](int threads, int total, uint32_t high) {
         for (int i0 = threadIdx.x & ~31; i0 < total; i0 += threads) {
@@ -307,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
             const int at = (int)(e & 0x3FFFu);
             v = load1(x + first + at);  // needed if the token is new; under way meanwhile
             if (mask) word = __ldg(mask + ((first + at) >> 5)) >> (at & 31);
-            slot = slot_of(at, entered);
+            slot = slot_of(table, at, may_overflow, entered);
             if (slot >= 0) {
               const uint32_t what = e & kWhat;
               if (what == kBias)
@@ -408,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
         enter(threads, waiting, high);
         __syncwarp();
         asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-        if (listed >= kList && n > kList && !apart) {  // it may be incomplete: a smaller range
+        if (listed >= kList && may_overflow && !apart) {  // it may be incomplete: a smaller range
           span = max(kList, ((n + 1) / 2 + 31) & ~31);
           __syncthreads();
           continue;
