@@ -717,7 +717,9 @@ int pkv_argmax_f32(const float* logits, int rows, int vocab, long long row_strid
  *   3. i among bias_ids: x = x + its bias (the last entry of an id counts)
  *   4. bit i % 32 of allow_mask[r][i / 32] is 0: x = -inf
  * out[r][i] = x.  out_ids[r] = the first index of the largest non-NaN x among
- * the tokens that the mask leaves; -1 if there is none.
+ * the tokens that the mask leaves; -1 if there is none.  (-2 would say that the
+ * CTAs of a row did not hear from each other within seconds: a fault of the
+ * device, not of the call.)
  *   logits        device [rows][row_stride], PKV_LOGITS_F32 / BF16 / F16
  *   out           device float [rows][out_stride] or NULL (ids only); may be
  *                 logits itself (F32, the same stride)

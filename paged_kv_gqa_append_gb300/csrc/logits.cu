@@ -74,6 +74,13 @@ constexpr int kEnterShare = 2;  // 1 of so many warps enters tokens while the ot
 constexpr int kEnterApart = 256;
 constexpr uint32_t kMaskedBits = 0xFFFFDEADu;  // a NaN that stands for "masked out" in the table
 constexpr uint32_t kWaitUs = 2000000;  // limit of the wait for the cluster's other CTAs
+// The CTAs of a row finish together but for those whose part has many listed tokens: up
+// to a pass for every 1024 tokens instead of every 16384, each over both lists.  Up to
+// this product of a part's tokens and the lists' ids that is 2^20 ids more, half a
+// millisecond, far within kWaitUs; beyond it the cluster closes with a barrier, which
+// does not show beside such lists.
+constexpr long long kLongLists = 1ll << 30;
+constexpr int kExchangeFailed = -2;    // id of a row whose CTAs did not hear from each other
 
 // How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
 // filled while others stream (256 x 128256 fp32 with penalties, biases and
@@ -102,6 +109,7 @@ struct LogitsParams {
   const float* bias_values;
   const uint32_t* mask;
   int vocab, ctas, part, bias_count;  // ctas: per row; part: tokens per CTA
+  int long_lists;
 };
 
 // 16 bytes of logits in fp32
@@ -180,6 +188,18 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar) {
     if (ok) return true;
     if (global_timer_ns() - t0 > (uint64_t)kWaitUs * 1000ull) return false;
   }
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The first CTA's last warp after a wait that ran out: the others may still send into its
+// shared memory, so it stays until they have exited (a barrier counts exited threads as
+// arrived).  Then all of it is there.
+__device__ __noinline__ bool wait_for_exit(uint32_t bar, bool closed) {
+  if (!closed) cluster_barrier();
+  return __all_sync(0xffffffffu, wait_cluster(bar));
 }
 
 struct Row {
@@ -509,19 +529,24 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const Logit
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
   if (!p.ids) return;
-  if (warp == 0) {
+  if (warp != 0) {
+    if (p.long_lists) cluster_barrier();
+  } else {
     const uint2 w = lane < kThreads / 32 ? best[lane] : make_uint2(0u, 0xFFFFFFFFu);
     top = w.x;
     id = w.y;
     best_of_warp(top, id);
     if (lane == 0) send8(smem_u32(&best_of[rank]), smem_u32(&arrived), (uint64_t)id << 32 | top);
+    __syncwarp();
+    if (p.long_lists) cluster_barrier();
     if (rank == 0) {
-      const bool all = wait_cluster(smem_u32(&arrived));
-      const uint64_t e = all && lane < p.ctas ? best_of[lane] : 0xFFFFFFFFull << 32;
+      bool all = __all_sync(0xffffffffu, wait_cluster(smem_u32(&arrived)));
+      if (!all) all = wait_for_exit(smem_u32(&arrived), p.long_lists);
+      const uint64_t e = lane < p.ctas ? best_of[lane] : 0xFFFFFFFFull << 32;
       top = (uint32_t)e;
       id = (uint32_t)(e >> 32);
       best_of_warp(top, id);
-      if (lane == 0) p.ids[row] = (int)id;
+      if (lane == 0) p.ids[row] = all ? (int)id : kExchangeFailed;
     }
   }
 }
@@ -530,6 +555,7 @@ template <typename T, typename Shape>
 int launch_logits(LogitsParams& p, int rows, int ctas, cudaStream_t stream) {
   p.ctas = ctas;
   p.part = ((p.vocab + ctas - 1) / ctas + 31) & ~31;
+  p.long_lists = (p.hist_stride + p.bias_count) > kLongLists / p.part;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
