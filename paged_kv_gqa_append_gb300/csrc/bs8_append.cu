@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "append_place.cuh"
 #include "bs8.cuh"
 #include "internal.h"
 #include "pkv.h"
@@ -52,7 +53,8 @@ struct Bs8AppendParams {
   uint8_t* pool;
   float* scales;
   int* d_err;
-  int T, num_seqs, bt_stride, max_blocks, num_pages, max_pos, chunk;
+  int T, num_seqs, bt_stride, num_pages, chunk;
+  int most;  // tokens that the tables, of pages and of rotations, have room for
 };
 
 // The last sequence s with cu[s] <= t (cu ascending, n = number of sequences),
@@ -72,12 +74,6 @@ __device__ int find_sequence(const int32_t* __restrict__ cu, int n, int t) {
   }
   return base - 1;
 }
-
-// A token's place: its sequence and position; ok only if both can be used.
-struct Place {
-  int seq, pos, end;      // end: the row behind the sequence's last new token
-  bool live, ok, first;   // live: the token belongs to a sequence; first: of its new ones
-};
 
 __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
   Place a{-1, 0, t + 1, false, false, false};
@@ -103,13 +99,7 @@ __device__ __forceinline__ Place place_of(const Bs8AppendParams& p, int t) {
     len = __ldg(p.seq_lens + a.seq);
   }
   a.live = true;
-  const int fresh = hi - lo;
-  if (hi <= t || hi > p.T || lo < 0) return a;  // not ascending, or beyond the rows given
-  a.end = hi;
-  if (len < fresh || len > (long long)p.max_blocks * PKV_PAGE_TOKENS || (p.cos && len > p.max_pos)) return a;
-  a.pos = len - fresh + (t - lo);
-  a.ok = true;
-  a.first = t == lo;
+  set_place(a, t, p.T, lo, hi, len, p.most);
   return a;
 }
 
@@ -434,9 +424,9 @@ extern "C" int kv_append_rope_bs8(const void* k, long long k_stride, const void*
   p.T = T;
   p.num_seqs = num_seqs;
   p.bt_stride = bt_row_stride;
-  p.max_blocks = max_blocks;
+  p.most = max_blocks * PKV_PAGE_TOKENS;
+  if (rope_cos && max_pos < p.most) p.most = max_pos;
   p.num_pages = num_pages;
-  p.max_pos = max_pos;
   p.chunk = T / num_seqs >= kChunkMany && T >= kManyTokensPerSm * sm_count(dev) ? kChunkMany : 1;
 
   cudaLaunchAttribute attr[1];
