@@ -575,7 +575,9 @@ int paged_gqa_decode_append_layers(const void* q, const void* k_new, const void*
  * scale = amax / top over the block's tokens and code = round-half-even(x /
  * scale), both divisions IEEE fp32, top = 127 for int8 (codes clamped to
  * [-127, 127]) and 448 for e4m3; scale 0 gives zero codes.  x is the row the
- * bf16 cache would hold.  Rows must be finite.
+ * bf16 cache would hold.  An infinity or NaN in a row makes the scale of its
+ * block infinite or NaN, and the whole block reads as NaN until slot 0 is written
+ * again.
  * ---------------------------------------------------------------------- */
 #define PKV_BS8_INT8 0
 #define PKV_BS8_E4M3 1

@@ -9,6 +9,8 @@ The new tokens of a call that fall into one block set its scale together:
 anew from slot 0 on, else the larger of the scale found and theirs; when that
 grows, a held code becomes the code of fp32(fp32(code * old) / new).
 
+Rows are finite here.
+
 Arrays: codes uint8 bytes [pages][2][8][16][64], scales float32 [pages][2][8].
 fp32 divisions and products are FP64 ones rounded once, which is the same.
 """

@@ -194,7 +194,8 @@ __device__ __forceinline__ void append_run(const Bs8AppendParams& p, int t, int 
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, max(top & 0xFFFF0000u, top << 16)));
   old = __shfl_sync(0xffffffffu, old, 0);
   const float fresh = __fdiv_rn(amax, kE4m3 ? 448.f : 127.f);
-  const bool grown = slot > 0 && fresh > old;
+  // (a NaN among the rows becomes the block's scale and stays it, so that it shows)
+  const bool grown = slot > 0 && (fresh > old || fresh != fresh);
   const float now = slot == 0 || grown ? fresh : old;
   if (lane == 0 && (slot == 0 || grown)) *scale = now;
   const auto write = [&](int r, const uint2& codes) {

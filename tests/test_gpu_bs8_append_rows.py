@@ -59,3 +59,38 @@ def test_cu_new_that_does_not_ascend(lib, cuda_device, cu, lens):
     got, sc, code = append(lib, cuda_device, "int8", codes, scales, rows(2, T, 8, 64), rows(3, T, 8, 64), cu, lens, bt)
     assert code == lib.ERR_DEVICE_INDEX
     assert np.array_equal(got, codes) and np.array_equal(sc, scales)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80])
+@pytest.mark.parametrize("at", [0, 4, 9])
+def test_rows_that_are_not_finite_show(lib, cuda_device, kind, bad, at):
+    """A NaN or an infinity in one value of K of one head: every token of that block reads
+    as NaN, before and after it, in this call and in later ones; the other blocks are
+    what they would be without it."""
+    codes, scales = random_pages(5, 2, kind)
+    bt = np.array([[1]], np.int32)
+    k, v = rows(6, 14, 8, 64), rows(7, 14, 8, 64)
+    k[at + 1:, 5] = OB.from_f32_rne((40 * OB.to_f64(k[at + 1:, 5])).astype(np.float32))      # finite rows that would grow the scale
+    k[at, 5, 33] = bad
+    clean = k.copy()
+    clean[:, 5] = 0
+    got, want = (codes, scales), (codes, scales, None, False)
+    for lo, hi in ((0, 4), (4, 9), (9, 10), (10, 14)):
+        *got, code = append(lib, cuda_device, kind, *got[:2], k[lo:hi], v[lo:hi], [0, hi - lo], [hi], bt)
+        want = O8.append(want[0], want[1], clean[lo:hi], v[lo:hi], [0, hi - lo], [hi], bt, kind)
+        assert code == 0
+        if at < hi:
+            assert not np.isfinite(got[1][1, 0, 5])
+            pool = torch.from_numpy(got[0].view(np.int8)).to(cuda_device).view(TYPES[kind])
+            sc = torch.from_numpy(got[1]).to(cuda_device)
+            read = lib.kv_read_bs8(pool, sc, to_dev_i32([1], cuda_device)).float()[0]
+            assert torch.isnan(read[0, 5, :hi]).all()
+            out = torch.zeros(1, 32, 64, dtype=torch.bfloat16, device=cuda_device)
+            lib.paged_gqa_decode_bs8(to_dev_bf16(rows(8, 1, 32, 64), cuda_device), pool, sc, to_dev_i32(bt, cuda_device),
+                                     to_dev_i32([hi], cuda_device), out, 0.125)
+            assert torch.isnan(out[0, 20:24].float()).all()
+            assert torch.isfinite(out[0, :20].float()).all() and torch.isfinite(out[0, 24:].float()).all()
+    other = np.ones((2, 2, 8), bool)
+    other[1, 0, 5] = False
+    assert np.array_equal(got[0][other], want[0][other]) and np.array_equal(got[1][other], want[1][other])
