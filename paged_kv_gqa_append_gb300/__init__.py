@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import re
 
 import numpy as np
 import torch
@@ -160,6 +161,10 @@ def _load_calls():
     spec = importlib.util.spec_from_file_location(__name__ + "._calls", CALLS_PATH)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
+    built, here = module.torch_version, re.match(r"\d+\.\d+\.\d+", torch.__version__).group()
+    if built != here:  # another layout of its tensors, perhaps
+        raise RuntimeError(f"_calls.so was built against torch {built}, this is {here}; build it with "
+                           "`python -m paged_kv_gqa_append_gb300.build`")
     _CALLS = module
     return module
 

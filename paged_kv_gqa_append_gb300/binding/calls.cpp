@@ -16,6 +16,7 @@
 #include <limits.h>
 #include <stdint.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "pkv.h"
 
@@ -343,4 +344,11 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the smal
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

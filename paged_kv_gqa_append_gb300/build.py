@@ -7,13 +7,15 @@ root and the shared library to ``paged_kv_gqa_append_gb300/libpkv.so``.
 The CUDA runtime is linked statically, so the library loads on a machine
 without a GPU driver (calls then fail with PKV_ERR_CUDA).  The Python binding's
 marshalling of the small calls (binding/calls.cpp) is compiled against the
-installed torch into ``paged_kv_gqa_append_gb300/_calls.so``; libpkv.so itself
-needs neither Python nor torch.
+installed torch into ``paged_kv_gqa_append_gb300/_calls.so``, and again when that
+is another one; libpkv.so itself needs neither Python's headers nor torch and is
+built without them.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -50,14 +52,46 @@ def sources():
 def _inputs():
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return sources() + headers + [BINDING, os.path.abspath(__file__)]
+    return sources() + headers + [os.path.abspath(__file__)]
+
+
+def _older(target, inputs):
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in inputs)
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None else None
+
+
+def _stamp_path():
+    return os.path.join(BUILD, "calls.torch")
+
+
+def _torch_stamp() -> str:
+    """What the binding is compiled against: torch, where it is, and Python."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"torch {version} {_torch_dir()} python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def binding_is_stale() -> bool:
+    """Without torch there is no binding to build."""
+    if _torch_dir() is None:
+        return False
+    if _older(BINDING_LIB, [BINDING, os.path.join(INCLUDE, "pkv.h"), os.path.abspath(__file__)]):
+        return True
+    try:
+        with open(_stamp_path()) as f:
+            return f.read() != _torch_stamp()
+    except OSError:
+        return True
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    return _older(LIB, _inputs()) or binding_is_stale()
 
 
 def _compile(src: str, ptxas_verbose: bool) -> tuple[str, str]:
@@ -73,7 +107,7 @@ def _compile(src: str, ptxas_verbose: bool) -> tuple[str, str]:
 
 def _compile_binding() -> str:
     obj = os.path.join(BUILD, "calls.cpp.o")
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING, "-o", obj,
            "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
@@ -86,7 +120,7 @@ def _compile_binding() -> str:
 
 
 def _link_binding(obj: str):
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch_dir()
     tmp = BINDING_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-lpkv", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
@@ -94,6 +128,8 @@ def _link_binding(obj: str):
     if r.returncode != 0:
         raise RuntimeError(f"link of _calls.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
+    with open(_stamp_path(), "w") as f:
+        f.write(_torch_stamp())
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
@@ -101,25 +137,26 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) 
     if not force and not ptxas_verbose and not is_stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
+    whole = force or ptxas_verbose or _older(LIB, _inputs())
+    srcs = sources() if whole else []
     with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if _torch_dir() is not None else None
         results = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
-        binding_obj = binding.result()
-    objs = [o for o, _ in results]
     logs = "".join(e for _, e in results)
     if ptxas_verbose:
         with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
             f.write(logs)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if whole:
+        tmp = LIB + ".tmp"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for o, _ in results]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if binding is not None:  # what may be wrong with it does not keep the library from being built
+        _link_binding(binding.result())
     if not quiet:
-        print(f"built {LIB}")
+        print(f"built {LIB}" + ("" if binding is not None else " (without the Python binding's _calls.so: no torch)"))
         if ptxas_verbose:
             print(logs)
     return LIB
