@@ -14,8 +14,8 @@
 //
 // A CTA of 16 warps (8 heads x {K, V}) looks at `chunk` consecutive tokens
 // and handles the runs that begin among them: one token per CTA for decode
-// steps and few tokens, 16 per CTA when sequences bring 16 tokens or more on
-// average, where most tokens begin no run.  The chunk's q heads are rotated by another CTA, so
+// steps and few tokens, 16 per CTA when sequences bring several tokens each, so
+// that most begin no run.  The chunk's q heads are rotated by another CTA, so
 // that neither waits for the other.
 //
 // Bound: memory, 3 KiB per token for K and V, and 8 KiB for q.  Codes without a
@@ -40,9 +40,13 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kRow = PKV_HEAD_DIM;
 constexpr int kChunkMany = 16;
-// Fewer tokens are few runs: each finds a CTA at once if every token has one (316
-// tokens of six sequences 5.6 us, by chunks 6.9 us; 1029 of four 10.2 and 5.9 us).
-constexpr int kManyTokensPerSm = 3;
+// By chunks: 8 tokens a sequence or more, and at least 3 per SM in all; or 2 and 12.  With
+// less there are few runs, and each finds a CTA at once if every token has one.  By
+// tokens and by chunks (us): 316 tokens of six sequences 5.6, 6.9; 1029 of four 10.2,
+// 5.9; 57 x 8 tokens 6.9, 6.1; 512 x 8 40, 16; 32 x 8 5.3, 6.0; 114 x 4 7.0, 9.3; 1024 x
+// 4 43, 21; 400 x 2 12, 17; 1000 x 2 28, 26; 4096 x 2 107, 61; 1000 x 1 14, 25.
+constexpr int kManyPerSequence = 8, kManyTokensPerSm = 3;
+constexpr int kMorePerSequence = 2, kMoreTokensPerSm = 12;
 
 struct Bs8AppendParams {
   const uint16_t *k, *v, *q_in;
@@ -428,7 +432,10 @@ extern "C" int kv_append_rope_bs8(const void* k, long long k_stride, const void*
   p.most = max_blocks * PKV_PAGE_TOKENS;
   if (rope_cos && max_pos < p.most) p.most = max_pos;
   p.num_pages = num_pages;
-  p.chunk = T / num_seqs >= kChunkMany && T >= kManyTokensPerSm * sm_count(dev) ? kChunkMany : 1;
+  const int sms = sm_count(dev);
+  const bool many = (T / num_seqs >= kManyPerSequence && T >= kManyTokensPerSm * sms) ||
+                    (T / num_seqs >= kMorePerSequence && T >= kMoreTokensPerSm * sms);
+  p.chunk = many ? kChunkMany : 1;
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
