@@ -343,7 +343,11 @@ struct Head {  // a consumer's state for one segment
           float d[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16(d, a0, a1, a2, a3, b0, b1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[2 * c2 + h][e] = fmaf(vs, d[e] * kLower, o[2 * c2 + h][e]);
+          for (int e = 0; e < 4; e += 2) {
+            const float2 low = mul2(make_float2(d[e], d[e + 1]), make_float2(kLower, kLower));
+            o[2 * c2 + h][e] = fmaf(vs, low.x, o[2 * c2 + h][e]);
+            o[2 * c2 + h][e + 1] = fmaf(vs, low.y, o[2 * c2 + h][e + 1]);
+          }
         }
       }
     }
