@@ -615,7 +615,7 @@ int kv_append_rope_bs8(const void* k, long long k_stride, const void* v, long lo
                        const void* q_in, long long q_stride, void* q_out, int* d_err,
                        void* stream);
 
-/* kv_read_bs8: pages as bf16 pages, out[i] = code * scale (rounded once) of
+/* kv_read_bs8: pages as bf16 pages, out[i] = code * scale (in fp32, then bf16) of
  * page page_ids[i], device bf16 [count][2][8][16][64]: a bf16 pool of `count`
  * pages, e.g. for paged_gqa_prefill over a cached prefix.  Slots that hold no
  * token read as whatever their bytes stand for.  A page id outside

@@ -35,12 +35,15 @@
 // fp32's largest do not overflow.
 //
 // Bound: memory, 1 KiB + 4 B of scales per token.  Of 32 sequences of 2048 tokens
-// (19.0 us, 52 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
+// (19.6 us, 51 % of the measured copy rate) the pages take 9 us at 7.5 TB/s; 2.3
 // us go by before the first copy is issued (lengths, their sums, the table
 // entries: loads that wait for one another), 3 us at the end, where SMs of larger
 // GPCs get less bandwidth each and finish their equal shares later, and 2.8 us
 // for the merge.  97 sequences of up to 8191 tokens run at 80 %.  A page holds
-// one warp for about 150 instructions; the tensor pipe is busy 27 % of the time.
+// one warp for about 210 instructions, everything around it included (58 % of the
+// issue slots); the tensor pipe is busy 26 % of the time.  The second column of the
+// probabilities costs 0.4 us of the 19.6 and the lowered sums 0.2; the ragged 97 take
+// the same time without both, 4096 sequences of 64 tokens 54 instead of 58 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,14 +73,15 @@ constexpr int kMaxSeqsBs8 = 4096;
 constexpr int kMinPages = 4;                            // least share of a CTA
 // Short sequences stay whole, one CTA's each: nothing to merge, nothing to add up
 // first.  Short is up to 8 pages, and one more per 8 sequences up to 24: one
-// sequence of 8 pages takes 6.5 us, by shares 6.9 us, of 12 pages 8.0 and 6.8 us; 64
-// of 16 pages 10.1 and 9.2 us (ragged 9.9 and 11.6 us), of 24 pages 13.4 and 10.6 us;
-// 152 of 24 pages 16.2 and 22.2 us; 1000 ragged ones to 24 pages 52 and 51 us.
+// sequence of 8 pages takes 6.5 us, by shares 7.1 us, of 12 pages 8.3 and 7.1 us; 64
+// of 8 pages 6.7 and 9.2 us, of 16 10.4 and 9.3 us (ragged 10.5 and 11.5 us), of 24
+// 14.4 and 11.1 us; 152 of 24 pages 16.6 and 21.7 us; 1000 ragged ones to 24 pages 57
+// and 53 us; 4096 of 4 pages 58 and 72 us.
 constexpr int kWholePages = 8, kWholePagesMost = 24;
 // Up to this many sequences the merge looks at every sequence; beyond it at every
 // CTA, in each of which one split sequence begins at most (4096 sequences of 64
-// tokens in shares: 67 us, by sequence 107 us; 256 of 2048: 99 and 105 us; 97 mixed
-// ones: 75.5 and 74 us).
+// tokens in shares: 72 us, by sequence 93 us; 1000 ragged ones to 300: 46 and 51 us;
+// 256 of 2048: 95.5 us both; 97 ragged ones to 8191: 73.7 and 72.6 us).
 constexpr int kBySequence = 128;
 constexpr uint32_t kWaitUs = 2000000;                   // limit of every wait
 constexpr float kLift = 14.f;                           // probabilities carry 2^14
@@ -865,6 +869,11 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   if (rc != PKV_OK) return rc;
   rc = cuda_status(cudaLaunchKernelEx(&cfg, decode, map, p), "cudaLaunchKernelEx(decode bs8)");
   if (rc != PKV_OK || ctas == 1 || whole) return rc;  // one CTA splits nothing
+  // Heads per CTA of the merge.  1, 8 and 16 of them (us): 1 sequence of 131071 tokens 32.5,
+  // 42.7, 48.4; 8 of 16384 29.8, 30.9, 32.0; 16 of 2048 15.6, 13.7, 13.7; 32 of 8192 55.5,
+  // 50.3, 50.2; 39 of 2048 29.7, 24.3, 22.5; 256 of 2048 144, 105, 97.  Two CTAs per SM from
+  // more CTAs than SMs on: 76 of 2048 (152 CTAs) 33.9, two per SM 35.5; 77 35.6 and 35.9;
+  // 128 53.2 and 52.8; 256 of 1024 56.6 and 56.2.
   const int heads = num_seqs <= 8 ? 1 : num_seqs * 4 <= sms ? 8 : 16;
   const long long items = p.by_cta ? ctas - 1 : num_seqs;  // nothing goes on behind the last CTA
   cfg.gridDim = dim3((unsigned)(items * (PKV_NUM_Q_HEADS / heads)));

@@ -19,8 +19,9 @@
 // last bias entry.  All warps first queue the ids that are in the part and take their tokens out of the bitmap of those that the
 // stream is to handle, which starts as the mask.  Then half of the warps enter
 // the queue into the table, 32 ids at a time, and finish the tokens, while the
-// other half streams already (256 rows of 128256 fp32 with everything kept 55.0 us;
-// all warps first at the table, then at the stream 56.5 us, a quarter 57.7 us).
+// other half streams already (256 rows of 128256 fp32 with penalties, 300 biases and
+// the logits kept 55.9 us; all warps first at the table, then at the stream 1.5 us
+// more, a quarter of them 2.7 us).
 // Integer atomics give the same numbers in any order, wherever a token's slot
 // is.  Whoever enters a token lists its slot, and the listed ones are finished
 // one thread each.
@@ -43,9 +44,11 @@
 // cluster barrier kept all 8 until the last had drained its stores).
 //
 // Bound: memory, the logits read (and written, when they are kept): 256 rows of
-// 128256 fp32 logits take 25.0 us for the ids alone (77 % of the measured copy
-// rate), 42.5 us with the logits written, 52 us with penalties and biases.  One
-// row is latency: 3.5 us, 5.8 us with penalties and a mask.
+// 128256 fp32 logits take 26.0 us for the ids alone (74 % of the measured copy
+// rate), 42.2 us with the logits written, 55.9 us with penalties and biases.  One
+// row is latency: 3.5 us, 5.8 us with penalties and a mask.  Lists that hold much of
+// the vocabulary cost a pass for every 1024 tokens, each over the whole lists: 1.1 ms
+// for a bias of every token.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -84,7 +87,7 @@ constexpr int kExchangeFailed = -2;    // id of a row whose CTAs did not hear fr
 
 // How a CTA works.  Many rows: four small CTAs per SM, so that one's table is
 // filled while others stream (256 x 128256 fp32 with penalties, biases and
-// output 56 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
+// output 55.9 us, with 2 x 512 threads 20 us more).  When all CTAs fit on the GPU at
 // once there is nothing else to overlap with, and more threads shorten both
 // parts (32 x 128256 bf16 11.5 us, with 256 threads 3 us more).
 struct Many {
@@ -582,8 +585,12 @@ template <typename T>
 int launch_logits(LogitsParams& p, int rows, int sms, cudaStream_t stream) {
   if ((long long)rows * kCtas <= (long long)sms * Few::kResident) return launch_logits<T, Few>(p, rows, kCtas, stream);
   // As many CTAs per row as run at once, but parts that one pass holds, and lists that leave a
-  // part's tokens few (184 rows of 15603 bf16 with 1231 ids and a mask: eight per row 21.5 us,
-  // four 16.2 us).
+  // part's tokens few.  1, 2, 4 and 8 CTAs per row (us, the rule's first): 40 rows of 15603
+  // bf16 8: 6.2 (6.5, 5.4, 5.5); 184 with 100 ids 2: 8.4 (7.9, 11.3, 15.9), with 1231 ids 4:
+  // 15.6 (27.6, 14.5, 19.5); 150 of 32000 fp32 with 1024 ids 4: 14.0 (20.6, 13.7, 16.6); 64 of
+  // 128256 fp32 8: 15.7 (56, 31, 20); 256 of 50000 fp32 4: 17.5 (24.5, 17.9, 22.8); 1000 of
+  // 32000 bf16 with 1000 ids 2: 43.2 (43.4, 52.5, 81.8); where it is off, by 20 % at most but
+  // for 200 of 4000 with 3000 ids, 8: 22.0 (50.8, 29.6, 16.3).
   int ctas = 1;
   while (ctas < kCtas && ((long long)rows * ctas * 2 <= (long long)sms * Many::kResident || (p.vocab + ctas - 1) / ctas > kMostTokens ||
                           (p.hist_stride + p.bias_count) / ctas > kList / 2))
