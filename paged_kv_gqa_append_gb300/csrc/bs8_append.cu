@@ -40,13 +40,15 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kRow = PKV_HEAD_DIM;
 constexpr int kChunkMany = 16;
-// By chunks: 8 tokens a sequence or more, and at least 3 per SM in all; or 2 and 12.  With
-// less there are few runs, and each finds a CTA at once if every token has one.  By
-// tokens and by chunks (us): 316 tokens of six sequences 5.6, 6.9; 1029 of four 10.2,
-// 5.9; 57 x 8 tokens 6.9, 6.1; 512 x 8 40, 16; 32 x 8 5.3, 6.0; 114 x 4 7.0, 9.3; 1024 x
-// 4 43, 21; 400 x 2 12, 17; 1000 x 2 28, 26; 4096 x 2 107, 61; 1000 x 1 14, 25.
-constexpr int kManyPerSequence = 8, kManyTokensPerSm = 3;
-constexpr int kMorePerSequence = 2, kMoreTokensPerSm = 12;
+// By chunks: 16 tokens a sequence or more, and at least 3 per SM in all; or 4 and 20.
+// With less there are few runs, and each finds a CTA at once if every token has one,
+// while a chunk's runs follow one another: 16 of one token, as beside a prompt, take 25
+// us (300 x 1 and a prompt of 1600: 20, 32).  By tokens and by chunks (us): 316 tokens of
+// six sequences 5.6, 6.9; 1029 of four 10.2, 5.9; 38 x 16 7.8, 5.3; 57 x 8 6.9, 6.1; 512
+// x 8 40, 16; 114 x 4 7.0, 9.3; 1024 x 4 43, 21; 400 x 2 12, 17; 1000 x 2 28, 26; 1000 x 1
+// 14, 25; 3000 x 1 and a prompt of 14000 182, 60.
+constexpr int kManyPerSequence = 16, kManyTokensPerSm = 3;
+constexpr int kMorePerSequence = 4, kMoreTokensPerSm = 20;
 
 struct Bs8AppendParams {
   const uint16_t *k, *v, *q_in;
