@@ -749,6 +749,68 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
                        const int32_t* bias_ids, const float* bias_values, int bias_count,
                        const uint32_t* allow_mask, long long mask_stride, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Pages handed out and taken back on the GPU, for decode loops that do not
+ * return to the host between steps (one captured graph replayed, say): what
+ * pkv_sched_grow and pkv_sched_finish do to block tables and the stack of free
+ * pages, in the same order, for a batch of rows.
+ *   free_pages  device int32 [num_pages]: a stack, free_pages[0 .. *free_count)
+ *               are the free page ids, the last of them is taken first
+ *   free_count  device int32
+ *   block_tables  device int32, layer l at + l * bt_layer_stride, row s at
+ *               + s * bt_row_stride, max_blocks entries used; the first
+ *               ceil(seq_lens[s] / 16) of a row are its pages
+ * Both calls are all or nothing.  At most 4096 rows and 2^30 entries
+ * num_layers * max_blocks.
+ * ---------------------------------------------------------------------- */
+
+/* pkv_grow_block_tables: row s, which holds seq_lens[s] tokens, is to hold
+ * new_tokens[s] more.  Its tables get the pages that takes, in every layer, popped
+ * row by row, in a row layer by layer, in a layer in order.  new_tokens NULL: one
+ * each.
+ *   seq_lens_out    int32 [num_seqs]: seq_lens + new_tokens (may be seq_lens)
+ *   free_count_out  int32: pages left (may be free_count)
+ *   cu_new          int32 [num_seqs + 1]: rows of the new tokens in a packed batch,
+ *                   0, new_tokens[0], ... (what kv_append_rope_bs8 and _int4 take)
+ *   positions, token_seq  int32 [T] or NULL: position and row of each new token
+ *                   (what kv_append_rope takes)
+ *   slots           int32 [num_layers][T] or NULL: 16 * page + position % 16 of
+ *                   each new token in every layer
+ * Entries of positions, token_seq and slots behind the last new token become -1.
+ * Nothing is taken, the lengths and the count are passed on as they were, cu_new
+ * is all 0 and the other outputs all -1, with *d_err set, if
+ *   PKV_ERR_DEVICE_INDEX    a length or number of new tokens is negative, a row
+ *                           would pass 16 * max_blocks tokens, the new tokens are
+ *                           more than T (T = 0 with none of the three outputs
+ *                           given: not checked), or *free_count is outside
+ *                           [0, num_pages]
+ *   PKV_ERR_POOL_EXHAUSTED  the stack has fewer pages than it takes
+ * Ids in the stack are handed out as they are; one outside [0, num_pages) gives
+ * slots -1 and sets *d_err = PKV_ERR_DEVICE_INDEX.  num_pages < 2^27. */
+int pkv_grow_block_tables(const int32_t* seq_lens, const int32_t* new_tokens, int num_seqs,
+                          int32_t* block_tables, int num_layers, long long bt_layer_stride,
+                          int bt_row_stride, int max_blocks, const int32_t* free_pages,
+                          int num_pages, const int32_t* free_count, int32_t* seq_lens_out,
+                          int32_t* free_count_out, int32_t* cu_new, int32_t* positions,
+                          int32_t* token_seq, int32_t* slots, int T, int* d_err, void* stream);
+
+/* pkv_release_pages: the pages of every row with finished[s] != 0 are put back
+ * on the stack, row by row, layer by layer, in order.
+ *   finished        device bytes [num_seqs]
+ *   seq_lens_out    int32 [num_seqs]: 0 for finished rows (may be seq_lens)
+ *   free_count_out  int32 (may be free_count)
+ * The tables are not written: entries behind a row's length are never read.
+ * Nothing is put back (lengths and count passed on as they were; what lies above
+ * the count in free_pages is of no meaning) with *d_err = PKV_ERR_DEVICE_INDEX if
+ * a length of a finished row is negative or above 16 * max_blocks, one of its
+ * page ids is outside [0, num_pages), the stack would hold more than num_pages, or
+ * *free_count is outside [0, num_pages]. */
+int pkv_release_pages(const int32_t* seq_lens, const uint8_t* finished, int num_seqs,
+                      const int32_t* block_tables, int num_layers, long long bt_layer_stride,
+                      int bt_row_stride, int max_blocks, int32_t* free_pages, int num_pages,
+                      const int32_t* free_count, int32_t* seq_lens_out, int32_t* free_count_out,
+                      int* d_err, void* stream);
+
 /* Wait for `stream`, then copy the device error word to *code_out (host).
  * If `clear` is non-zero the word is reset to 0 afterwards. */
 int pkv_read_device_error(int* d_err, void* stream, int clear, int* code_out);

@@ -111,6 +111,9 @@ _SIGS = {
                                   _p]),
     "pkv_process_logits": (_i, [_p, _i, _i, _i, _ll, _p, _ll, _p, _p, _ll, _p, _p, _p, _p, _p, _p,
                                 _p, _i, _p, _ll, _p]),
+    "pkv_grow_block_tables": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p, _p, _p,
+                                   _i, _p, _p]),
+    "pkv_release_pages": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p]),
     "pkv_read_device_error": (_i, [_p, _p, _i, _ip]),
     "pkv_credit_pages": (_i, [_i, _i, _i]),
     "pkv_sched_create": (_p, [_i, _i, _i, _i]),
@@ -1211,6 +1214,91 @@ def process_logits(logits, out=None, ids=None, history=None, history_lens=None, 
           stride[0] if rows > 1 else vocab, dst, out_stride, id_ptr, hist, H, h_lens, p_lens, rep, pres, freq,
           b_ids, b_vals, B, mask, mask_stride))
     return ids
+
+
+# ------------------------------------------------- block tables on the GPU --
+
+def new_free_pages(num_pages: int, device):
+    """The stack of a pool whose pages are all free: (ids [num_pages] int32 in
+    the order of a fresh Scheduler, page 0 taken first; count [1] int32)."""
+    return (torch.arange(num_pages - 1, -1, -1, dtype=_I32, device=device),
+            torch.full((1,), num_pages, dtype=_I32, device=device))
+
+
+def _layer_tables(t, dev, rows):
+    """block_tables [layers, >= rows, width] as (address, layers, layer stride,
+    row stride, width)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32:
+        raise TypeError("block_tables must be an int32 tensor")
+    if t.device != dev:
+        raise ValueError(f"block_tables must be on {dev}, got {t.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] < rows or shape[0] < 1 or shape[2] < 1 or (stride[2] != 1 and shape[2] > 1):
+        raise ValueError("block_tables must be [layers, >= num_seqs, width] with contiguous rows")
+    row = stride[1] if shape[1] > 1 else shape[2]
+    layer = stride[0] if shape[0] > 1 else rows * row
+    if row < shape[2] or (shape[0] > 1 and layer < rows * row):
+        raise ValueError("block_tables: rows and layers must not overlap")
+    return t.data_ptr(), shape[0], layer, row, shape[2]
+
+
+def _stack(free_pages, free_count, seq_lens, seq_lens_out, free_count_out, dev, S):
+    """The stack and where the new lengths and count go (by default in place)."""
+    if getattr(free_pages, "dtype", None) is not _I32:
+        raise TypeError("free_pages must be an int32 tensor")
+    return (_vec(free_pages, "free_pages", _I32, dev, free_pages.numel()), free_pages.numel(),
+            _vec(free_count, "free_count", _I32, dev, 1),
+            _vec(seq_lens if seq_lens_out is None else seq_lens_out, "seq_lens_out", _I32, dev, S),
+            _vec(free_count if free_count_out is None else free_count_out, "free_count_out", _I32, dev, 1))
+
+
+def grow_block_tables(seq_lens, new_tokens, block_tables, free_pages, free_count, seq_lens_out=None,
+                      free_count_out=None, cu_new=None, positions=None, token_seq=None, slots=None, d_err=None,
+                      max_blocks=None, stream=None):
+    """Room for new_tokens[s] (None: one each) more tokens in every row, on the
+    GPU; returns cu_new ([num_seqs + 1] int32, the rows' offsets).
+
+    block_tables [layers, >= num_seqs, width] int32 get pages popped from the
+    stack free_pages (new_free_pages) as Scheduler.grow would, row by row and
+    layer by layer; seq_lens and free_count change in place, or go to
+    seq_lens_out and free_count_out.  positions, token_seq [T] int32 and slots
+    [layers, T] int32 (16 * page + position % 16): of every new token, -1 behind
+    the last.  All or nothing: too few pages (PKV_ERR_POOL_EXHAUSTED) or a row
+    that cannot grow (PKV_ERR_DEVICE_INDEX) sets d_err, and nothing is taken."""
+    dev = _on_device(seq_lens, "seq_lens")
+    S = seq_lens.numel()
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    new = _opt(new_tokens, "new_tokens", _I32, dev, S)
+    bt, layers, layer, row, width = _layer_tables(block_tables, dev, S)
+    stack, pages, count, lens_to, count_to = _stack(free_pages, free_count, seq_lens, seq_lens_out, free_count_out, dev, S)
+    T = next((t.numel() for t in (positions, token_seq) if t is not None),
+             0 if slots is None else slots.numel() // layers)
+    pos, seq = _opt(positions, "positions", _I32, dev, T), _opt(token_seq, "token_seq", _I32, dev, T)
+    slot = _opt(slots, "slots", _I32, dev, layers * T)
+    if cu_new is None:
+        cu_new = _empty(S + 1, _I32, dev, stream)
+    _call(dev, stream, "pkv_grow_block_tables", (lens, new, S, bt, layers, layer, row,
+          width if max_blocks is None else max_blocks, stack, pages, count, lens_to, count_to,
+          _vec(cu_new, "cu_new", _I32, dev, S + 1), pos, seq, slot, T, _device_error(d_err, dev)))
+    return cu_new
+
+
+def release_pages(seq_lens, finished, block_tables, free_pages, free_count, seq_lens_out=None, free_count_out=None,
+                  d_err=None, max_blocks=None, stream=None):
+    """The pages of the rows with finished[s] (bool or uint8) put back on the
+    stack, on the GPU, as Scheduler.finish would row by row; their lengths
+    become 0.  In place or to seq_lens_out and free_count_out; all or nothing
+    (d_err: PKV_ERR_DEVICE_INDEX)."""
+    dev = _on_device(seq_lens, "seq_lens")
+    S = seq_lens.numel()
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    if getattr(finished, "dtype", None) not in (torch.bool, torch.uint8):
+        raise TypeError("finished must be a bool or uint8 tensor")
+    done = _vec(finished, "finished", finished.dtype, dev, S)
+    bt, layers, layer, row, width = _layer_tables(block_tables, dev, S)
+    stack, pages, count, lens_to, count_to = _stack(free_pages, free_count, seq_lens, seq_lens_out, free_count_out, dev, S)
+    _call(dev, stream, "pkv_release_pages", (lens, done, S, bt, layers, layer, row,
+          width if max_blocks is None else max_blocks, stack, pages, count, lens_to, count_to, _device_error(d_err, dev)))
 
 
 def pkv_read_device_error(d_err, clear: bool = True, stream=None) -> int:
