@@ -73,6 +73,11 @@ extern "C" {
  * value, [2 (K,V)][8][16][64], and one fp32 scale per (page, K|V, KV head). */
 #define PKV_BS8_PAGE_BYTES (PKV_PAGE_ELEMS) /* 16384 */
 
+/* 4-bit pages (int4): one block per (page, KV head) = K codes [16][64] of 4
+ * bits, V codes, and a bf16 scale and minimum for each K and V row. */
+#define PKV_I4_BLOCK_BYTES 1152 /* 512 + 512 + 2 * 16 * 4 */
+#define PKV_I4_PAGE_BYTES (PKV_NUM_KV_HEADS * PKV_I4_BLOCK_BYTES) /* 9216 */
+
 typedef enum pkv_status {
   PKV_OK = 0,
   PKV_ERR_INVALID_ARGUMENT = 1,   /* null pointer, negative size, bad stride  */
@@ -648,6 +653,47 @@ int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_sca
                          int max_blocks, const int32_t* seq_lens, int num_seqs, int max_seq_len,
                          void* out, float scale, void* workspace, size_t workspace_bytes,
                          int* d_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit pages (int4) - a cache of 0.28 of the bf16 size: every row (token, KV
+ * head, K or V) has 64 codes of 4 bits, a scale and a minimum, and is never
+ * written again.
+ *   kv_pool    device bytes [num_pages][8][1152], 16-byte aligned
+ * With the row's smallest and largest value lo and hi (bf16 values, so lo is
+ * kept exactly), every operation IEEE fp32:
+ *   scale = bf16((hi / 2 - lo / 2) / 7.5), 0 where that is below 2^-126
+ *   inv   = 2 / scale
+ *   code  = min(15, round-half-even((x / 2 - lo / 2) * inv))    (0 for scale 0)
+ * and a code c stands for lo + c * scale.  x is the row the bf16 cache would
+ * hold.  A row with an infinity or NaN gets scale = lo = NaN and codes 0: it reads
+ * as NaN.
+ * Inside a block of 1152 bytes, for slot r = 8 u + g (u = 0, 1) and dim d:
+ *   K code   byte 16 (4 g + d / 16) + 8 u + d % 16 / 2
+ *   V code   byte 512 + 16 (4 (d / 8) + g / 2) + 8 u + 4 (d % 8 / 4) + 2 (g % 2)
+ *                + d % 4 / 2
+ *   even d in the low half of the byte, odd d in the high half;
+ *   scale    bf16 at byte 1024 + 16 g + 4 u (K), + 8 (V); the minimum behind it
+ * which is the order in which the decode's matrix instructions take them.
+ * ---------------------------------------------------------------------- */
+
+/* kv_append_rope_int4: the newest tokens of every sequence written into their
+ * pages; arguments, ragged rows, rotation and errors as kv_append_rope_bs8
+ * (without its limit on two sequences of a call that write one page: rows are
+ * independent of each other; a slot written twice by one call holds either). */
+int kv_append_rope_int4(const void* k, long long k_stride, const void* v, long long v_stride,
+                        const int32_t* cu_new, const int32_t* seq_lens, int T,
+                        const int32_t* block_tables, int num_seqs, int bt_row_stride,
+                        int max_blocks, void* kv_pool, int num_pages, const float* rope_cos,
+                        const float* rope_sin, int max_pos, const void* q_in, long long q_stride,
+                        void* q_out, int* d_err, void* stream);
+
+/* kv_read_int4: pages as bf16 pages, out[i] = bf16(lo + code * scale) of page
+ * page_ids[i], device bf16 [count][2][8][16][64]: a bf16 pool of `count` pages,
+ * e.g. for paged_gqa_prefill over a cached prefix.  Slots that hold no token
+ * read as whatever their bytes stand for.  A page id outside [0, num_pages)
+ * gives a zero page and sets *d_err. */
+int kv_read_int4(const void* kv_pool, int num_pages, const int32_t* page_ids, int count, void* out,
+                 int* d_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * paged_gqa_prefill - causal GQA attention of each sequence's newest tokens

@@ -111,6 +111,9 @@ _SIGS = {
                                   _p]),
     "pkv_process_logits": (_i, [_p, _i, _i, _i, _ll, _p, _ll, _p, _p, _ll, _p, _p, _p, _p, _p, _p,
                                 _p, _i, _p, _ll, _p]),
+    "kv_append_rope_int4": (_i, [_p, _ll, _p, _ll, _p, _p, _i, _p, _i, _i, _i, _p, _i, _p, _p, _i, _p,
+                                 _ll, _p, _p, _p]),
+    "kv_read_int4": (_i, [_p, _i, _p, _i, _p, _p, _p]),
     "pkv_grow_block_tables": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p, _p, _p,
                                    _i, _p, _p]),
     "pkv_release_pages": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p]),
@@ -937,6 +940,86 @@ def paged_gqa_decode_bs8(q, kv_pool, kv_scales, block_tables, seq_lens, out, sca
     _call(dev, stream, "paged_gqa_decode_bs8", (q_ptr, pool, scales, pages, code, bt, row, mb, lens, S,
           PAGE_TOKENS * mb if max_seq_len is None else int(max_seq_len), dst, float(scale),
           _vec(workspace, "workspace", torch.uint8, dev, size), size, err))
+
+
+# ------------------------------------------------------ 4-bit pages (int4) --
+
+I4_BLOCK_BYTES = 1152
+_I4_PAGE = (NUM_KV_HEADS, I4_BLOCK_BYTES)
+
+
+def new_int4_pool(num_pages: int, device) -> torch.Tensor:
+    """An empty pool of 4-bit pages [num_pages, 8, 1152] uint8 (block format: pkv.h)."""
+    return torch.zeros((num_pages, *_I4_PAGE), dtype=torch.uint8, device=device)
+
+
+def _int4_pool(kv_pool):
+    """Checks a pool of 4-bit pages; returns (device, address, pages)."""
+    dev = _on_device(kv_pool, "kv_pool")
+    if kv_pool.dtype is not torch.uint8:
+        raise TypeError(f"kv_pool must be uint8, got {kv_pool.dtype}")
+    shape = kv_pool.shape
+    if shape[1:] != _I4_PAGE or not kv_pool.is_contiguous():
+        raise ValueError(f"kv_pool must be a contiguous [num_pages, {NUM_KV_HEADS}, {I4_BLOCK_BYTES}]")
+    return dev, kv_pool.data_ptr(), shape[0]
+
+
+def kv_append_rope_int4(k, v, cu_new, seq_lens, block_tables, kv_pool, rope_cos=None, rope_sin=None, q_in=None,
+                        q_out=None, d_err=None, max_blocks=None, stream=None):
+    """The newest tokens of every sequence written into 4-bit pages
+    (new_int4_pool): every row of 64 values as codes with a scale and a minimum.
+
+    Rows cu_new[s] .. cu_new[s + 1] - 1 of k and v are the last tokens of the
+    seq_lens[s] that sequence s then holds (cu_new = arange for a decode step).
+    With tables [max_pos, 32], K (and q_in into q_out) are rotated as in
+    kv_append_rope; without, K is taken as it is.  k, v [T, 8, 64], q_in
+    [T, 32, 64] bf16 with any token stride that is a multiple of 8."""
+    dev, pool, pages = _int4_pool(kv_pool)
+    k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
+    v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
+    S = seq_lens.numel()
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    cu = _vec(cu_new, "cu_new", _I32, dev, S + 1)
+    bt, _, row = _block_rows(block_tables, dev, S)
+    cos = sin = q_ptr = q_dst = None
+    max_pos = q_stride = 0
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    if rope_cos is not None:
+        shape = rope_cos.shape
+        if len(shape) != 2 or shape[1] != ROPE_PAIRS:
+            raise ValueError("rope_cos and rope_sin must be [max_pos, 32]")
+        max_pos = shape[0]
+        cos = _vec(rope_cos, "rope_cos", _F32, dev, max_pos * ROPE_PAIRS)
+        sin = _vec(rope_sin, "rope_sin", _F32, dev, max_pos * ROPE_PAIRS)
+    if (q_in is None) != (q_out is None):
+        raise ValueError("q_in and q_out go together")
+    if q_in is not None:
+        if rope_cos is None:
+            raise ValueError("q_in needs rope_cos and rope_sin")
+        q_ptr, q_stride, _ = _rows(q_in, "q_in", NUM_Q_HEADS, dev, T)
+        q_dst = _vec(q_out, "q_out", _BF16, dev, T * _Q_ROW_ELEMS)
+    err = _device_error(d_err, dev)
+    if T == 0 or S == 0:
+        return
+    _call(dev, stream, "kv_append_rope_int4", (k_ptr, k_stride, v_ptr, v_stride, cu, lens, T, bt, S, row,
+          row if max_blocks is None else max_blocks, pool, pages, cos, sin, max_pos, q_ptr, q_stride, q_dst, err))
+
+
+def kv_read_int4(kv_pool, page_ids, out=None, d_err=None, stream=None):
+    """Pages page_ids of a 4-bit pool as bf16 pages [len(page_ids), 2, 8, 16, 64]
+    (a bf16 pool, e.g. for paged_gqa_prefill over a cached prefix with block
+    table 0 .. n - 1)."""
+    dev, pool, pages = _int4_pool(kv_pool)
+    n = page_ids.numel()
+    ids = _vec(page_ids, "page_ids", _I32, dev, n)
+    if out is None:
+        out = _empty((n, *_PAGE), _BF16, dev, stream)
+    dst = _vec(out, "out", _BF16, dev, n * _PAGE_ELEMS)
+    err = _device_error(d_err, dev)
+    if n:
+        _call(dev, stream, "kv_read_int4", (pool, pages, ids, n, dst, err))
+    return out
 
 
 def paged_gqa_decode_append(q, k_new, v_new, kv_pool, block_tables, seq_lens, out, rope_cos,
