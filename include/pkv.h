@@ -695,6 +695,29 @@ int kv_append_rope_int4(const void* k, long long k_stride, const void* v, long l
 int kv_read_int4(const void* kv_pool, int num_pages, const int32_t* page_ids, int count, void* out,
                  int* d_err, void* stream);
 
+/* paged_gqa_decode over int4 pages: attention over the values the codes stand
+ * for, scores and sums in fp32, output rounded to bf16; lengths of zero, bad
+ * lengths and bad page ids as paged_gqa_decode.
+ * Codes enter fp16 tensor-core MMAs exactly.  Each q head is scaled by the
+ * power of two that brings its largest |value| into [2^14, 2^15) and is exact in
+ * fp16 but for values below 2^-27 of that one, which are off by at most 2^-36 of
+ * it.  A weight (a probability times its V row's scale) enters the product as two
+ * fp16 values, off by 2^-22 of it and by no less than 2^-37 of the largest one.
+ *   max_seq_len  host upper bound of seq_lens (chooses how the work is split; a
+ *                larger actual length is still handled; 0: 16 max_blocks)
+ *   workspace    at least paged_gqa_decode_int4_workspace_bytes(num_seqs)
+ *                bytes, 16-byte aligned, of any content: every call writes
+ *                what it reads.  Calls that may run at the same time, two
+ *                captured graphs among them, need distinct workspaces
+ * At most 4096 sequences, and fewer than 2^30 entries num_seqs * max_blocks of
+ * the tables. */
+size_t paged_gqa_decode_int4_workspace_bytes(int num_seqs);
+int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num_pages,
+                          const int32_t* block_tables, int bt_row_stride, int max_blocks,
+                          const int32_t* seq_lens, int num_seqs, int max_seq_len, void* out,
+                          float scale, void* workspace, size_t workspace_bytes, int* d_err,
+                          void* stream);
+
 /* ------------------------------------------------------------------------
  * paged_gqa_prefill - causal GQA attention of each sequence's newest tokens
  * over its own pages: a whole prompt, or a chunk of one after a cached

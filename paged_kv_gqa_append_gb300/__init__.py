@@ -114,6 +114,8 @@ _SIGS = {
     "kv_append_rope_int4": (_i, [_p, _ll, _p, _ll, _p, _p, _i, _p, _i, _i, _i, _p, _i, _p, _p, _i, _p,
                                  _ll, _p, _p, _p]),
     "kv_read_int4": (_i, [_p, _i, _p, _i, _p, _p, _p]),
+    "paged_gqa_decode_int4_workspace_bytes": (_sz, [_i]),
+    "paged_gqa_decode_int4": (_i, [_p, _p, _i, _p, _i, _i, _p, _i, _i, _p, _f, _p, _sz, _p, _p]),
     "pkv_grow_block_tables": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p, _p, _p,
                                    _i, _p, _p]),
     "pkv_release_pages": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p]),
@@ -1020,6 +1022,46 @@ def kv_read_int4(kv_pool, page_ids, out=None, d_err=None, stream=None):
     if n:
         _call(dev, stream, "kv_read_int4", (pool, pages, ids, n, dst, err))
     return out
+
+
+def paged_gqa_decode_int4_workspace_bytes(num_seqs: int) -> int:
+    return int(_L().paged_gqa_decode_int4_workspace_bytes(num_seqs))
+
+
+def alloc_int4_workspace(num_seqs: int, device, stream=None) -> torch.Tensor:
+    """Caller-owned workspace for paged_gqa_decode_int4 of up to num_seqs
+    sequences (allocated on `stream`, default the current one)."""
+    with torch.cuda.device(device):
+        n = paged_gqa_decode_int4_workspace_bytes(num_seqs)
+    if n <= 0:
+        raise PkvError(3 if num_seqs > 4096 else 5, "paged_gqa_decode_int4_workspace_bytes")
+    return _empty(n, torch.uint8, device, stream)
+
+
+def paged_gqa_decode_int4(q, kv_pool, block_tables, seq_lens, out, scale, workspace=None, max_seq_len=None,
+                          d_err=None, max_blocks=None, stream=None):
+    """paged_gqa_decode over 4-bit pages (new_int4_pool): q, out
+    [num_seqs, 32, 64] bf16, q rotated.  workspace: alloc_int4_workspace, one
+    for each stream or captured graph that may run at the same time."""
+    dev, pool, pages = _int4_pool(kv_pool)
+    shape = q.shape
+    if shape[-2:] != _Q_ROW:
+        raise ValueError(f"q must end in shape {_Q_ROW}, got {tuple(shape)}")
+    n = q.numel()
+    S = n // _Q_ROW_ELEMS
+    q_ptr, dst = _vec(q, "q", _BF16, dev, n), _vec(out, "out", _BF16, dev, n)
+    lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
+    bt, _, row = _block_rows(block_tables, dev, S)
+    mb = row if max_blocks is None else max_blocks
+    err = _device_error(d_err, dev)
+    if S == 0:
+        return
+    if workspace is None:
+        workspace = alloc_int4_workspace(S, dev, stream)
+    size = workspace.numel()
+    _call(dev, stream, "paged_gqa_decode_int4", (q_ptr, pool, pages, bt, row, mb, lens, S,
+          PAGE_TOKENS * mb if max_seq_len is None else int(max_seq_len), dst, float(scale),
+          _vec(workspace, "workspace", torch.uint8, dev, size), size, err))
 
 
 def paged_gqa_decode_append(q, k_new, v_new, kv_pool, block_tables, seq_lens, out, rope_cos,

@@ -1,0 +1,722 @@
+// One decode step of grouped-query attention over pages of 4-bit codes with a scale
+// and a minimum for every row, sm_103a.
+//
+// For sequence s with n tokens, KV head g and its query heads h (one pass with a
+// running reference instead of the maximum, exponentials in base 2):
+//   x_j = scale log2(e) (ks_j (q_h . ck_j) + kl_j sum q_h),   p_j = 2^(x_j - R)
+//   out_h = (sum_j (p_j vs_j) cv_j + sum_j p_j vl_j) / sum_j p_j
+// so scales and minima touch scores and probabilities only, and the codes 0..15
+// themselves enter the MMAs.  A code is the fp16 number of the same bits, c 2^-24, or
+// c 2^-20 where it stands 4 bits higher: two bit masks and one shift turn 32 bits into
+// the eight codes as four registers of operands, and the factors cost nothing -- those
+// of K go into q, those of V into the end.
+//
+// Tiles: a page is the 16 rows of m16n8k16.  S^T = K q^T has the four query heads twice
+// in its eight columns, side by side, so a lane holds its score once for each copy: it
+// computes one probability and puts the rounding to fp16 into one column and what that
+// left into the other (22 bits in all), which the product O^T = V^T P^T has room for.
+// The accumulators' layout is turned into the B operand's by movmatrix.  The order of a
+// block (int4.cuh) gives each lane its 16 codes of K, 16 of V and scales as three
+// 16-byte words.  Products of one page are added to the output's sums outside the tensor
+// core, which would round them towards zero: with codes that are never negative that
+// would add up.
+//
+// References: R is the next whole number over the largest score, set again only when a
+// score passes R + 1.  The weights p vs and p vl / 16 are multiplied by a power of two,
+// `lift`, that brings the largest of them near 2^14, set again only when one passes 2^15:
+// a head's sums are near that, whatever V's size.  Both are seldom, so the usual page has
+// two votes and no reduction.  What is merged are means and the logarithms of their
+// weights, which neither overflow nor vanish for any V that bf16 holds.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "int4.cuh"
+#include "internal.h"
+#include "pkv.h"
+#include "ptx.cuh"
+#include "split_merge.cuh"
+
+namespace pkv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kHeads = PKV_NUM_KV_HEADS;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRing = 4;                 // pages on their way to a warp, and the one that it works on
+constexpr int kCtasPerSm = 2;            // of the kernel for shares
+constexpr int kMaxSeqsInt4 = 4096;
+constexpr int kMinPages = 4;             // least share of a CTA
+constexpr int kList = 1024;              // page ids of a share held at a time
+constexpr int kMostCluster = 8;
+constexpr float kStart = -1.5e38f;       // R before the first score
+constexpr float kMostLift = 0x1p126f;
+// Means are merged 2^10 times smaller than they are: up to 304 of them are added up.
+constexpr float kMeanDown = 0x1p-10f, kMeanUp = 0x1p10f;
+
+struct Int4DecodeParams {
+  const uint16_t* q;
+  const uint8_t* pool;
+  const int32_t *block_tables, *seq_lens;
+  uint16_t* out;
+  float* parts;
+  int2* span;  // by sequence: first and last CTA of a split one; by CTA: the split sequence that begins
+               // there and its last CTA; else (-1, -1)
+  int* d_err;
+  float scale;
+  int num_pages, bt_stride, max_blocks, num_seqs, min_pages, by_cta;
+};
+
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Pages of sequence s: none for an empty or refused one.
+__device__ __forceinline__ int pages_of(const Int4DecodeParams& p, int s, bool& refused) {
+  const int n = __ldg(p.seq_lens + s);
+  refused = n < 0 || n > (long long)p.max_blocks * PKV_PAGE_TOKENS;
+  return refused ? 0 : (int)(((unsigned)n + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS);
+}
+
+// A warp's state for the four query heads of one KV head over some pages.  Lane (g, t) = 4 g + t
+// has the scores of head t with slots g and g + 8, and dims 8 g .. 8 g + 7 of its output.
+struct Group {
+  uint32_t q[8];       // B operands of the four k-steps
+  float fa, fb, fl;    // x = (S fa) (ks fb) + kl fl
+  float ref, lift;
+  float l, low;        // this lane's sum of p, of p vl lift
+  float o[4][4];       // tile w: dims 8 g + 2 w (two columns), 8 g + 2 w + 1 (16 times too large), lifted
+
+  // q of head g / 2, dims 16 t .. 16 t + 15
+  __device__ static void fetch(const Int4DecodeParams& p, int seq, int head, uint4 (&raw)[2]) {
+    static_assert(PKV_GROUP == 4, "two columns for each head of a group");
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + (g >> 1)) * PKV_HEAD_DIM + 16 * t);
+    raw[0] = src[0];
+    raw[1] = src[1];
+  }
+
+  __device__ void start(const uint4 (&raw)[2], float scale) {
+    const int t = threadIdx.x & 3;
+    float x[16];
+    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    uint32_t bits = 0;  // of the largest finite |q|: magnitudes order as their bits
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[2 * e] = bf16lo_to_f32(w[e]);
+      x[2 * e + 1] = bf16hi_to_f32(w[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+      bits = max(bits, b < 0x7F800000u ? b : 0u);
+    }
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
+    // 2^up brings it into [2^14, 2^15), unless it is 0; infinities and NaN stay what they are, in
+    // their own head.  up lies in [-113, 141]: two factors keep each a normal number.
+    const int up = bits ? 14 - ((int)(bits >> 23) - 127) : 0;
+    const int u0 = up / 2, u1 = up - u0;
+    const float f0 = __uint_as_float((uint32_t)(127 + u0) << 23), f1 = __uint_as_float((uint32_t)(127 + u1) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      x[e] = x[e] * f0 * f1;
+      sum += x[e];
+    }
+    // word i of K has dims 16 t + 8 i + (0..7), four bits each: those 4 apart share a register, and
+    // every second pair is 16 times too large
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float* y = x + 8 * i + 2 * j;
+        q[4 * i + 2 * j] = pack_f16x2(y[0], y[4]);
+        q[4 * i + 2 * j + 1] = pack_f16x2(y[1] * 0.0625f, y[5] * 0.0625f);
+      }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const float c = scale * 1.4426950408889634f;
+    const float d0 = __uint_as_float((uint32_t)(127 - u0) << 23), d1 = __uint_as_float((uint32_t)(127 - u1) << 23);
+    // from the head of the q that this lane has to that of its scores
+    fa = __shfl_sync(0xffffffffu, d0 * 0x1p24f, 8 * t);
+    fb = __shfl_sync(0xffffffffu, d1 * c, 8 * t);
+    fl = __shfl_sync(0xffffffffu, (sum * d0) * (d1 * c), 8 * t);
+    ref = kStart;
+    l = low = 0.f;
+    lift = kMostLift;
+#pragma unroll
+    for (int w4 = 0; w4 < 4; ++w4)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[w4][e] = 0.f;
+  }
+
+  // A block in shared memory, `live` of whose 16 slots are the sequence's.
+  __device__ __forceinline__ void page(uint32_t block, int live) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    const uint4 k = lds128(block + 16 * lane), v = lds128(block + kI4V + 16 * lane), sc = lds128(block + kI4Scales + 16 * g);
+    constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains
+    mma_f16(s0, k.x & kLow, k.z & kLow, k.x & kHigh, k.z & kHigh, q[0], q[1]);
+    mma_f16(s1, k.y & kLow, k.w & kLow, k.y & kHigh, k.w & kHigh, q[4], q[5]);
+    {
+      const uint32_t a = k.x >> 8, b = k.z >> 8, c = k.y >> 8, d = k.w >> 8;
+      mma_f16(s0, a & kLow, b & kLow, a & kHigh, b & kHigh, q[2], q[3]);
+      mma_f16(s1, c & kLow, d & kLow, c & kHigh, d & kHigh, q[6], q[7]);
+    }
+    // slots g and g + 8
+    float vs0 = bf16lo_to_f32(sc.z), vl0 = bf16hi_to_f32(sc.z), vs1 = bf16lo_to_f32(sc.w), vl1 = bf16hi_to_f32(sc.w);
+    float x0 = fmaf((s0[0] + s1[0]) * fa, bf16lo_to_f32(sc.x) * fb, bf16hi_to_f32(sc.x) * fl);
+    float x1 = fmaf((s0[2] + s1[2]) * fa, bf16lo_to_f32(sc.y) * fb, bf16hi_to_f32(sc.y) * fl);
+    if (live < PKV_PAGE_TOKENS) {  // what lies behind the sequence's end may be anything
+      if (g >= live) {
+        x0 = -INFINITY;
+        vs0 = vl0 = 0.f;
+      }
+      if (g + 8 >= live) {
+        x1 = -INFINITY;
+        vs1 = vl1 = 0.f;
+      }
+    }
+    if (__any_sync(0xffffffffu, fmaxf(x0, x1) > ref + 1.f)) {
+      float top = fmaxf(x0, x1);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float now = fmaxf(ref, ceilf(top));
+      const float keep = exp2_approx(ref - now);  // (a head whose reference stays: 1)
+      l *= keep;
+      // the lifted sums stay as they are, unless that lifts them too far
+      const float more = fminf(lift * exp2_approx(now - ref), kMostLift);
+      lower(more * keep / lift);
+      lift = more;
+      ref = now;
+    }
+    const float p0 = exp2_approx(x0 - ref), p1 = exp2_approx(x1 - ref);
+    l += p0 + p1;
+    float y0 = p0 * lift * vs0, y1 = p1 * lift * vs1, z0 = p0 * lift * vl0, z1 = p1 * lift * vl1;
+    if (__any_sync(0xffffffffu, fmaxf(fabsf(y0), fabsf(y1)) > 0x1p15f || fmaxf(fabsf(z0), fabsf(z1)) > 0x1p19f)) {
+      float top = fmaxf(fmaxf(p0 * fabsf(vs0), p1 * fabsf(vs1)), fmaxf(p0 * (0.0625f * fabsf(vl0)), p1 * (0.0625f * fabsf(vl1))));
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (top * lift > 0x1p15f) {  // (the same for all lanes of a head)
+        // 2^13 up to 2^14; top is above 2^-111
+        const float now = __uint_as_float((uint32_t)max(1, 127 + 13 + 127 - (int)(__float_as_uint(top) >> 23)) << 23);
+        lower(now / lift);
+        lift = now;
+        y0 = p0 * now * vs0;
+        y1 = p1 * now * vs1;
+        z0 = p0 * now * vl0;
+        z1 = p1 * now * vl1;
+      }
+      __syncwarp();
+    }
+    low += z0 + z1;
+    // rounded to fp16, and what that leaves
+    const uint32_t near = pack_f16x2(y0, y1);
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&near));
+    const uint32_t rest = pack_f16x2(y0 - r.x, y1 - r.y);
+    const uint32_t b0 = movmatrix_trans(__byte_perm(near, rest, 0x5410));
+    const uint32_t b1 = movmatrix_trans(__byte_perm(near, rest, 0x7632));
+    const uint32_t even[2] = {v.x, v.y}, odd[2] = {v.z, v.w};  // slots 2 t, 2 t + 1; and 8 more
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t a = j ? even[w] >> 8 : even[w], b = j ? odd[w] >> 8 : odd[w];
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(d, a & kLow, a & kHigh, b & kLow, b & kHigh, b0, b1);
+        float* to = o[2 * w + j];
+        const float2 u = add2(make_float2(to[0], to[1]), make_float2(d[0], d[1]));
+        const float2 z = add2(make_float2(to[2], to[3]), make_float2(d[2], d[3]));
+        to[0] = u.x;
+        to[1] = u.y;
+        to[2] = z.x;
+        to[3] = z.y;
+      }
+  }
+
+  __device__ __forceinline__ void lower(float by) {
+    low *= by;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[w][e] *= by;
+  }
+
+  // The means of dims 8 g .. 8 g + 7 of head t, times `unit`, and the logarithm of their weight.
+  __device__ __forceinline__ float finish(float (&x)[8], float unit) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+      low += __shfl_xor_sync(0xffffffffu, low, d);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l, down = unit / lift;  // (no page: 0)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      x[2 * w] = fmaf(o[w][0] + o[w][1], 0x1p24f, low) * inv * down;
+      x[2 * w + 1] = fmaf(o[w][2] + o[w][3], 0x1p20f, low) * inv * down;
+    }
+    return l == 0.f ? kStart : ref + __log2f(l);
+  }
+};
+
+__device__ __forceinline__ void write_row(uint16_t* out, int seq, int head, const float (&x)[8], bool bad) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (!bad)
+    v = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  *reinterpret_cast<uint4*>(out + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + t) * PKV_HEAD_DIM + 8 * g) = v;
+}
+
+// A warp's ring of blocks, filled by its own asynchronous copies.
+struct Ring {
+  uint32_t base;
+  int slot, next;  // worked on, and written next
+  __device__ __forceinline__ explicit Ring(uint32_t at) : base(at), slot(0), next(0) {}
+  __device__ __forceinline__ uint32_t at(int i) const { return base + i * kI4BlockBytes; }
+  __device__ __forceinline__ void copy(const uint8_t* block) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t dst = at(next) + 16 * lane;
+    const uint8_t* src = block + 16 * lane;
+    cp_async16(dst, src);
+    cp_async16(dst + 512, src + 512);
+    if (lane < 8) cp_async16(dst + 1024, src + 1024);
+  }
+  __device__ __forceinline__ void commit() {
+    cp_async_commit();
+    if (++next == kRing) next = 0;
+  }
+  // the oldest block has landed, for all lanes, and the one before it is no longer read
+  __device__ __forceinline__ uint32_t wait() {
+    cp_async_wait<kRing - 2>();
+    __syncwarp();
+    const uint32_t here = at(slot);
+    if (++slot == kRing) slot = 0;
+    return here;
+  }
+};
+
+struct Held {  // what a warp of the kernel for whole sequences has found: means and the logarithm of their weight
+  float o[PKV_GROUP][PKV_HEAD_DIM];
+  float weight[PKV_GROUP];
+  int bad;
+};
+
+// One sequence and KV head for each cluster of CTAs (of one or more): every warp takes every
+// (warps)-th page, and what they find is put together in shared memory, over the cluster's CTAs
+// too.  Nothing goes through global memory.
+__global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4DecodeParams p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ Held sum;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;
+  const int head = blockIdx.y, seq = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  bool refused;
+  const int pages = pages_of(p, seq, refused), len = __ldg(p.seq_lens + seq);
+  uint16_t* out = p.out + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP) * PKV_HEAD_DIM;
+  if (pages == 0) {
+    if (rank == 0 && warp == 0) reinterpret_cast<uint4*>(out)[lane] = make_uint4(0, 0, 0, 0);
+    if (refused && rank == 0 && threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+    return;
+  }
+  const int first = rank * kWarps + warp, stride = ctas * kWarps;
+  const int count = first < pages ? (pages - first + stride - 1) / stride : 0;
+  const int32_t* table = p.block_tables + (size_t)seq * p.bt_stride;
+  bool bad = false;
+  // ids of 32 pages, and of the 32 behind them under way
+  const auto ids = [&](int i) { return i + lane < count ? __ldg(table + first + (i + lane) * stride) : 0; };
+  int id = ids(0), coming = count > 32 ? ids(32) : 0;
+  uint4 raw[2];
+  Group::fetch(p, seq, head, raw);
+  Ring ring(smem_u32(dyn) + warp * (kRing * kI4BlockBytes));
+  const auto issue = [&](int i) {
+    if (i < count) {
+      if (i && (i & 31) == 0) {
+        id = coming;
+        coming = ids(i + 32);
+      }
+      int page = __shfl_sync(0xffffffffu, id, i & 31);
+      if (page < 0 || page >= p.num_pages) {
+        bad = true;
+        page = 0;
+      }
+      ring.copy(p.pool + ((size_t)page * kHeads + head) * kI4BlockBytes);
+    }
+    ring.commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
+  Group st;
+  st.start(raw, p.scale);
+  for (int i = 0; i < count; ++i) {
+    const uint32_t block = ring.wait();
+    st.page(block, min(PKV_PAGE_TOKENS, len - (first + i * stride) * PKV_PAGE_TOKENS));
+    issue(i + kRing - 1);
+  }
+  float x[8];
+  const float weight = st.finish(x, kMeanDown);
+  // into the warp's own ring, which nothing is on its way to any more
+  static_assert(sizeof(Held) <= kRing * kI4BlockBytes && kI4BlockBytes % 16 == 0, "room for what a warp found");
+  cp_async_wait<0>();
+  __syncwarp();
+  Held* mine = reinterpret_cast<Held*>(dyn + warp * (kRing * kI4BlockBytes));
+  {
+    const int g = lane >> 2, t = lane & 3;
+    float4* to = reinterpret_cast<float4*>(mine->o[t] + 8 * g);
+    to[0] = make_float4(x[0], x[1], x[2], x[3]);
+    to[1] = make_float4(x[4], x[5], x[6], x[7]);
+    if (g == 0) mine->weight[t] = weight;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+  const int h = threadIdx.x / PKV_HEAD_DIM, d = threadIdx.x % PKV_HEAD_DIM;
+  static_assert(kThreads == PKV_GROUP * PKV_HEAD_DIM, "a thread for each output");
+  const auto of = [&](int w) { return reinterpret_cast<const Held*>(dyn + w * (kRing * kI4BlockBytes)); };
+  float ref = kStart, o = 0.f, total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, of(w)->weight[h]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float scaled = exp2_approx(of(w)->weight[h] - ref);
+    o = fmaf(scaled, of(w)->o[h][d], o);
+    total += scaled;
+  }
+  if (ctas == 1) {
+    const float y = bad ? 0.f : o * (1.f / total) * kMeanUp, z = __shfl_down_sync(0xffffffffu, y, 1);
+    if (d % 2 == 0) *reinterpret_cast<uint32_t*>(out + threadIdx.x) = pack_bf16x2(y, z);
+    return;
+  }
+  sum.o[h][d] = o * (1.f / total);
+  if (d == 0) sum.weight[h] = ref + __log2f(total);
+  if (threadIdx.x == 0) sum.bad = bad;
+  cluster.sync();
+  // each CTA an equal part of the 256 outputs
+  const int per = kThreads / ctas;
+  if ((int)threadIdx.x < per) {
+    const int at = rank * per + threadIdx.x, hh = at / PKV_HEAD_DIM, dd = at % PKV_HEAD_DIM;
+    ref = kStart;
+    o = total = 0.f;
+    bad = false;
+    float weights[kMostCluster], means[kMostCluster];
+#pragma unroll
+    for (int c = 0; c < kMostCluster; ++c) {
+      const Held* other = cluster.map_shared_rank(&sum, c < ctas ? c : 0);
+      weights[c] = c < ctas ? other->weight[hh] : kStart;
+      means[c] = c < ctas ? other->o[hh][dd] : 0.f;
+      if (c < ctas) bad |= other->bad != 0;
+    }
+#pragma unroll
+    for (int c = 0; c < kMostCluster; ++c) ref = fmaxf(ref, weights[c]);
+#pragma unroll
+    for (int c = 0; c < kMostCluster; ++c) {
+      const float scaled = c < ctas ? exp2_approx(weights[c] - ref) : 0.f;
+      o = fmaf(scaled, means[c], o);
+      total += scaled;
+    }
+    const float y = bad ? 0.f : o * (1.f / total) * kMeanUp, z = __shfl_down_sync(0xffffffffu, y, 1);
+    if (dd % 2 == 0) *reinterpret_cast<uint32_t*>(out + at) = pack_bf16x2(y, z);
+  }
+  cluster.sync();  // nobody's shared memory goes while it is read
+}
+
+struct ShareSmem {
+  int sum[kWarps];
+  int first_seq, before;  // the sequence that the CTA's share begins in, and the pages before that
+  int list[kList];        // page ids, -1 for what cannot be one
+};
+
+// The pages of all sequences are one long list; every CTA takes an equal share of it, whatever the
+// lengths, one KV head per warp.  Parts of split sequences go to the workspace (split_merge.cuh).
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const Int4DecodeParams p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ ShareSmem sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+
+  // Where this CTA's share of the list of pages (below 2^30 of them) begins.
+  int begin, end, seq, page;
+  unsigned share;
+  const auto shares = [&](int total) {
+    share = max(((unsigned)total + gridDim.x - 1) / gridDim.x, (unsigned)p.min_pages);
+    begin = (int)min((unsigned)total, share * blockIdx.x);
+    end = min(total, begin + (int)share);
+  };
+  const auto record = [&](int s, int at, int n, bool refused) {
+    if (s % (int)gridDim.x != (int)blockIdx.x) return;
+    if (!p.by_cta) {
+      const int c0 = (int)((unsigned)at / share), c1 = n ? (int)((unsigned)(at + n - 1) / share) : c0;
+      p.span[s] = c0 == c1 ? make_int2(-1, -1) : make_int2(c0, c1);
+    }
+    if (n == 0) {
+      uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)s * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
+      for (int i = 0; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+      if (refused) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+    }
+  };
+  if (p.num_seqs <= 32) {  // every warp finds out by itself
+    bool refused = false;
+    const int n = lane < p.num_seqs ? pages_of(p, lane, refused) : 0;
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    shares(__shfl_sync(0xffffffffu, run, 31));
+    const int before = run - n;
+    const uint32_t here = __ballot_sync(0xffffffffu, before <= begin && begin < run);
+    seq = here ? __ffs(here) - 1 : 0;
+    page = begin - __shfl_sync(0xffffffffu, before, seq);
+    pdl_launch_dependents();
+    if (warp == 0 && lane < p.num_seqs) record(lane, before, n, refused);
+  } else {  // a thread's sequences, then the sums over all
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) {
+      bool refused;
+      mine += pages_of(p, s, refused);
+    }
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) sh.sum[warp] = run;
+    __syncthreads();
+    int before = run - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.sum[w];
+      total += sh.sum[w];
+    }
+    shares(total);
+    if (before <= begin && begin < before + mine) {
+      int at = before;
+      for (int s = s0; s < s1; ++s) {
+        bool refused;
+        const int n = pages_of(p, s, refused);
+        if (at <= begin && begin < at + n) {
+          sh.first_seq = s;
+          sh.before = at;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    seq = sh.first_seq;
+    page = begin - sh.before;
+    pdl_launch_dependents();
+    int at = before;
+    for (int s = s0; s < s1; ++s) {
+      bool refused;
+      const int n = pages_of(p, s, refused);
+      record(s, at, n, refused);
+      at += n;
+    }
+  }
+  if (begin >= end) {
+    if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = make_int2(-1, -1);
+    return;
+  }
+
+  const int head = warp;
+  Ring ring(smem_u32(dyn) + warp * (kRing * kI4BlockBytes));
+  int2 split = make_int2(-1, -1);  // the sequence that begins here and goes on, and its last CTA
+  bool refused, bad = false;
+  int pages = pages_of(p, seq, refused), len = __ldg(p.seq_lens + seq), from = page;
+  int list_seq = seq, list_page = page;
+  uint4 raw[2];
+  Group::fetch(p, seq, head, raw);
+  Group st;
+  st.start(raw, p.scale);
+  for (int at = begin; at < end;) {
+    const int stop = min(end, at + kList), items = stop - at;
+    if (at > begin) __syncthreads();  // the last ids are no longer read
+    for (int i = 0; i < items;) {     // the ids of the next pages, sequence by sequence
+      const int n = pages_of(p, list_seq, refused), some = min(n - list_page, items - i);
+      const int32_t* table = p.block_tables + (size_t)list_seq * p.bt_stride + list_page;
+      for (int j = threadIdx.x; j < some; j += kThreads) {
+        const int id = __ldg(table + j);
+        const bool ok = id >= 0 && id < p.num_pages;
+        sh.list[i + j] = ok ? id : -1;
+        if (!ok) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+      }
+      i += some;
+      list_page += some;
+      if (list_page == n) {
+        list_page = 0;
+        do ++list_seq;
+        while (list_seq < p.num_seqs && pages_of(p, list_seq, refused) == 0);
+      }
+    }
+    __syncthreads();
+    const auto issue = [&](int i) {
+      if (i < items) ring.copy(p.pool + ((size_t)max(sh.list[i], 0) * kHeads + head) * kI4BlockBytes);
+      ring.commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) issue(i);
+    for (int i = 0; i < items; ++i) {
+      const uint32_t block = ring.wait();
+      bad |= sh.list[i] < 0;
+      st.page(block, min(PKV_PAGE_TOKENS, len - page * PKV_PAGE_TOKENS));
+      issue(i + kRing - 1);
+      ++page;
+      ++at;
+      if (page < pages && at < end) continue;
+      // the end of the sequence, or of the share inside it
+      float x[8];
+      const bool all = from == 0 && page == pages;
+      const float weight = st.finish(x, all ? 1.f : kMeanDown);
+      if (all) {
+        write_row(p.out, seq, head, x, bad);
+      } else {
+        const int g = lane >> 2, t = lane & 3, hq = head * PKV_GROUP + t;
+        float* part = p.parts + ((size_t)blockIdx.x * 2 + (from > 0 ? 0 : 1)) * kPartFloats;
+        float4* to = reinterpret_cast<float4*>(part + hq * PKV_HEAD_DIM + 8 * g);
+        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+        to[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (g == 0)
+          *reinterpret_cast<float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * hq) = make_float2(weight, bad ? kNothing : 1.f);
+        if (from == 0) split = make_int2(seq, (int)((unsigned)(at - page + pages - 1) / share));
+      }
+      if (at < end) {
+        do ++seq;
+        while (seq < p.num_seqs && (pages = pages_of(p, seq, refused)) == 0);
+        len = __ldg(p.seq_lens + seq);
+        page = from = 0;
+        bad = false;
+        Group::fetch(p, seq, head, raw);
+        st.start(raw, p.scale);
+      }
+    }
+    cp_async_wait<0>();
+    ring = Ring(ring.base);
+    __syncwarp();
+  }
+  if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = split;
+}
+
+constexpr int kSmemBytes = kWarps * kRing * kI4BlockBytes;
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" size_t paged_gqa_decode_int4_workspace_bytes(int num_seqs) {
+  if (num_seqs < 0 || num_seqs > kMaxSeqsInt4) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  const int sms = sm_count(dev);
+  if (sms <= 0) return 0;
+  return parts_bytes(sms * kCtasPerSm) + span_bytes(sms * kCtasPerSm, num_seqs);
+}
+
+extern "C" int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num_pages, const int32_t* block_tables,
+                                     int bt_row_stride, int max_blocks, const int32_t* seq_lens, int num_seqs,
+                                     int max_seq_len, void* out, float scale, void* workspace,
+                                     size_t workspace_bytes, int* d_err, void* stream) {
+  if (num_seqs < 0 || num_pages < 1 || max_blocks < 1 || bt_row_stride < max_blocks || max_seq_len < 0 || !isfinite(scale))
+    return PKV_ERR_INVALID_ARGUMENT;
+  if (num_seqs == 0) return PKV_OK;
+  if (!q || !kv_pool || !block_tables || !seq_lens || !out || !workspace) return PKV_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
+        reinterpret_cast<uintptr_t>(d_err)) & 3u))
+    return PKV_ERR_MISALIGNED;
+  if (num_seqs > kMaxSeqsInt4 || (long long)max_blocks * num_seqs >= (1ll << 30)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  int dev = 0;
+  int rc = bind_stream_device(stream, &dev);
+  if (rc != PKV_OK) return rc;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
+  const int most = sms * kCtasPerSm;
+  if (workspace_bytes < parts_bytes(most) + span_bytes(most, num_seqs)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+
+  Int4DecodeParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.pool = static_cast<const uint8_t*>(kv_pool);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.parts = static_cast<float*>(workspace);
+  p.span = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + parts_bytes(most));
+  p.d_err = d_err;
+  p.scale = scale;
+  p.num_pages = num_pages;
+  p.bt_stride = bt_row_stride;
+  p.max_blocks = max_blocks;
+  p.num_seqs = num_seqs;
+  p.min_pages = kMinPages;
+
+  const long long longest = max_seq_len > 0 ? max_seq_len : (long long)max_blocks * PKV_PAGE_TOKENS;
+  const long long most_pages = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
+  const bool whole = most_pages * num_seqs <= 64ll * 128 && most_pages <= 256;
+  int ctas = 1;
+  while (ctas < kMostCluster && (long long)num_seqs * kHeads * ctas * 2 <= 2 * sms && most_pages > ctas * kWarps) ctas *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  if (whole) {
+    p.by_cta = 0;
+    cfg.gridDim = dim3((unsigned)ctas, kHeads, (unsigned)num_seqs);
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, int4_whole_kernel, p), "cudaLaunchKernelEx(decode int4)");
+  }
+  p.by_cta = num_seqs > kBySequence;
+  long long shares = (most_pages * num_seqs + kMinPages - 1) / kMinPages;
+  if (shares > most) shares = most;
+  if (shares < 1) shares = 1;
+  cfg.gridDim = dim3((unsigned)shares);
+  cfg.numAttrs = 1;
+  rc = cuda_status(cudaLaunchKernelEx(&cfg, int4_share_kernel, p), "cudaLaunchKernelEx(decode int4)");
+  if (rc != PKV_OK || shares == 1) return rc;  // one CTA splits nothing
+  return launch_merge(cfg, p.parts, p.span, p.out, num_seqs, (int)shares, p.by_cta, sms, kMeanUp, "cudaLaunchKernelEx(merge int4)");
+}
