@@ -819,6 +819,45 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
                        const uint32_t* allow_mask, long long mask_stride, void* stream);
 
 /* ------------------------------------------------------------------------
+ * pkv_sample_logits - the next token of each row, drawn from the softmax of
+ * logits / temperature restricted by top-k, top-p and min-p, from given random
+ * numbers.
+ *
+ * Row r with temperature T > 0, w_i = exp((x_i - max x) / T) over the tokens whose
+ * logit is not NaN, Z = sum w; tokens are ranked by logit, ties by id.  Token i
+ * is kept if all three hold (the limits look at the same distribution, so that
+ * their order does not matter):
+ *   top_k   its rank is below top_k[r]             (top_k <= 0: no limit)
+ *   top_p   the w of the tokens ranked before it sum to less than top_p[r] Z
+ *           (the first one is always kept; top_p >= 1: no limit)
+ *   min_p   w_i >= min_p[r]                        (the first one is always kept)
+ * and the kept token with the largest w_i / noise[r][i] is drawn (the first one
+ * of equals), which follows the kept tokens' distribution when the noise holds
+ * independent exponential variates.  A noise value below 2^-126 or a NaN counts
+ * as 2^-126, infinity as the largest number.  Tokens of logit -inf are never drawn; where the largest logit is
+ * +inf, the tokens that have it count as w = 1, all others as 0.
+ * T = 0 takes the first largest logit.  out_ids[r] = -1 if no logit is above
+ * -inf, or if T is negative, infinite or NaN, or top_p or min_p NaN.
+ * log_probs[r] = (x - max x) / T - log Z of the token drawn, before the limits
+ * (with T = 1 where T = 0); NaN for id -1.
+ *   logits       device [rows][row_stride], PKV_LOGITS_F32 / BF16 / F16
+ *   noise        device float [rows][noise_stride], noise_stride >= vocab; not
+ *                read for rows with T = 0; may be NULL if no row draws
+ *                (temperature given as NULL is 1 for every row: noise needed)
+ *   temperature  device float [rows] or NULL (1)
+ *   top_k        device int32 [rows] or NULL
+ *   top_p, min_p device float [rows] or NULL
+ *   out_ids      device int32 [rows]
+ *   log_probs    device float [rows] or NULL
+ * One cluster of up to 8 CTAs per row; sums in a fixed order, so a call gives the
+ * same result every time.  Host-side checks only (no device error).
+ * ---------------------------------------------------------------------- */
+int pkv_sample_logits(const void* logits, int dtype, int rows, int vocab, long long row_stride,
+                      const float* noise, long long noise_stride, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p,
+                      int32_t* out_ids, float* log_probs, void* stream);
+
+/* ------------------------------------------------------------------------
  * Pages handed out and taken back on the GPU, for decode loops that do not
  * return to the host between steps (one captured graph replayed, say): what
  * pkv_sched_grow and pkv_sched_finish do to block tables and the stack of free

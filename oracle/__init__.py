@@ -27,6 +27,7 @@ to check by eye, in FP64 NumPy with per-element loops where that is clearer:
 * ``int4_kv``    pages of 4-bit codes with a scale and a minimum for each row: the
                  append and attention over them.
 * ``logits``     penalties, biases and masks on logits, and the next token.
+* ``sampling``   the next token drawn under top-k, top-p and min-p.
 * ``page_stack`` block tables that grow and shrink by a stack of free pages.
 * ``admission``  the admission-credit rule and a FIFO continuous-batching
                  simulation with on-demand page allocation.
@@ -47,4 +48,4 @@ Sources (titles of the pages that define the path):
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 (closed forms, invariants, brute force, library routines); none is unpinned.
 """
-from . import admission, argmax, bf16, bs8_kv, int4_kv, int8_kv, logits, norm_rope, page_stack, paged_kv, rope  # noqa: F401
+from . import admission, argmax, bf16, bs8_kv, int4_kv, int8_kv, logits, norm_rope, page_stack, paged_kv, rope, sampling  # noqa: F401

@@ -116,6 +116,7 @@ _SIGS = {
     "kv_read_int4": (_i, [_p, _i, _p, _i, _p, _p, _p]),
     "paged_gqa_decode_int4_workspace_bytes": (_sz, [_i]),
     "paged_gqa_decode_int4": (_i, [_p, _p, _i, _p, _i, _i, _p, _i, _i, _p, _f, _p, _sz, _p, _p]),
+    "pkv_sample_logits": (_i, [_p, _i, _i, _i, _ll, _p, _ll, _p, _p, _p, _p, _p, _p, _p]),
     "pkv_grow_block_tables": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p, _p, _p,
                                    _i, _p, _p]),
     "pkv_release_pages": (_i, [_p, _p, _i, _p, _i, _ll, _i, _i, _p, _i, _p, _p, _p, _p, _p]),
@@ -1338,6 +1339,50 @@ def process_logits(logits, out=None, ids=None, history=None, history_lens=None, 
     _call(dev, stream, "pkv_process_logits", (logits.data_ptr(), dtype, rows, vocab,
           stride[0] if rows > 1 else vocab, dst, out_stride, id_ptr, hist, H, h_lens, p_lens, rep, pres, freq,
           b_ids, b_vals, B, mask, mask_stride))
+    return ids
+
+
+def sample_logits(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, logprobs=None,
+                  stream=None):
+    """The next token of each row, drawn from softmax(logits / temperature)
+    restricted by top-k, top-p and min-p; returns ids ([rows] int32, -1 where
+    nothing can be drawn).
+
+    logits [rows, vocab] fp32, bf16 or fp16, e.g. what process_logits wrote.
+    noise [rows, vocab] fp32: independent exponential variates
+    (``torch.empty(...).exponential_()``); the kept token with the largest
+    weight / noise is drawn.  Row strides may exceed vocab.  temperature, top_p,
+    min_p [rows] fp32 and top_k [rows] int32 (None: 1, or no limit); temperature
+    0 takes the largest logit, and noise may be None where no row draws.  All
+    three limits look at the same distribution (pkv.h).  logprobs [rows] fp32
+    gets the token's log-probability under softmax(logits / temperature)."""
+    dev = _on_device(logits, "logits")
+    shape, stride, dtype = logits.shape, logits.stride(), LOGITS_DTYPES.get(logits.dtype)
+    if dtype is None or len(shape) != 2:
+        raise TypeError("logits must be a 2-D float32, bfloat16 or float16 tensor")
+    rows, vocab = shape
+    if vocab < 1 or (stride[1] != 1 and vocab > 1):
+        raise ValueError("logits rows must be contiguous and not empty")
+    chance, chance_stride = None, 0
+    if noise is None:
+        if temperature is None and rows:
+            raise ValueError("noise is needed unless every temperature is 0")
+    else:
+        if getattr(noise, "dtype", None) is not _F32:
+            raise TypeError("noise must be a float32 tensor")
+        chance_stride = noise.stride()
+        if noise.device != dev or noise.shape != shape or (chance_stride[1] != 1 and vocab > 1):
+            raise ValueError("noise must be [rows, vocab] on the logits' device with contiguous rows")
+        chance, chance_stride = noise.data_ptr(), chance_stride[0] if rows > 1 else vocab
+    temp = _opt(temperature, "temperature", _F32, dev, rows)
+    k = _opt(top_k, "top_k", _I32, dev, rows)
+    p, floor = _opt(top_p, "top_p", _F32, dev, rows), _opt(min_p, "min_p", _F32, dev, rows)
+    if ids is None:
+        ids = _empty(rows, _I32, dev, stream)
+    id_ptr, lp = _vec(ids, "ids", _I32, dev, rows), _opt(logprobs, "logprobs", _F32, dev, rows)
+    if rows:
+        _call(dev, stream, "pkv_sample_logits", (logits.data_ptr(), dtype, rows, vocab, stride[0] if rows > 1 else vocab,
+              chance, chance_stride, temp, k, p, floor, id_ptr, lp))
     return ids
 
 

@@ -1,0 +1,678 @@
+// The next token of each row, drawn from softmax(logits / temperature) restricted by
+// top-k, top-p and min-p, from given exponential variates (sm_103a).
+//
+// With w_i = 2^(c (x_i - max x)), c = log2(e) / T, the token drawn is the kept one with
+// the largest w_i / e_i: the race of independent exponentials, which follows the kept
+// tokens' distribution.  Which tokens are kept needs no sorting.  The kept ones are the
+// first so many by rank, so
+//   - the winner of the race among all candidates is the answer if it is kept: the
+//     tokens ranked before it are fewer than k, their w sum to less than p Z, and its own
+//     w reaches the floor -- one pass of counting and adding;
+//   - else nothing behind it is kept either, and the race goes on among the tokens ranked
+//     before it.
+// A rejected winner is a random token of what is left, so a few rounds are enough; noise
+// that is made to take many is met by bisecting for the last kept token after kRounds.
+//
+// Candidates: k tokens are at least as large as the smallest of the warps' q-th largest
+// thread maxima when there are k / q warps; min-p bounds the logits by max x; for top-p
+// the same bound is tried, and holds if the tokens above it have p of the sum.  So there
+// are usually a few hundred candidates in a row, listed in shared memory warp by warp in
+// order, and only their noise is read.  Where the lists overflow, or without limits, the
+// passes go over all logits.
+//
+// A cluster of CTAs has a row: each holds a part of it in shared memory (read once), and
+// after every pass sends its sums and its best to the others, behind a cluster barrier.
+// Sums are over fixed positions in a fixed order; ties of a race go to the lowest id.
+//
+// Bound: memory, the logits read once, and the noise once where there are no limits.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "pkv.h"
+#include "ptx.cuh"
+
+namespace pkv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostCtas = 8;
+constexpr int kLeast = 4096;         // tokens of a CTA that make another one worth its barrier
+constexpr int kMostHeld = 100 << 10;  // bytes of logits in a CTA's shared memory
+constexpr int kList = 64;            // candidates of a warp
+constexpr int kMostQ = 16;
+constexpr int kTryQ = 4;             // of the bound tried for top-p
+constexpr int kRounds = 12;
+
+struct SampleParams {
+  const void* logits;
+  const float* noise;
+  long long stride, noise_stride;
+  const float *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  int32_t* ids;
+  float* log_probs;
+  int vocab, ctas;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <class T>
+struct Wide;
+template <>
+struct Wide<float> {
+  static constexpr int kN = 4;
+  __device__ static void widen(const uint4& a, float (&x)[4]) {
+    x[0] = __uint_as_float(a.x);
+    x[1] = __uint_as_float(a.y);
+    x[2] = __uint_as_float(a.z);
+    x[3] = __uint_as_float(a.w);
+  }
+  __device__ static float one(float x) { return x; }
+};
+template <>
+struct Wide<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  __device__ static void widen(const uint4& a, float (&x)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = bf16lo_to_f32(w[e]);
+      x[2 * e + 1] = bf16hi_to_f32(w[e]);
+    }
+  }
+  __device__ static float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+};
+template <>
+struct Wide<__half> {
+  static constexpr int kN = 8;
+  __device__ static void widen(const uint4& a, float (&x)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+  __device__ static float one(__half x) { return __half2float(x); }
+};
+
+// NaN as -inf, +inf as the largest number: differences are never NaN where one is finite.
+__device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+__device__ __forceinline__ float tame_noise(float e) { return fminf(fmaxf(e, 0x1p-126f), FLT_MAX); }
+
+// Floats in order as unsigned numbers, and back.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// What a warp, a CTA and a row have found in a pass.
+struct Found {
+  float max, sum, bound;      // first pass: largest logit, sum of w under that maximum, the bound
+  float race, x;              // the race: its best and that token's logit
+  int id;
+  float mass;                 // check: of the tokens ranked before the pivot
+  int count, overflow;
+};
+
+struct Pivot {
+  float x;
+  int id;
+  __device__ __forceinline__ bool before(float y, int i) const { return y > x || (y == x && i < id); }
+};
+
+struct Smem {
+  Found warps[kWarps];
+  Found rows[2][kMostCtas];  // of all CTAs, for every second pass
+  float x[kWarps][kList];
+  int id[kWarps][kList];
+};
+
+template <class T, bool kHeld>
+struct Row {
+  static constexpr int kN = Wide<T>::kN;
+  static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
+  const SampleParams& p;
+  Smem& sh;
+  uint4* held;               // the part's logits, if they are held
+  const T* logits;
+  const float* noise;
+  int head, vectors, v0, v1;  // tokens before the first 16-byte boundary; whole vectors, and this CTA's
+  int rank, turn;
+  bool wide_noise;
+
+  __device__ Row(const SampleParams& q, Smem& s, uint4* h) : p(q), sh(s), held(h), turn(0) {
+    const int r = blockIdx.x / p.ctas;
+    rank = blockIdx.x % p.ctas;
+    logits = static_cast<const T*>(p.logits) + (long long)r * p.stride;
+    noise = p.noise ? p.noise + (long long)r * p.noise_stride : nullptr;
+    head = min(p.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(logits) & 15)) % 16 / sizeof(T)));
+    vectors = (p.vocab - head) / kN;
+    const int per = (vectors + p.ctas - 1) / p.ctas;
+    v0 = min(vectors, rank * per);
+    v1 = min(vectors, v0 + per);
+    wide_noise = (reinterpret_cast<uintptr_t>(noise + head) & 15) == 0;
+  }
+  // the tokens beside the vectors: one each for the first threads of the first CTA
+  __device__ __forceinline__ int extra() const {
+    const int loose = head + (p.vocab - head - vectors * kN);
+    if (rank != 0 || (int)threadIdx.x >= loose) return -1;
+    return (int)threadIdx.x < head ? (int)threadIdx.x : (int)threadIdx.x + vectors * kN;
+  }
+  __device__ __forceinline__ void vector(int v, float (&x)[kN]) const {
+    const uint4 raw = kHeld ? held[v - v0] : __ldg(reinterpret_cast<const uint4*>(logits + head) + v);
+    Wide<T>::widen(raw, x);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) x[e] = tame(x[e]);
+  }
+  // f(x, id) for every logit of this thread, always in the same order
+  template <class F>
+  __device__ __forceinline__ void every(const F& f) const {
+    const int i = extra();
+    if (i >= 0) f(tame(Wide<T>::one(logits[i])), i);
+    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+      float x[kN];
+      vector(v, x);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) f(x[e], head + v * kN + e);
+    }
+  }
+
+  // This CTA's Found to every CTA of the cluster; theirs are in the array returned.
+  __device__ const Found* exchange(const Found& mine) {
+    const cg::cluster_group cluster = cg::this_cluster();
+    Found* to = &sh.rows[turn][rank];
+    if (p.ctas == 1) {
+      if (threadIdx.x == 0) *to = mine;
+      __syncthreads();
+    } else {
+      if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = mine;
+      cluster.sync();
+    }
+    turn ^= 1;
+    return sh.rows[turn ^ 1];
+  }
+};
+
+__device__ __forceinline__ bool better(float r, int i, float than, int id) {
+  return r > than || (r == than && i < id);
+}
+
+// A thread's best of the race to that of the CTA, with the sums of a check.
+__device__ __forceinline__ Found gather(Smem& sh, float race, float x, int id, float mass, int count, bool overflow) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float r2 = __shfl_xor_sync(0xffffffffu, race, o), x2 = __shfl_xor_sync(0xffffffffu, x, o);
+    const int i2 = __shfl_xor_sync(0xffffffffu, id, o);
+    if (better(r2, i2, race, id)) {
+      race = r2;
+      x = x2;
+      id = i2;
+    }
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  overflow = __any_sync(0xffffffffu, overflow);
+  __syncthreads();  // what the last pass left here has been read
+  if (lane == 0) {
+    Found& f = sh.warps[warp];
+    f.race = race;
+    f.x = x;
+    f.id = id;
+    f.mass = mass;
+    f.count = count;
+    f.overflow = overflow;
+  }
+  __syncthreads();
+  Found all = sh.warps[0];
+#pragma unroll 4
+  for (int w = 1; w < kWarps; ++w) {
+    const Found& f = sh.warps[w];
+    if (better(f.race, f.id, all.race, all.id)) {
+      all.race = f.race;
+      all.x = f.x;
+      all.id = f.id;
+    }
+    all.mass += f.mass;
+    all.count += f.count;
+    all.overflow |= f.overflow;
+  }
+  return all;
+}
+
+__device__ __forceinline__ Found merge(const Found* rows, int ctas) {
+  Found all = rows[0];
+  for (int c = 1; c < ctas; ++c) {
+    const Found& f = rows[c];
+    if (better(f.race, f.id, all.race, all.id)) {
+      all.race = f.race;
+      all.x = f.x;
+      all.id = f.id;
+    }
+    all.mass += f.mass;
+    all.count += f.count;
+    all.overflow |= f.overflow;
+  }
+  return all;
+}
+
+template <class T, bool kHeld>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+  extern __shared__ uint4 held[];
+  __shared__ Smem sh;
+  using R = Row<T, kHeld>;
+  constexpr int kN = R::kN;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_id = blockIdx.x / p.ctas;
+  // no CTA writes into another's shared memory before that one runs
+  if (p.ctas > 1) cg::this_cluster().barrier_arrive();
+  pdl_wait();
+  pdl_launch_dependents();
+  R row(p, sh, held);
+  const float temp = p.temperature ? p.temperature[row_id] : 1.f;
+  const float top_p = p.top_p ? p.top_p[row_id] : 1.f, floor = p.min_p ? p.min_p[row_id] : 0.f;
+  const int want_k = p.top_k ? p.top_k[row_id] : 0;
+  const bool greedy = temp == 0.f;
+  const auto answer = [&](int id, float lp) {
+    if (row.rank == 0 && threadIdx.x == 0) {
+      p.ids[row_id] = id;
+      if (p.log_probs) p.log_probs[row_id] = lp;
+    }
+  };
+  if (!(temp >= 0.f && temp < INFINITY) || top_p != top_p || floor != floor || (!greedy && !p.noise)) {
+    answer(-1, NAN);
+    if (p.ctas > 1) cg::this_cluster().barrier_wait();
+    return;
+  }
+  const float c = greedy ? 1.4426950408889634f : fminf(1.4426950408889634f / temp, FLT_MAX);
+  const int limit = want_k > 0 && want_k < p.vocab ? want_k : INT_MAX;
+
+  // First pass: the largest logit and the sum of w.
+  float top = -FLT_MAX, sum = 0.f;
+  const auto take = [&](const float* x, int n) {
+    float most = x[0];
+#pragma unroll
+    for (int e = 1; e < n; ++e) most = fmaxf(most, x[e]);
+    if (most > top) {
+      sum *= exp2_approx((top - most) * c);
+      top = most;
+    }
+#pragma unroll
+    for (int e = 0; e < n; ++e) sum += exp2_approx((x[e] - top) * c);
+  };
+  {
+    const int i = row.extra();
+    if (i >= 0) {
+      const float x[1] = {tame(Wide<T>::one(row.logits[i]))};
+      take(x, 1);
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(row.logits + row.head);
+    for (int v = row.v0 + threadIdx.x; v < row.v1; v += R::kBatch * kThreads) {
+      uint4 raw[R::kBatch];
+#pragma unroll
+      for (int u = 0; u < R::kBatch; ++u)
+        if (v + u * kThreads < row.v1) raw[u] = __ldg(src + v + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < R::kBatch; ++u) {
+        if (v + u * kThreads >= row.v1) break;
+        if (kHeld) held[v + u * kThreads - row.v0] = raw[u];
+        float x[kN];
+        Wide<T>::widen(raw[u], x);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x[e] = tame(x[e]);
+        take(x, kN);
+      }
+    }
+  }
+  // the q-th largest of the warp's thread maxima: with that many in every warp, at least `limit`
+  const int teams = kWarps * p.ctas;
+  const bool by_k = limit != INT_MAX && (limit + teams - 1) / teams <= kMostQ;
+  const bool by_p = top_p < 1.f;
+  const int q = greedy ? 0 : by_k ? (limit + teams - 1) / teams : by_p ? kTryQ : 0;
+  float bound = -INFINITY;
+  {
+    uint32_t key = key_of(top);
+    for (int i = 0; i < q; ++i) {
+      const uint32_t most = __reduce_max_sync(0xffffffffu, key);
+      bound = of_key(most);
+      const uint32_t who = __ballot_sync(0xffffffffu, key == most);
+      if (lane == __ffs(who) - 1) key = 0;
+    }
+  }
+  {
+    float m = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s = sum * exp2_approx((top - m) * c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      sh.warps[warp].max = m;
+      sh.warps[warp].sum = s;
+      sh.warps[warp].bound = bound;
+    }
+  }
+  __syncthreads();
+  Found mine = {};
+  mine.max = -FLT_MAX;
+  mine.bound = INFINITY;
+  for (int w = 0; w < kWarps; ++w) {
+    mine.max = fmaxf(mine.max, sh.warps[w].max);
+    mine.bound = fminf(mine.bound, sh.warps[w].bound);
+  }
+  for (int w = 0; w < kWarps; ++w) mine.sum = fmaf(sh.warps[w].sum, exp2_approx((sh.warps[w].max - mine.max) * c), mine.sum);
+  if (p.ctas > 1) cg::this_cluster().barrier_wait();
+  const Found* all = row.exchange(mine);
+  float most = -FLT_MAX, z = 0.f;
+  bound = INFINITY;
+  for (int i = 0; i < p.ctas; ++i) {
+    most = fmaxf(most, all[i].max);
+    bound = fminf(bound, all[i].bound);
+  }
+  for (int i = 0; i < p.ctas; ++i) z = fmaf(all[i].sum, exp2_approx((all[i].max - most) * c), z);
+  if (z == 0.f) {  // nothing above -inf
+    answer(-1, NAN);
+    return;
+  }
+  const auto finish = [&](const Found& f) {
+    answer(f.id, (greedy ? f.x - most : (f.x - most) / temp) - logf(z));
+  };
+
+  if (greedy) {
+    int first = INT_MAX;
+    row.every([&](float x, int i) {
+      if (x == most) first = min(first, i);
+    });
+    finish(merge(row.exchange(gather(sh, first == INT_MAX ? -INFINITY : 0.f, most, first, 0.f, 0, false)), p.ctas));
+    return;
+  }
+
+  // Second pass: candidates from `bound` on, listed, and their race.
+  const bool by_floor = floor > 0.f;
+  if (!by_k && !by_p) bound = -INFINITY;
+  const bool tried = by_p && !by_k;  // holds only if the tokens from the bound on have the mass
+  float sure = by_k ? bound : -INFINITY;
+  if (by_floor) {  // a little below what the floor's comparison of w decides
+    const float y = (log2f(fminf(floor, 1.f)) - 0x1p-12f) / c;
+    sure = fmaxf(sure, most + (y - fabsf(most) * 0x1p-20f));
+    bound = fmaxf(bound, sure);
+  }
+  const auto score = [&](float x, float e) { return (x - most) * c - __log2f(e); };
+  // a thread's best, its race computed with the accurate logarithm
+  const auto exactly = [&](float x, float e) { return (x - most) * c - log2f(e); };
+  float race = -INFINITY, best_x = -INFINITY, best_e = 1.f;
+  int best = INT_MAX;
+  const auto run = [&](float x, int i, float e) {
+    const float r = score(x, e);
+    if (better(r, i, race, best)) {
+      race = r;
+      best_x = x;
+      best_e = e;
+      best = i;
+    }
+  };
+  const auto best_of_thread = [&]() { race = best == INT_MAX ? -INFINITY : exactly(best_x, best_e); };
+  // the race over all logits from `least` on that are ranked before the pivot
+  const auto race_all = [&](float least, const Pivot& at) {
+    race = best_x = -INFINITY;
+    best = INT_MAX;
+    const auto in = [&](float x, int i) { return x >= least && at.before(x, i); };
+    const int i = row.extra();
+    if (i >= 0) {
+      const float x = tame(Wide<T>::one(row.logits[i]));
+      if (in(x, i)) run(x, i, tame_noise(row.noise[i]));
+    }
+    constexpr int kSteps = 2;
+    for (int v = row.v0 + threadIdx.x; v < row.v1; v += kSteps * kThreads) {
+      float e[kSteps][kN], x[kSteps][kN];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const int vu = v + u * kThreads;
+        if (vu >= row.v1) break;
+        row.vector(vu, x[u]);
+        const int id = row.head + vu * kN;
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) any |= in(x[u][j], id + j);
+        if (!any) continue;
+        if (row.wide_noise) {
+#pragma unroll
+          for (int j = 0; j < kN; j += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(row.noise + id + j));
+            e[u][j] = f.x;
+            e[u][j + 1] = f.y;
+            e[u][j + 2] = f.z;
+            e[u][j + 3] = f.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) e[u][j] = __ldg(row.noise + id + j);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const int vu = v + u * kThreads;
+        if (vu >= row.v1) break;
+        const int id = row.head + vu * kN;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (in(x[u][j], id + j)) run(x[u][j], id + j, tame_noise(e[u][j]));
+      }
+    }
+    best_of_thread();
+  };
+
+  bool listed = bound > -INFINITY;
+  int here = 0;  // candidates of this warp
+  Found now = {};
+  if (listed) {
+    float mass = 0.f;
+    bool overflow = false;
+    const auto list = [&](bool hit, float x, int i) {
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      const int at = here + __popc(hits & ((1u << lane) - 1u));
+      if (hit) {
+        mass += exp2_approx((x - most) * c);
+        if (at < kList) {
+          sh.x[warp][at] = x;
+          sh.id[warp][at] = i;
+          run(x, i, tame_noise(__ldg(row.noise + i)));
+        }
+      }
+      here += __popc(hits);
+    };
+    const int i = row.extra();
+    const float loose = i >= 0 ? tame(Wide<T>::one(row.logits[i])) : -INFINITY;
+    list(i >= 0 && loose >= bound, loose, i);
+    for (int v = row.v0 + threadIdx.x; v - lane < row.v1 && here <= kList; v += kThreads) {
+      float x[kN];
+      bool any = false;
+      if (v < row.v1) {
+        row.vector(v, x);
+        float m = x[0];
+#pragma unroll
+        for (int j = 1; j < kN; ++j) m = fmaxf(m, x[j]);
+        any = m >= bound;
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) list(any && x[j] >= bound, any ? x[j] : 0.f, row.head + v * kN + j);
+    }
+    overflow = here > kList;
+    here = min(here, kList);
+    best_of_thread();
+    now = merge(row.exchange(gather(sh, race, best_x, best, mass, 0, overflow)), p.ctas);
+    // (where the sums of w before the bound reach p Z, but for their rounding)
+    listed = !now.overflow && (!tried || bound == sure || now.mass >= top_p * z * (1.f + 0x1p-18f));
+  }
+  if (!listed) {
+    race_all(sure, Pivot{-INFINITY, INT_MAX});
+    now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
+  }
+  if (limit == INT_MAX && !by_p && !by_floor) {
+    finish(now);
+    return;
+  }
+
+  // Rounds: is the winner kept?  Else the race among those ranked before it.
+  const auto kept = [&](float x, int count, float mass) {
+    return count == 0 || (count < limit && (!by_p || mass < top_p * z) && (!by_floor || exp2_approx((x - most) * c) >= floor));
+  };
+  // the tokens before the pivot, and with `again` their race
+  const auto check = [&](const Pivot& at, bool again) {
+    float mass = 0.f;
+    int count = 0;
+    race = best_x = -INFINITY;
+    best = INT_MAX;
+    if (listed) {
+      for (int j = lane; j < here; j += 32) {
+        const float x = sh.x[warp][j];
+        const int i = sh.id[warp][j];
+        if (!at.before(x, i)) continue;
+        mass += exp2_approx((x - most) * c);
+        ++count;
+        if (again) run(x, i, tame_noise(__ldg(row.noise + i)));
+      }
+      best_of_thread();
+    } else {
+      row.every([&](float x, int i) {
+        if (!at.before(x, i)) return;
+        mass += exp2_approx((x - most) * c);
+        ++count;
+      });
+    }
+    return merge(row.exchange(gather(sh, race, best_x, best, mass, count, false)), p.ctas);
+  };
+  Pivot at{now.x, now.id};
+  for (int round = 0; round < kRounds; ++round) {
+    at = Pivot{now.x, now.id};
+    const Found f = check(at, true);
+    if (kept(at.x, f.count, f.mass)) {
+      finish(now);
+      return;
+    }
+    if (listed) {
+      now = f;
+    } else {
+      race_all(sure, at);
+      now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
+    }
+  }
+  // The last kept place by bisection, first the logit, then the id: (hi, 0) is kept, (lo, 0), behind
+  // the last winner that was not, is not.
+  uint32_t lo = key_of(at.x) - 1, hi = key_of(most);
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const Found f = check(Pivot{of_key(mid), 0}, false);
+    if (kept(of_key(mid), f.count, f.mass))
+      hi = mid;
+    else
+      lo = mid;
+  }
+  int in = 0, out = p.vocab;  // the place (hi, in) is kept, (hi, out) is not or there is none
+  while (out - in > 1) {
+    const int mid = in + (out - in) / 2;
+    const Found f = check(Pivot{of_key(hi), mid}, false);
+    if (kept(of_key(hi), f.count, f.mass))
+      in = mid;
+    else
+      out = mid;
+  }
+  const Pivot last{of_key(hi), in + 1};  // before this: everything kept
+  if (listed) {
+    now = check(last, true);
+  } else {
+    race_all(sure, last);
+    now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
+  }
+  finish(now);
+}
+
+template <class T>
+int launch(const SampleParams& p, cudaLaunchConfig_t cfg) {
+  const size_t part = ((size_t)p.vocab / Wide<T>::kN + p.ctas - 1) / p.ctas * 16;
+  const bool held = part <= kMostHeld;
+  cfg.dynamicSmemBytes = held ? part : 0;
+  auto* kernel = held ? sample_kernel<T, true> : sample_kernel<T, false>;
+  if (held) {
+    const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld),
+                               "cudaFuncSetAttribute(sample)");
+    if (rc != PKV_OK) return rc;
+  }
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(sample)");
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_sample_logits(const void* logits, int dtype, int rows, int vocab, long long row_stride,
+                                 const float* noise, long long noise_stride, const float* temperature,
+                                 const int32_t* top_k, const float* top_p, const float* min_p, int32_t* out_ids,
+                                 float* log_probs, void* stream) {
+  if (rows < 0 || vocab < 1 || row_stride < vocab || (noise && noise_stride < vocab) || dtype < PKV_LOGITS_F32 ||
+      dtype > PKV_LOGITS_F16)
+    return PKV_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return PKV_OK;
+  if (!logits || !out_ids || (!noise && !temperature)) return PKV_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(logits) & (dtype == PKV_LOGITS_F32 ? 3u : 1u)) ||
+      ((reinterpret_cast<uintptr_t>(noise) | reinterpret_cast<uintptr_t>(temperature) |
+        reinterpret_cast<uintptr_t>(top_k) | reinterpret_cast<uintptr_t>(top_p) | reinterpret_cast<uintptr_t>(min_p) |
+        reinterpret_cast<uintptr_t>(out_ids) | reinterpret_cast<uintptr_t>(log_probs)) & 3u))
+    return PKV_ERR_MISALIGNED;
+  if (vocab > (1 << 30) || rows > (1 << 27)) return PKV_ERR_UNSUPPORTED_SHAPE;
+  int dev = 0;
+  const int rc = bind_stream_device(stream, &dev);
+  if (rc != PKV_OK) return rc;
+
+  SampleParams p;
+  p.logits = logits;
+  p.noise = noise;
+  p.stride = row_stride;
+  p.noise_stride = noise_stride;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.ids = out_ids;
+  p.log_probs = log_probs;
+  p.vocab = vocab;
+  p.ctas = 1;
+  while (p.ctas < kMostCtas && vocab > p.ctas * kLeast) p.ctas *= 2;
+
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (dtype == PKV_LOGITS_F32) return launch<float>(p, cfg);
+  if (dtype == PKV_LOGITS_BF16) return launch<__nv_bfloat16>(p, cfg);
+  return launch<__half>(p, cfg);
+}
