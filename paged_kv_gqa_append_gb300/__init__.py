@@ -977,6 +977,11 @@ def kv_append_rope_int4(k, v, cu_new, seq_lens, block_tables, kv_pool, rope_cos=
     With tables [max_pos, 32], K (and q_in into q_out) are rotated as in
     kv_append_rope; without, K is taken as it is.  k, v [T, 8, 64], q_in
     [T, 32, 64] bf16 with any token stride that is a multiple of 8."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).append_int4(kv_pool, k, v, cu_new, seq_lens, block_tables, rope_cos, rope_sin, q_in,
+                                                   q_out, d_err, max_blocks)
+        if st >= 0:
+            return _check(st, "kv_append_rope_int4")
     dev, pool, pages = _int4_pool(kv_pool)
     k_ptr, k_stride, T = _rows(k, "k", NUM_KV_HEADS, dev)
     v_ptr, v_stride, _ = _rows(v, "v", NUM_KV_HEADS, dev, T)
@@ -1013,6 +1018,11 @@ def kv_read_int4(kv_pool, page_ids, out=None, d_err=None, stream=None):
     """Pages page_ids of a 4-bit pool as bf16 pages [len(page_ids), 2, 8, 16, 64]
     (a bf16 pool, e.g. for paged_gqa_prefill over a cached prefix with block
     table 0 .. n - 1)."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).read_int4(kv_pool, page_ids, out, d_err)
+        if st >= 0:
+            _check(st, "kv_read_int4")
+            return out
     dev, pool, pages = _int4_pool(kv_pool)
     n = page_ids.numel()
     ids = _vec(page_ids, "page_ids", _I32, dev, n)
@@ -1044,6 +1054,11 @@ def paged_gqa_decode_int4(q, kv_pool, block_tables, seq_lens, out, scale, worksp
     """paged_gqa_decode over 4-bit pages (new_int4_pool): q, out
     [num_seqs, 32, 64] bf16, q rotated.  workspace: alloc_int4_workspace, one
     for each stream or captured graph that may run at the same time."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).decode_int4(kv_pool, q, block_tables, seq_lens, out, scale, workspace, max_seq_len,
+                                                   d_err, max_blocks)
+        if st >= 0:
+            return _check(st, "paged_gqa_decode_int4")
     dev, pool, pages = _int4_pool(kv_pool)
     shape = q.shape
     if shape[-2:] != _Q_ROW:
@@ -1356,6 +1371,13 @@ def sample_logits(logits, noise, temperature=None, top_k=None, top_p=None, min_p
     0 takes the largest logit, and noise may be None where no row draws.  All
     three limits look at the same distribution (pkv.h).  logprobs [rows] fp32
     gets the token's log-probability under softmax(logits / temperature)."""
+    if stream is None:
+        if ids is None and isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2:
+            ids = torch.empty(logits.shape[0], dtype=_I32, device=logits.device)
+        st = (_CALLS or _load_calls()).sample_logits(logits, noise, temperature, top_k, top_p, min_p, ids, logprobs)
+        if st >= 0:
+            _check(st, "pkv_sample_logits")
+            return ids
     dev = _on_device(logits, "logits")
     shape, stride, dtype = logits.shape, logits.stride(), LOGITS_DTYPES.get(logits.dtype)
     if dtype is None or len(shape) != 2:
@@ -1435,6 +1457,14 @@ def grow_block_tables(seq_lens, new_tokens, block_tables, free_pages, free_count
     [layers, T] int32 (16 * page + position % 16): of every new token, -1 behind
     the last.  All or nothing: too few pages (PKV_ERR_POOL_EXHAUSTED) or a row
     that cannot grow (PKV_ERR_DEVICE_INDEX) sets d_err, and nothing is taken."""
+    if stream is None:
+        if cu_new is None and isinstance(seq_lens, torch.Tensor) and seq_lens.is_cuda:
+            cu_new = torch.empty(seq_lens.numel() + 1, dtype=_I32, device=seq_lens.device)
+        st = (_CALLS or _load_calls()).grow_tables(seq_lens, new_tokens, block_tables, free_pages, free_count, seq_lens_out,
+                                                   free_count_out, cu_new, positions, token_seq, slots, d_err, max_blocks)
+        if st >= 0:
+            _check(st, "pkv_grow_block_tables")
+            return cu_new
     dev = _on_device(seq_lens, "seq_lens")
     S = seq_lens.numel()
     lens = _vec(seq_lens, "seq_lens", _I32, dev, S)
@@ -1459,6 +1489,11 @@ def release_pages(seq_lens, finished, block_tables, free_pages, free_count, seq_
     stack, on the GPU, as Scheduler.finish would row by row; their lengths
     become 0.  In place or to seq_lens_out and free_count_out; all or nothing
     (d_err: PKV_ERR_DEVICE_INDEX)."""
+    if stream is None:
+        st = (_CALLS or _load_calls()).release_pages(seq_lens, finished, block_tables, free_pages, free_count, seq_lens_out,
+                                                     free_count_out, d_err, max_blocks)
+        if st >= 0:
+            return _check(st, "pkv_release_pages")
     dev = _on_device(seq_lens, "seq_lens")
     S = seq_lens.numel()
     lens = _vec(seq_lens, "seq_lens", _I32, dev, S)

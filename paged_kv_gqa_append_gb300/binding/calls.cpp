@@ -109,6 +109,16 @@ struct Args {
     scales = vec(i + 1, ScalarType::Float, t->size(0) * 2 * PKV_NUM_KV_HEADS);
     return int8 ? PKV_BS8_INT8 : PKV_BS8_E4M3;
   }
+  // a pool of 4-bit pages, whose device is the call's
+  void* int4(int i, int& pages) {
+    const at::Tensor* t = first(i);
+    if (!t) return nullptr;
+    if (t->scalar_type() != ScalarType::Byte || t->dim() != 3 || t->size(1) != PKV_NUM_KV_HEADS ||
+        t->size(2) != PKV_I4_BLOCK_BYTES || !t->is_contiguous())
+      return fail();
+    pages = to_int(t->size(0));
+    return t->data_ptr();
+  }
   int64_t elements(int i) {
     if (!ok || !THPVariable_Check(at[i])) return ok = false, 0;
     return THPVariable_Unpack(at[i]).numel();
@@ -315,6 +325,176 @@ long process_logits(Args& a) {
                             static_cast<const uint32_t*>(mask), mask_stride, a.stream());
 }
 
+// kv_pool, k, v, cu_new, seq_lens, block_tables, rope_cos, rope_sin, q_in, q_out, d_err, max_blocks
+long append_int4(Args& a) {
+  enum { POOL, K, V, CU, LENS, BT, COS, SIN, Q, QO, ERR, MB };
+  int pages = 0;
+  void* pool = a.int4(POOL, pages);
+  int64_t T = -1;
+  long long qs = 0, ks = 0, vs = 0;
+  void* k = a.rows(K, PKV_NUM_KV_HEADS, T, ks);
+  void* v = a.rows(V, PKV_NUM_KV_HEADS, T, vs);
+  const int64_t S = a.elements(LENS);
+  if (!a.ok || T < 1 || S < 1 || a.none(COS) != a.none(SIN) || a.none(Q) != a.none(QO) || (!a.none(Q) && a.none(COS)))
+    return kOther;
+  void* lens = a.vec(LENS, ScalarType::Int, S);
+  void* cu = a.vec(CU, ScalarType::Int, S + 1);
+  int all = 0, width = 0;
+  void* bt = a.tables(BT, S, all, width);
+  int64_t max_pos = 0;
+  void *cos = nullptr, *sin = nullptr, *q = nullptr, *qo = nullptr;
+  if (!a.none(COS)) {
+    const at::Tensor* t = a.tensor(COS, ScalarType::Float);
+    if (!t || t->dim() != 2 || t->size(1) != PKV_ROPE_PAIRS) return kOther;
+    max_pos = t->size(0);
+    cos = a.vec(COS, ScalarType::Float, max_pos * PKV_ROPE_PAIRS);
+    sin = a.vec(SIN, ScalarType::Float, max_pos * PKV_ROPE_PAIRS);
+  }
+  if (!a.none(Q)) {
+    q = a.rows(Q, PKV_NUM_Q_HEADS, T, qs);
+    qo = a.vec(QO, ScalarType::BFloat16, T * kQRow);
+  }
+  void* err = a.error_word(ERR);
+  const int mb = a.integer(MB, width), tokens = a.to_int(T), seqs = a.to_int(S), positions = a.to_int(max_pos);
+  if (!a.ok) return kOther;
+  return kv_append_rope_int4(k, ks, v, vs, a.ints(cu), a.ints(lens), tokens, a.ints(bt), seqs, width, mb, pool, pages,
+                             static_cast<float*>(cos), static_cast<float*>(sin), positions, q, qs, qo,
+                             static_cast<int*>(err), a.stream());
+}
+
+// kv_pool, page_ids, out, d_err
+long read_int4(Args& a) {
+  int pages = 0;
+  void* pool = a.int4(0, pages);
+  const int64_t n = a.elements(1);
+  if (!a.ok || n < 1) return kOther;
+  void* ids = a.vec(1, ScalarType::Int, n);
+  void* out = a.vec(2, ScalarType::BFloat16, n * PKV_PAGE_ELEMS);
+  void* err = a.error_word(3);
+  const int count = a.to_int(n);
+  if (!a.ok) return kOther;
+  return kv_read_int4(pool, pages, a.ints(ids), count, out, static_cast<int*>(err), a.stream());
+}
+
+// kv_pool, q, block_tables, seq_lens, out, scale, workspace, max_seq_len, d_err, max_blocks
+long decode_int4(Args& a) {
+  enum { POOL, Q, BT, LENS, OUT, SCALE, WS, LONGEST, ERR, MB };
+  int pages = 0;
+  void* pool = a.int4(POOL, pages);
+  const at::Tensor* t = a.tensor(Q, ScalarType::BFloat16);
+  if (!t || t->dim() < 2 || t->size(-1) != PKV_HEAD_DIM || t->size(-2) != PKV_NUM_Q_HEADS || t->numel() < 1) return kOther;
+  const int64_t n = t->numel(), S = n / kQRow;
+  void* q = a.vec(Q, ScalarType::BFloat16, n);
+  void* out = a.vec(OUT, ScalarType::BFloat16, n);
+  void* lens = a.vec(LENS, ScalarType::Int, S);
+  int all = 0, width = 0;
+  void* bt = a.tables(BT, S, all, width);
+  const float scale = a.number(SCALE);
+  const int64_t size = a.elements(WS);
+  void* ws = a.vec(WS, ScalarType::Byte, size);
+  void* err = a.error_word(ERR);
+  const int mb = a.integer(MB, width), seqs = a.to_int(S);
+  if (!a.ok || (a.none(LONGEST) && (mb < 0 || mb > INT_MAX / PKV_PAGE_TOKENS))) return kOther;
+  const int longest = a.integer(LONGEST, PKV_PAGE_TOKENS * mb);
+  if (!a.ok) return kOther;
+  return paged_gqa_decode_int4(q, pool, pages, a.ints(bt), width, mb, a.ints(lens), seqs, longest, out, scale, ws,
+                               (size_t)size, static_cast<int*>(err), a.stream());
+}
+
+// logits, noise, temperature, top_k, top_p, min_p, ids, logprobs
+long sample_logits(Args& a) {
+  enum { X, NOISE, TEMP, K, P, FLOOR, IDS, LP };
+  const at::Tensor* x = a.first(X);
+  if (!x || x->dim() != 2) return kOther;
+  const ScalarType type = x->scalar_type();
+  const int dtype = type == ScalarType::Float ? PKV_LOGITS_F32 : type == ScalarType::BFloat16 ? PKV_LOGITS_BF16
+                    : type == ScalarType::Half ? PKV_LOGITS_F16 : -1;
+  const int64_t rows = x->size(0), vocab = x->size(1);
+  if (dtype < 0 || rows < 1 || vocab < 2 || x->stride(1) != 1 || a.none(NOISE)) return kOther;
+  const at::Tensor* e = a.tensor(NOISE, ScalarType::Float);
+  if (!e || e->dim() != 2 || e->size(0) != rows || e->size(1) != vocab || e->stride(1) != 1) return kOther;
+  void* temp = a.opt(TEMP, ScalarType::Float, rows);
+  void* k = a.opt(K, ScalarType::Int, rows);
+  void* p = a.opt(P, ScalarType::Float, rows);
+  void* floor = a.opt(FLOOR, ScalarType::Float, rows);
+  void* ids = a.vec(IDS, ScalarType::Int, rows);
+  void* lp = a.opt(LP, ScalarType::Float, rows);
+  const int r = a.to_int(rows), v = a.to_int(vocab);
+  if (!a.ok) return kOther;
+  return pkv_sample_logits(x->data_ptr(), dtype, r, v, rows > 1 ? x->stride(0) : vocab, e->data_ptr<float>(),
+                           rows > 1 ? e->stride(0) : vocab, static_cast<float*>(temp), a.ints(k), static_cast<float*>(p),
+                           static_cast<float*>(floor), static_cast<int32_t*>(ids), static_cast<float*>(lp), a.stream());
+}
+
+// The tables of all layers and the stack of a call on it.
+struct Stack {
+  void *lens, *bt, *free_pages, *count, *lens_to, *count_to;
+  int seqs, layers, row, width, pages;
+  long long layer;
+  // at: of the lengths, the tables, the stack, its count, the new lengths and count
+  Stack(Args& a, int lens_at, int bt_at, int free_at, int count_at, int lens_to_at, int count_to_at) {
+    if (!a.first(lens_at)) return;
+    const int64_t S = a.elements(lens_at);
+    seqs = a.to_int(S);
+    lens = a.vec(lens_at, ScalarType::Int, S);
+    lens_to = a.none(lens_to_at) ? lens : a.vec(lens_to_at, ScalarType::Int, S);
+    count = a.vec(count_at, ScalarType::Int, 1);
+    count_to = a.none(count_to_at) ? count : a.vec(count_to_at, ScalarType::Int, 1);
+    const int64_t n = a.elements(free_at);
+    free_pages = a.vec(free_at, ScalarType::Int, n);
+    pages = a.to_int(n);
+    const at::Tensor* t = a.tensor(bt_at, ScalarType::Int);
+    if (!t || t->dim() != 3 || t->size(0) < 1 || t->size(1) < S || t->size(2) < 1 || t->stride(2) != 1) {
+      a.ok = false;
+      return;
+    }
+    bt = t->data_ptr();
+    layers = a.to_int(t->size(0));
+    width = a.to_int(t->size(2));
+    row = a.to_int(t->size(1) > 1 ? t->stride(1) : t->size(2));
+    layer = layers > 1 ? (long long)t->stride(0) : (long long)S * row;
+    if (row < width || (layers > 1 && layer < S * row)) a.ok = false;
+  }
+};
+
+// seq_lens, new_tokens, block_tables, free_pages, free_count, seq_lens_out, free_count_out, cu_new, positions,
+// token_seq, slots, d_err, max_blocks
+long grow_tables(Args& a) {
+  enum { LENS, NEW, BT, FREE, COUNT, LENS_TO, COUNT_TO, CU, POS, SEQ, SLOTS, ERR, MB };
+  Stack s(a, LENS, BT, FREE, COUNT, LENS_TO, COUNT_TO);
+  if (!a.ok || s.seqs < 1) return kOther;
+  void* added = a.opt(NEW, ScalarType::Int, s.seqs);
+  void* cu = a.vec(CU, ScalarType::Int, (int64_t)s.seqs + 1);
+  const int64_t T = !a.none(POS) ? a.elements(POS) : !a.none(SEQ) ? a.elements(SEQ) : a.none(SLOTS) ? 0 : a.elements(SLOTS) / s.layers;
+  void* pos = a.opt(POS, ScalarType::Int, T);
+  void* seq = a.opt(SEQ, ScalarType::Int, T);
+  void* slots = a.opt(SLOTS, ScalarType::Int, T * s.layers);
+  void* err = a.error_word(ERR);
+  const int mb = a.integer(MB, s.width), tokens = a.to_int(T);
+  if (!a.ok) return kOther;
+  return pkv_grow_block_tables(a.ints(s.lens), a.ints(added), s.seqs, static_cast<int32_t*>(s.bt), s.layers, s.layer, s.row, mb,
+                               a.ints(s.free_pages), s.pages, a.ints(s.count), static_cast<int32_t*>(s.lens_to),
+                               static_cast<int32_t*>(s.count_to), static_cast<int32_t*>(cu), static_cast<int32_t*>(pos),
+                               static_cast<int32_t*>(seq), static_cast<int32_t*>(slots), tokens, static_cast<int*>(err),
+                               a.stream());
+}
+
+// seq_lens, finished, block_tables, free_pages, free_count, seq_lens_out, free_count_out, d_err, max_blocks
+long release_pages(Args& a) {
+  enum { LENS, DONE, BT, FREE, COUNT, LENS_TO, COUNT_TO, ERR, MB };
+  Stack s(a, LENS, BT, FREE, COUNT, LENS_TO, COUNT_TO);
+  if (!a.ok || s.seqs < 1 || !THPVariable_Check(a.at[DONE])) return kOther;
+  const ScalarType type = THPVariable_Unpack(a.at[DONE]).scalar_type();
+  if (type != ScalarType::Bool && type != ScalarType::Byte) return kOther;
+  void* done = a.vec(DONE, type, s.seqs);
+  void* err = a.error_word(ERR);
+  const int mb = a.integer(MB, s.width);
+  if (!a.ok) return kOther;
+  return pkv_release_pages(a.ints(s.lens), static_cast<uint8_t*>(done), s.seqs, a.ints(s.bt), s.layers, s.layer, s.row, mb,
+                           static_cast<int32_t*>(s.free_pages), s.pages, a.ints(s.count), static_cast<int32_t*>(s.lens_to),
+                           static_cast<int32_t*>(s.count_to), static_cast<int*>(err), a.stream());
+}
+
 template <long (*F)(Args&), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* at, Py_ssize_t n) {
   long st = kOther;
@@ -337,6 +517,12 @@ PyMethodDef kMethods[] = {
     {"decode_bs8", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<decode_bs8, 11>)), METH_FASTCALL, nullptr},
     {"process_logits", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<process_logits, 12>)), METH_FASTCALL,
      nullptr},
+    {"append_int4", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<append_int4, 12>)), METH_FASTCALL, nullptr},
+    {"read_int4", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<read_int4, 4>)), METH_FASTCALL, nullptr},
+    {"decode_int4", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<decode_int4, 10>)), METH_FASTCALL, nullptr},
+    {"sample_logits", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<sample_logits, 8>)), METH_FASTCALL, nullptr},
+    {"grow_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<grow_tables, 13>)), METH_FASTCALL, nullptr},
+    {"release_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<release_pages, 9>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the small calls (see calls.cpp).", -1, kMethods,
