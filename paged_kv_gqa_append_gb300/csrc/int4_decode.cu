@@ -49,11 +49,13 @@ namespace cg = cooperative_groups;
 constexpr int kHeads = PKV_NUM_KV_HEADS;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRing = 4;                 // pages on their way to a warp, and the one that it works on
-constexpr int kCtasPerSm = 2;            // of the kernel for shares
+constexpr int kPages = 2;                // of a stage: what a step takes
+constexpr int kRing = 3;                 // stages on their way to a warp, and the one that it works on
+constexpr int kStageBytes = kPages * kI4BlockBytes;
+constexpr int kCtasPerSm = 2;
 constexpr int kMaxSeqsInt4 = 4096;
 constexpr int kMinPages = 4;             // least share of a CTA
-constexpr int kList = 1024;              // page ids of a share held at a time
+constexpr int kList = 1024;              // page ids of a share held at a time (even)
 constexpr int kMostCluster = 8;
 constexpr float kStart = -1.5e38f;       // R before the first score
 constexpr float kMostLift = 0x1p126f;
@@ -70,7 +72,7 @@ struct Int4DecodeParams {
                // there and its last CTA; else (-1, -1)
   int* d_err;
   float scale;
-  int num_pages, bt_stride, max_blocks, num_seqs, min_pages, by_cta;
+  int num_pages, bt_stride, max_blocks, num_seqs, min_pages, by_cta, own;  // own: a CTA for each sequence
 };
 
 template <int kLeft>
@@ -84,13 +86,35 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the product alone: zeros that need no registers
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// movmatrix_trans (ptx.cuh), free to move
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -111,6 +135,7 @@ __device__ __forceinline__ int pages_of(const Int4DecodeParams& p, int s, bool& 
 struct Group {
   uint32_t q[8];       // B operands of the four k-steps
   float fa, fb, fl;    // x = (S fa) (ks fb) + kl fl
+  bool apart;          // some head's fa is not 1
   float ref, lift;
   float l, low;        // this lane's sum of p, of p vl lift
   float o[4][4];       // tile w: dims 8 g + 2 w (two columns), 8 g + 2 w + 1 (16 times too large), lifted
@@ -168,8 +193,12 @@ struct Group {
     const float c = scale * 1.4426950408889634f;
     const float d0 = __uint_as_float((uint32_t)(127 - u0) << 23), d1 = __uint_as_float((uint32_t)(127 - u1) << 23);
     // from the head of the q that this lane has to that of its scores
-    fa = __shfl_sync(0xffffffffu, d0 * 0x1p24f, 8 * t);
-    fb = __shfl_sync(0xffffffffu, d1 * c, 8 * t);
+    // (d0 d1 c 2^24 alone, unless a float does not hold that)
+    const float both = d0 * 0x1p24f * (d1 * c);
+    const bool far = !(fabsf(both) < 0x1p120f);
+    fa = __shfl_sync(0xffffffffu, far ? d0 * 0x1p24f : 1.f, 8 * t);
+    fb = __shfl_sync(0xffffffffu, far ? d1 * c : both, 8 * t);
+    apart = __any_sync(0xffffffffu, far);
     fl = __shfl_sync(0xffffffffu, (sum * d0) * (d1 * c), 8 * t);
     ref = kStart;
     l = low = 0.f;
@@ -180,38 +209,69 @@ struct Group {
       for (int e = 0; e < 4; ++e) o[w4][e] = 0.f;
   }
 
-  // A block in shared memory, `live` of whose 16 slots are the sequence's.
-  __device__ __forceinline__ void page(uint32_t block, int live) {
+  static constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+  static constexpr int kSlots = 2 * kPages;  // of a lane: g and g + 8 of either page
+
+  // Two pages whose blocks are in shared memory, at this lane's first bytes; `live` of their 32 slots
+  // are the sequence's.
+  __device__ __forceinline__ void step(uint32_t blocks, int live) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
-    const uint4 k = lds128(block + 16 * lane), v = lds128(block + kI4V + 16 * lane), sc = lds128(block + kI4Scales + 16 * g);
-    constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};  // two chains
-    mma_f16(s0, k.x & kLow, k.z & kLow, k.x & kHigh, k.z & kHigh, q[0], q[1]);
-    mma_f16(s1, k.y & kLow, k.w & kLow, k.y & kHigh, k.w & kHigh, q[4], q[5]);
-    {
+    const uint32_t words = blocks - 16 * (lane - g) + kI4Scales;
+    float r[kSlots], t[kSlots], p[kSlots], vs[kSlots], vl[kSlots];
+#pragma unroll
+    for (int u = 0; u < kPages; ++u) {
+      const uint4 k = lds128(blocks + u * kI4BlockBytes);
+      const uint4 sc = lds128(words + u * kI4BlockBytes);
+      float s[4];
+      mma_first(s, k.x & kLow, k.z & kLow, k.x & kHigh, k.z & kHigh, q[0], q[1]);
+      mma_add(s, k.y & kLow, k.w & kLow, k.y & kHigh, k.w & kHigh, q[4], q[5]);
       const uint32_t a = k.x >> 8, b = k.z >> 8, c = k.y >> 8, d = k.w >> 8;
-      mma_f16(s0, a & kLow, b & kLow, a & kHigh, b & kHigh, q[2], q[3]);
-      mma_f16(s1, c & kLow, d & kLow, c & kHigh, d & kHigh, q[6], q[7]);
-    }
-    // slots g and g + 8
-    float vs0 = bf16lo_to_f32(sc.z), vl0 = bf16hi_to_f32(sc.z), vs1 = bf16lo_to_f32(sc.w), vl1 = bf16hi_to_f32(sc.w);
-    float x0 = fmaf((s0[0] + s1[0]) * fa, bf16lo_to_f32(sc.x) * fb, bf16hi_to_f32(sc.x) * fl);
-    float x1 = fmaf((s0[2] + s1[2]) * fa, bf16lo_to_f32(sc.y) * fb, bf16hi_to_f32(sc.y) * fl);
-    if (live < PKV_PAGE_TOKENS) {  // what lies behind the sequence's end may be anything
-      if (g >= live) {
-        x0 = -INFINITY;
-        vs0 = vl0 = 0.f;
+      mma_add(s, a & kLow, b & kLow, a & kHigh, b & kHigh, q[2], q[3]);
+      mma_add(s, c & kLow, d & kLow, c & kHigh, d & kHigh, q[6], q[7]);
+      r[2 * u] = s[0];
+      r[2 * u + 1] = s[2];
+      if (apart) {
+        r[2 * u] *= fa;
+        r[2 * u + 1] *= fa;
       }
-      if (g + 8 >= live) {
-        x1 = -INFINITY;
-        vs1 = vl1 = 0.f;
-      }
+      t[2 * u] = bf16lo_to_f32(sc.x) * fb;
+      t[2 * u + 1] = bf16lo_to_f32(sc.y) * fb;
+      p[2 * u] = exp2_approx(fmaf(r[2 * u], t[2 * u], fmaf(bf16hi_to_f32(sc.x), fl, -ref)));
+      p[2 * u + 1] = exp2_approx(fmaf(r[2 * u + 1], t[2 * u + 1], fmaf(bf16hi_to_f32(sc.y), fl, -ref)));
+      vs[2 * u] = bf16lo_to_f32(sc.z);
+      vl[2 * u] = bf16hi_to_f32(sc.z);
+      vs[2 * u + 1] = bf16lo_to_f32(sc.w);
+      vl[2 * u + 1] = bf16hi_to_f32(sc.w);
     }
-    if (__any_sync(0xffffffffu, fmaxf(x0, x1) > ref + 1.f)) {
-      float top = fmaxf(x0, x1);
+    if (live < kPages * PKV_PAGE_TOKENS) {  // what lies behind the sequence's end may be anything
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (g + 8 * i >= live) p[i] = vs[i] = vl[i] = 0.f;
+    }
+    float y[kSlots], z[kSlots];
+    const auto sum_of = [](const float (&v)[kSlots]) { return (v[0] + v[1]) + (v[2] + v[3]); };
+    const auto weigh = [&]() {
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const float lifted = p[i] * lift;
+        y[i] = lifted * vs[i];
+        z[i] = lifted * vl[i];
+      }
+    };
+    weigh();
+    float psum = sum_of(p), zsum = sum_of(z);
+    // a score 3 above R makes p 8; the scales of V are not negative, and NaN comes here too
+    if (__any_sync(0xffffffffu, !(psum <= 8.f) || !(fabsf(sum_of(y)) <= 0x1p15f) || !(fabsf(zsum) <= 0x1p60f))) {
+      float x[kSlots], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        const uint32_t word = lds32(words + (i >> 1) * kI4BlockBytes + 4 * (i & 1));
+        x[i] = g + 8 * i < live ? fmaf(r[i], t[i], bf16hi_to_f32(word) * fl) : -INFINITY;
+        top = fmaxf(top, x[i]);
+      }
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float now = fmaxf(ref, ceilf(top));
+      const float now = top > ref + 1.f ? ceilf(top) : ref;
       const float keep = exp2_approx(ref - now);  // (a head whose reference stays: 1)
       l *= keep;
       // the lifted sums stay as they are, unless that lifts them too far
@@ -219,48 +279,58 @@ struct Group {
       lower(more * keep / lift);
       lift = more;
       ref = now;
-    }
-    const float p0 = exp2_approx(x0 - ref), p1 = exp2_approx(x1 - ref);
-    l += p0 + p1;
-    float y0 = p0 * lift * vs0, y1 = p1 * lift * vs1, z0 = p0 * lift * vl0, z1 = p1 * lift * vl1;
-    if (__any_sync(0xffffffffu, fmaxf(fabsf(y0), fabsf(y1)) > 0x1p15f || fmaxf(fabsf(z0), fabsf(z1)) > 0x1p19f)) {
-      float top = fmaxf(fmaxf(p0 * fabsf(vs0), p1 * fabsf(vs1)), fmaxf(p0 * (0.0625f * fabsf(vl0)), p1 * (0.0625f * fabsf(vl1))));
+      float most = 0.f;
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (top * lift > 0x1p15f) {  // (the same for all lanes of a head)
-        // 2^13 up to 2^14; top is above 2^-111
-        const float now = __uint_as_float((uint32_t)max(1, 127 + 13 + 127 - (int)(__float_as_uint(top) >> 23)) << 23);
-        lower(now / lift);
-        lift = now;
-        y0 = p0 * now * vs0;
-        y1 = p1 * now * vs1;
-        z0 = p0 * now * vl0;
-        z1 = p1 * now * vl1;
+      for (int i = 0; i < kSlots; ++i) {
+        p[i] = exp2_approx(x[i] - ref);
+        most = fmaxf(most, p[i] * fmaxf(fabsf(vs[i]), 0.0625f * fabsf(vl[i])));
       }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+      if (most * lift > 0x1p14f) {  // (the same for all lanes of a head)
+        // 2^13 up to 2^14; the largest weight is above 2^-112
+        const float to = __uint_as_float((uint32_t)max(1, 127 + 13 + 127 - (int)(__float_as_uint(most) >> 23)) << 23);
+        lower(to / lift);
+        lift = to;
+      }
+      weigh();
+      psum = sum_of(p);
+      zsum = sum_of(z);
       __syncwarp();
     }
-    low += z0 + z1;
-    // rounded to fp16, and what that leaves
-    const uint32_t near = pack_f16x2(y0, y1);
-    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&near));
-    const uint32_t rest = pack_f16x2(y0 - r.x, y1 - r.y);
-    const uint32_t b0 = movmatrix_trans(__byte_perm(near, rest, 0x5410));
-    const uint32_t b1 = movmatrix_trans(__byte_perm(near, rest, 0x7632));
-    const uint32_t even[2] = {v.x, v.y}, odd[2] = {v.z, v.w};  // slots 2 t, 2 t + 1; and 8 more
+    l += psum;
+    low += zsum;
+    uint32_t b0[kPages], b1[kPages];
+    uint4 v[kPages];
+#pragma unroll
+    for (int u = 0; u < kPages; ++u) {
+      // rounded to fp16, and what that leaves
+      const uint32_t near = pack_f16x2(y[2 * u], y[2 * u + 1]);
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&near));
+      const uint32_t rest = pack_f16x2(y[2 * u] - h.x, y[2 * u + 1] - h.y);
+      b0[u] = transposed(__byte_perm(near, rest, 0x5410));
+      b1[u] = transposed(__byte_perm(near, rest, 0x7632));
+      v[u] = lds128(blocks + u * kI4BlockBytes + kI4V);  // slots 2 t, 2 t + 1 (x, y), and 8 more (z, w)
+    }
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t a = j ? even[w] >> 8 : even[w], b = j ? odd[w] >> 8 : odd[w];
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, a & kLow, a & kHigh, b & kLow, b & kHigh, b0, b1);
+        float d[4];
+#pragma unroll
+        for (int u = 0; u < kPages; ++u) {
+          const uint32_t even = w ? v[u].y : v[u].x, odd = w ? v[u].w : v[u].z;
+          const uint32_t a = j ? even >> 8 : even, b = j ? odd >> 8 : odd;
+          if (u == 0) mma_first(d, a & kLow, a & kHigh, b & kLow, b & kHigh, b0[u], b1[u]);
+          else mma_add(d, a & kLow, a & kHigh, b & kLow, b & kHigh, b0[u], b1[u]);
+        }
         float* to = o[2 * w + j];
-        const float2 u = add2(make_float2(to[0], to[1]), make_float2(d[0], d[1]));
-        const float2 z = add2(make_float2(to[2], to[3]), make_float2(d[2], d[3]));
-        to[0] = u.x;
-        to[1] = u.y;
-        to[2] = z.x;
-        to[3] = z.y;
+        const float2 f = add2(make_float2(to[0], to[1]), make_float2(d[0], d[1]));
+        const float2 h = add2(make_float2(to[2], to[3]), make_float2(d[2], d[3]));
+        to[0] = f.x;
+        to[1] = f.y;
+        to[2] = h.x;
+        to[3] = h.y;
       }
   }
 
@@ -297,44 +367,57 @@ __device__ __forceinline__ void write_row(uint16_t* out, int seq, int head, cons
   *reinterpret_cast<uint4*>(out + ((size_t)seq * PKV_NUM_Q_HEADS + head * PKV_GROUP + t) * PKV_HEAD_DIM + 8 * g) = v;
 }
 
-// A warp's ring of blocks, filled by its own asynchronous copies.
+// A warp's ring of stages, filled by its own asynchronous copies.
 struct Ring {
-  uint32_t base;
-  int slot, next;  // worked on, and written next
-  __device__ __forceinline__ explicit Ring(uint32_t at) : base(at), slot(0), next(0) {}
-  __device__ __forceinline__ uint32_t at(int i) const { return base + i * kI4BlockBytes; }
-  __device__ __forceinline__ void copy(const uint8_t* block) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t dst = at(next) + 16 * lane;
-    const uint8_t* src = block + 16 * lane;
-    cp_async16(dst, src);
-    cp_async16(dst + 512, src + 512);
-    if (lane < 8) cp_async16(dst + 1024, src + 1024);
+  uint32_t base;        // this lane's first bytes of it
+  const uint8_t* from;  // of the head's block of page 0
+  int slot, next;       // worked on, and written next
+  bool some;            // the lanes that a block's last 128 bytes go to
+  __device__ __forceinline__ Ring(uint32_t at, const uint8_t* pool, int head)
+      : base(at + 16 * (threadIdx.x & 31)),
+        from(pool + (size_t)head * kI4BlockBytes + 16 * (threadIdx.x & 31)),
+        slot(0),
+        next(0),
+        some((threadIdx.x & 31) < 8) {}
+  __device__ __forceinline__ void copy(int u, int page) {
+    const uint32_t dst = base + next + u * kI4BlockBytes;
+    const uint8_t* src = from + (size_t)(uint32_t)page * kI4PageBytes;
+    asm volatile(
+        "cp.async.cg.shared.global [%0], [%1], 16;\n\t"
+        "cp.async.cg.shared.global [%0 + 512], [%1 + 512], 16;" ::"r"(dst), "l"(src)
+        : "memory");
+    if (some) asm volatile("cp.async.cg.shared.global [%0 + 1024], [%1 + 1024], 16;" ::"r"(dst), "l"(src) : "memory");
   }
   __device__ __forceinline__ void commit() {
     cp_async_commit();
-    if (++next == kRing) next = 0;
+    next = next == (kRing - 1) * kStageBytes ? 0 : next + kStageBytes;
   }
-  // the oldest block has landed, for all lanes, and the one before it is no longer read
+  // the oldest stage has landed, for all lanes, and the one before it is no longer read; where this
+  // lane's bytes of it are
   __device__ __forceinline__ uint32_t wait() {
     cp_async_wait<kRing - 2>();
     __syncwarp();
-    const uint32_t here = at(slot);
-    if (++slot == kRing) slot = 0;
+    const uint32_t here = base + slot;
+    slot = slot == (kRing - 1) * kStageBytes ? 0 : slot + kStageBytes;
     return here;
+  }
+  __device__ __forceinline__ void restart() {
+    cp_async_wait<0>();
+    __syncwarp();
+    slot = next = 0;
   }
 };
 
-struct Held {  // what a warp of the kernel for whole sequences has found: means and the logarithm of their weight
+struct alignas(16) Held {  // what a warp of the kernel for whole sequences has found: means and the logarithm of their weight
   float o[PKV_GROUP][PKV_HEAD_DIM];
   float weight[PKV_GROUP];
   int bad;
 };
 
 // One sequence and KV head for each cluster of CTAs (of one or more): every warp takes every
-// (warps)-th page, and what they find is put together in shared memory, over the cluster's CTAs
+// (warps)-th pair of pages, and what they find is put together in shared memory, over the cluster's CTAs
 // too.  Nothing goes through global memory.
-__global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_whole_kernel(const Int4DecodeParams p) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Held sum;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -351,28 +434,32 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
     if (refused && rank == 0 && threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
     return;
   }
-  const int first = rank * kWarps + warp, stride = ctas * kWarps;
-  const int count = first < pages ? (pages - first + stride - 1) / stride : 0;
+  // pairs of pages: this warp's first one, and the distance to the next
+  const int first = rank * kWarps + warp, stride = ctas * kWarps, pairs = (pages + 1) / kPages;
+  const int count = first < pairs ? (pairs - first + stride - 1) / stride : 0;
   const int32_t* table = p.block_tables + (size_t)seq * p.bt_stride;
   bool bad = false;
-  // ids of 32 pages, and of the 32 behind them under way
-  const auto ids = [&](int i) { return i + lane < count ? __ldg(table + first + (i + lane) * stride) : 0; };
-  int id = ids(0), coming = count > 32 ? ids(32) : 0;
+  // ids of 16 pairs, and of the 16 behind them under way
+  const auto ids = [&](int i) {
+    const int at = (first + (i + (lane >> 1)) * stride) * kPages + (lane & 1);
+    if (i + (lane >> 1) >= count || at >= pages) return 0;
+    const int id = __ldg(table + at);
+    const bool ok = id >= 0 && id < p.num_pages;
+    bad |= !ok;
+    return ok ? id : 0;
+  };
+  int id = ids(0), coming = count > 16 ? ids(16) : 0;
   uint4 raw[2];
   Group::fetch(p, seq, head, raw);
-  Ring ring(smem_u32(dyn) + warp * (kRing * kI4BlockBytes));
+  Ring ring(smem_u32(dyn) + warp * (kRing * kStageBytes), p.pool, head);
   const auto issue = [&](int i) {
     if (i < count) {
-      if (i && (i & 31) == 0) {
+      if (i && (i & 15) == 0) {
         id = coming;
-        coming = ids(i + 32);
+        coming = ids(i + 16);
       }
-      int page = __shfl_sync(0xffffffffu, id, i & 31);
-      if (page < 0 || page >= p.num_pages) {
-        bad = true;
-        page = 0;
-      }
-      ring.copy(p.pool + ((size_t)page * kHeads + head) * kI4BlockBytes);
+#pragma unroll
+      for (int u = 0; u < kPages; ++u) ring.copy(u, __shfl_sync(0xffffffffu, id, (2 * i + u) & 31));
     }
     ring.commit();
   };
@@ -381,17 +468,17 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
   Group st;
   st.start(raw, p.scale);
   for (int i = 0; i < count; ++i) {
-    const uint32_t block = ring.wait();
-    st.page(block, min(PKV_PAGE_TOKENS, len - (first + i * stride) * PKV_PAGE_TOKENS));
+    const uint32_t blocks = ring.wait();
+    st.step(blocks, len - (first + i * stride) * (kPages * PKV_PAGE_TOKENS));
     issue(i + kRing - 1);
   }
   float x[8];
   const float weight = st.finish(x, kMeanDown);
   // into the warp's own ring, which nothing is on its way to any more
-  static_assert(sizeof(Held) <= kRing * kI4BlockBytes && kI4BlockBytes % 16 == 0, "room for what a warp found");
+  static_assert(sizeof(Held) <= kRing * kStageBytes && kI4BlockBytes % 16 == 0, "room for what a warp found");
   cp_async_wait<0>();
   __syncwarp();
-  Held* mine = reinterpret_cast<Held*>(dyn + warp * (kRing * kI4BlockBytes));
+  Held* mine = reinterpret_cast<Held*>(dyn + warp * (kRing * kStageBytes));
   {
     const int g = lane >> 2, t = lane & 3;
     float4* to = reinterpret_cast<float4*>(mine->o[t] + 8 * g);
@@ -403,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
   if (bad && threadIdx.x == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
   const int h = threadIdx.x / PKV_HEAD_DIM, d = threadIdx.x % PKV_HEAD_DIM;
   static_assert(kThreads == PKV_GROUP * PKV_HEAD_DIM, "a thread for each output");
-  const auto of = [&](int w) { return reinterpret_cast<const Held*>(dyn + w * (kRing * kI4BlockBytes)); };
+  const auto of = [&](int w) { return reinterpret_cast<const Held*>(dyn + w * (kRing * kStageBytes)); };
   float ref = kStart, o = 0.f, total = 0.f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, of(w)->weight[h]);
@@ -422,19 +509,20 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
   if (d == 0) sum.weight[h] = ref + __log2f(total);
   if (threadIdx.x == 0) sum.bad = bad;
   cluster.sync();
-  // each CTA an equal part of the 256 outputs
-  const int per = kThreads / ctas;
-  if ((int)threadIdx.x < per) {
-    const int at = rank * per + threadIdx.x, hh = at / PKV_HEAD_DIM, dd = at % PKV_HEAD_DIM;
+  // each CTA an equal part of the 256 outputs, a thread two of them
+  const int at = rank * (kThreads / ctas) + 2 * (int)threadIdx.x;
+  if (2 * (int)threadIdx.x < kThreads / ctas) {
+    const int hh = at / PKV_HEAD_DIM, dd = at % PKV_HEAD_DIM;
     ref = kStart;
-    o = total = 0.f;
+    total = 0.f;
     bad = false;
-    float weights[kMostCluster], means[kMostCluster];
+    float weights[kMostCluster];
+    float2 means[kMostCluster], y = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < kMostCluster; ++c) {
       const Held* other = cluster.map_shared_rank(&sum, c < ctas ? c : 0);
       weights[c] = c < ctas ? other->weight[hh] : kStart;
-      means[c] = c < ctas ? other->o[hh][dd] : 0.f;
+      means[c] = c < ctas ? *reinterpret_cast<const float2*>(other->o[hh] + dd) : make_float2(0.f, 0.f);
       if (c < ctas) bad |= other->bad != 0;
     }
 #pragma unroll
@@ -442,11 +530,12 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
 #pragma unroll
     for (int c = 0; c < kMostCluster; ++c) {
       const float scaled = c < ctas ? exp2_approx(weights[c] - ref) : 0.f;
-      o = fmaf(scaled, means[c], o);
+      y.x = fmaf(scaled, means[c].x, y.x);
+      y.y = fmaf(scaled, means[c].y, y.y);
       total += scaled;
     }
-    const float y = bad ? 0.f : o * (1.f / total) * kMeanUp, z = __shfl_down_sync(0xffffffffu, y, 1);
-    if (dd % 2 == 0) *reinterpret_cast<uint32_t*>(out + at) = pack_bf16x2(y, z);
+    const float inv = kMeanUp * (1.f / total);
+    *reinterpret_cast<uint32_t*>(out + at) = bad ? 0u : pack_bf16x2(y.x * inv, y.y * inv);
   }
   cluster.sync();  // nobody's shared memory goes while it is read
 }
@@ -454,7 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2) int4_whole_kernel(const Int4Decod
 struct ShareSmem {
   int sum[kWarps];
   int first_seq, before;  // the sequence that the CTA's share begins in, and the pages before that
-  int list[kList];        // page ids, -1 for what cannot be one
+  int bad;                // ids among the listed ones that cannot be one
+  alignas(8) int list[kList];  // page ids in pairs of one sequence; 0 for one that cannot be and behind an odd one
+  uint32_t wrong[kList / 32];   // those that cannot be
 };
 
 // The pages of all sequences are one long list; every CTA takes an equal share of it, whatever the
@@ -485,7 +576,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const 
       if (refused) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
     }
   };
-  if (p.num_seqs <= 32) {  // every warp finds out by itself
+  if (p.own) {
+    bool refused;
+    pdl_launch_dependents();
+    seq = blockIdx.x;
+    begin = page = 0;
+    end = pages_of(p, seq, refused);
+    share = max(end, 1);
+    if (end == 0 && warp == 0) {
+      uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM);
+      for (int i = lane; i < PKV_NUM_Q_HEADS * PKV_HEAD_DIM / 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+      if (refused && lane == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+    }
+  } else if (p.num_seqs <= 32) {  // every warp finds out by itself
     bool refused = false;
     const int n = lane < p.num_seqs ? pages_of(p, lane, refused) : 0;
     int run = n;
@@ -554,28 +657,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const 
   }
 
   const int head = warp;
-  Ring ring(smem_u32(dyn) + warp * (kRing * kI4BlockBytes));
+  Ring ring(smem_u32(dyn) + warp * (kRing * kStageBytes), p.pool, head);
   int2 split = make_int2(-1, -1);  // the sequence that begins here and goes on, and its last CTA
   bool refused, bad = false;
-  int pages = pages_of(p, seq, refused), len = __ldg(p.seq_lens + seq), from = page;
-  int list_seq = seq, list_page = page;
+  int pages = pages_of(p, seq, refused), from = page;
+  int left = __ldg(p.seq_lens + seq) - page * PKV_PAGE_TOKENS;  // tokens from the next page on
+  int list_seq = seq, list_page = page, list_at = begin;
   uint4 raw[2];
   Group::fetch(p, seq, head, raw);
   Group st;
   st.start(raw, p.scale);
   for (int at = begin; at < end;) {
-    const int stop = min(end, at + kList), items = stop - at;
     if (at > begin) __syncthreads();  // the last ids are no longer read
-    for (int i = 0; i < items;) {     // the ids of the next pages, sequence by sequence
-      const int n = pages_of(p, list_seq, refused), some = min(n - list_page, items - i);
+    if (threadIdx.x == 0) sh.bad = 0;
+    if (threadIdx.x < kList / 32) sh.wrong[threadIdx.x] = 0;
+    __syncthreads();
+    int items = 0;
+    while (list_at < end && items < kList) {  // the ids of the next pages, sequence by sequence
+      const int n = pages_of(p, list_seq, refused), some = min(min(n - list_page, end - list_at), kList - items);
       const int32_t* table = p.block_tables + (size_t)list_seq * p.bt_stride + list_page;
-      for (int j = threadIdx.x; j < some; j += kThreads) {
-        const int id = __ldg(table + j);
+      for (int j = threadIdx.x; j < some + (some & 1); j += kThreads) {
+        const int id = j < some ? __ldg(table + j) : 0;
         const bool ok = id >= 0 && id < p.num_pages;
-        sh.list[i + j] = ok ? id : -1;
-        if (!ok) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+        sh.list[items + j] = ok ? id : 0;
+        if (!ok) {
+          sh.bad = 1;
+          atomicOr(&sh.wrong[(items + j) / 32], 1u << (items + j) % 32);
+          report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
+        }
       }
-      i += some;
+      items += some + (some & 1);
+      list_at += some;
       list_page += some;
       if (list_page == n) {
         list_page = 0;
@@ -584,19 +696,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const 
       }
     }
     __syncthreads();
+    const bool any_bad = sh.bad != 0;
     const auto issue = [&](int i) {
-      if (i < items) ring.copy(p.pool + ((size_t)max(sh.list[i], 0) * kHeads + head) * kI4BlockBytes);
+      if (i < items) {
+        const int2 id = *reinterpret_cast<const int2*>(sh.list + i);
+        ring.copy(0, id.x);
+        ring.copy(1, id.y);
+      }
       ring.commit();
     };
 #pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) issue(i);
-    for (int i = 0; i < items; ++i) {
-      const uint32_t block = ring.wait();
-      bad |= sh.list[i] < 0;
-      st.page(block, min(PKV_PAGE_TOKENS, len - page * PKV_PAGE_TOKENS));
-      issue(i + kRing - 1);
-      ++page;
-      ++at;
+    for (int i = 0; i < kRing - 1; ++i) issue(i * kPages);
+    for (int i = 0; i < items; i += kPages) {
+      const uint32_t blocks = ring.wait();
+      const int n = min(kPages, min(pages - page, end - at));
+      if (any_bad) bad |= (sh.wrong[i / 32] >> i % 32 & 3u) != 0;  // (the one behind an odd page is not)
+      st.step(blocks, min(n * PKV_PAGE_TOKENS, left));
+      issue(i + (kRing - 1) * kPages);
+      page += n;
+      at += n;
+      left -= n * PKV_PAGE_TOKENS;
       if (page < pages && at < end) continue;
       // the end of the sequence, or of the share inside it
       float x[8];
@@ -611,27 +730,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const 
         to[0] = make_float4(x[0], x[1], x[2], x[3]);
         to[1] = make_float4(x[4], x[5], x[6], x[7]);
         if (g == 0)
-          *reinterpret_cast<float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * hq) = make_float2(weight, bad ? kNothing : 1.f);
+          *reinterpret_cast<float2*>(part + PKV_NUM_Q_HEADS * PKV_HEAD_DIM + 2 * hq) =
+              make_float2(weight, bad ? kNothing : 1.f);
         if (from == 0) split = make_int2(seq, (int)((unsigned)(at - page + pages - 1) / share));
       }
       if (at < end) {
         do ++seq;
         while (seq < p.num_seqs && (pages = pages_of(p, seq, refused)) == 0);
-        len = __ldg(p.seq_lens + seq);
+        left = __ldg(p.seq_lens + seq);
         page = from = 0;
         bad = false;
         Group::fetch(p, seq, head, raw);
         st.start(raw, p.scale);
       }
     }
-    cp_async_wait<0>();
-    ring = Ring(ring.base);
-    __syncwarp();
+    ring.restart();
   }
   if (p.by_cta && threadIdx.x == 0) p.span[blockIdx.x] = split;
 }
 
-constexpr int kSmemBytes = kWarps * kRing * kI4BlockBytes;
+constexpr int kSmemBytes = kWarps * kRing * kStageBytes;
 
 }  // namespace
 }  // namespace pkv
@@ -689,9 +807,20 @@ extern "C" int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num
 
   const long long longest = max_seq_len > 0 ? max_seq_len : (long long)max_blocks * PKV_PAGE_TOKENS;
   const long long most_pages = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
-  const bool whole = most_pages * num_seqs <= 64ll * 128 && most_pages <= 256;
+  // How the work is split, by the caller's bound (us: a CTA per sequence / clusters / shares):
+  //  - a CTA for each of many sequences, if they are short, or if such CTAs keep the SMs about as busy as
+  //    shares would: 80 of 8 pages 7.3 / 9.6 / 11.5, 256 of 16 14.0 / 28.1 / 22.5, 2000 ragged to 4 39 / - /
+  //    48, 300 of 128 66 / - / 79; 100 of 64 24.1 / 22.8 / 24.1, 64 of 32 14.6 / 11.7 / 15.3;
+  //  - else a cluster for each sequence and KV head, as many CTAs as two for each SM allow, as long as
+  //    these take few pages each: 1 of 128 pages - / 4.8 / 7.5, 1 of 1024 - / 11.5 / 11.0, 4 of 128 - / 5.5
+  //    / 8.7, 32 of 128 - / 12.9 / 18.1, 64 of 128 - / 23.2 / 25.6, 32 of 512 - / 42.4 / 41.6;
+  //  - else shares: 1 of 8192 pages - / 40.5 / 24.4, 97 ragged to 512 - / 60 / 55.
+  const int slots = kCtasPerSm * sms, waves = (num_seqs + slots - 1) / slots;
+  const double busy = num_seqs <= sms ? 0.86 * num_seqs / sms : (double)num_seqs / (waves * slots);
+  p.own = 2 * num_seqs > sms && (most_pages <= 24 || (most_pages <= 128 && busy >= 0.6));
   int ctas = 1;
-  while (ctas < kMostCluster && (long long)num_seqs * kHeads * ctas * 2 <= 2 * sms && most_pages > ctas * kWarps) ctas *= 2;
+  while (ctas < kMostCluster && num_seqs * kHeads * ctas * 2 <= slots && most_pages > ctas * kWarps) ctas *= 2;
+  const bool whole = !p.own && most_pages <= 64 * (ctas + 1) && most_pages * num_seqs <= 64 * 128;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -704,19 +833,24 @@ extern "C" int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
+  auto* kernel = whole ? int4_whole_kernel : int4_share_kernel;
+  rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
+                   "cudaFuncSetAttribute(decode int4)");
+  if (rc != PKV_OK) return rc;
   if (whole) {
     p.by_cta = 0;
     cfg.gridDim = dim3((unsigned)ctas, kHeads, (unsigned)num_seqs);
     cfg.numAttrs = 2;
-    return cuda_status(cudaLaunchKernelEx(&cfg, int4_whole_kernel, p), "cudaLaunchKernelEx(decode int4)");
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(decode int4)");
   }
-  p.by_cta = num_seqs > kBySequence;
-  long long shares = (most_pages * num_seqs + kMinPages - 1) / kMinPages;
-  if (shares > most) shares = most;
+  p.by_cta = !p.own && num_seqs > kBySequence;
+  // no more CTAs than the bound can give work to (the shares follow the actual lengths)
+  long long shares = p.own ? num_seqs : (most_pages * num_seqs + kMinPages - 1) / kMinPages;
+  if (!p.own && shares > most) shares = most;
   if (shares < 1) shares = 1;
   cfg.gridDim = dim3((unsigned)shares);
   cfg.numAttrs = 1;
-  rc = cuda_status(cudaLaunchKernelEx(&cfg, int4_share_kernel, p), "cudaLaunchKernelEx(decode int4)");
-  if (rc != PKV_OK || shares == 1) return rc;  // one CTA splits nothing
+  rc = cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(decode int4)");
+  if (rc != PKV_OK || shares == 1 || p.own) return rc;  // nothing is split
   return launch_merge(cfg, p.parts, p.span, p.out, num_seqs, (int)shares, p.by_cta, sms, kMeanUp, "cudaLaunchKernelEx(merge int4)");
 }
