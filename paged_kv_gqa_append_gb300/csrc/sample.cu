@@ -50,6 +50,7 @@ constexpr int kMostHeld = 100 << 10;  // bytes of logits in a CTA's shared memor
 constexpr int kList = 64;            // candidates of a warp
 constexpr int kMostQ = 16;
 constexpr int kTryQ = 4;             // of the bound tried for top-p
+constexpr int kCandidates = 2048;  // of a row, at most, in lists
 constexpr int kRounds = 12;
 
 struct SampleParams {
@@ -123,14 +124,57 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// What a warp, a CTA and a row have found in a pass.
-struct Found {
-  float max, sum, bound;      // first pass: largest logit, sum of w under that maximum, the bound
-  float race, x;              // the race: its best and that token's logit
-  int id;
-  float mass;                 // check: of the tokens ranked before the pivot
-  int count, overflow;
+// What a thread, a warp, a CTA and a row have found: in the first pass
+struct First {
+  float max, sum, bound;  // largest logit, sum of w under that maximum, the bound
 };
+// and in the others.
+struct Found {
+  float race, x;     // the race: its best, and that token's logit
+  int id;
+  float mass;        // the sum of w of the tokens asked about
+  int count, flags;  // how many they are; whether a list overflowed
+};
+__device__ __forceinline__ bool better(float r, int i, float than, int id) { return r > than || (r == than && i < id); }
+__device__ __forceinline__ void combine(First& a, const First& b, float c) {
+  const float m = fmaxf(a.max, b.max);
+  // (rounded one by one: the same whichever of the two is whose)
+  a.sum = __fadd_rn(__fmul_rn(a.sum, exp2_approx((a.max - m) * c)), __fmul_rn(b.sum, exp2_approx((b.max - m) * c)));
+  a.max = m;
+  a.bound = fminf(a.bound, b.bound);
+}
+__device__ __forceinline__ void combine(Found& a, const Found& b) {
+  if (better(b.race, b.id, a.race, a.id)) {
+    a.race = b.race;
+    a.x = b.x;
+    a.id = b.id;
+  }
+  a.mass += b.mass;
+  a.count += b.count;
+  a.flags |= b.flags;
+}
+// over groups of n lanes; all lanes get the result
+__device__ __forceinline__ void over_lanes(First& f, int n, float c) {
+  for (int o = n / 2; o > 0; o >>= 1) {
+    First g;
+    g.max = __shfl_xor_sync(0xffffffffu, f.max, o);
+    g.sum = __shfl_xor_sync(0xffffffffu, f.sum, o);
+    g.bound = __shfl_xor_sync(0xffffffffu, f.bound, o);
+    combine(f, g, c);
+  }
+}
+__device__ __forceinline__ void over_lanes(Found& f, int n) {
+  for (int o = n / 2; o > 0; o >>= 1) {
+    Found g;
+    g.race = __shfl_xor_sync(0xffffffffu, f.race, o);
+    g.x = __shfl_xor_sync(0xffffffffu, f.x, o);
+    g.id = __shfl_xor_sync(0xffffffffu, f.id, o);
+    g.mass = __shfl_xor_sync(0xffffffffu, f.mass, o);
+    g.count = __shfl_xor_sync(0xffffffffu, f.count, o);
+    g.flags = __shfl_xor_sync(0xffffffffu, f.flags, o);
+    combine(f, g);
+  }
+}
 
 struct Pivot {
   float x;
@@ -139,16 +183,17 @@ struct Pivot {
 };
 
 struct Smem {
-  Found warps[kWarps];
-  Found rows[2][kMostCtas];  // of all CTAs, for every second pass
+  First firsts[kWarps], first_rows[kMostCtas];
+  Found warps[2][kWarps], rows[2][kMostCtas];  // two of each: one is read while the next is written
   float x[kWarps][kList];
-  int id[kWarps][kList];
+  int id[kWarps][kList], here[kWarps];
+  int base[kWarps * kMostCtas + 1];
 };
 
 template <class T, bool kHeld>
 struct Row {
   static constexpr int kN = Wide<T>::kN;
-  static constexpr int kBatch = 4;  // 16-byte loads in flight per thread
+  static constexpr int kBatch = kHeld ? 8 : 4;  // 16-byte loads in flight per thread
   const SampleParams& p;
   Smem& sh;
   uint4* held;               // the part's logits, if they are held
@@ -195,83 +240,161 @@ struct Row {
     }
   }
 
-  // This CTA's Found to every CTA of the cluster; theirs are in the array returned.
-  __device__ const Found* exchange(const Found& mine) {
+  // The CTA's, of all threads; every thread gets it.
+  __device__ __forceinline__ Found of_cta(Found f) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    over_lanes(f, 32);
+    if (lane == 0) sh.warps[turn][warp] = f;
+    __syncthreads();
+    f = sh.warps[turn][lane % kWarps];
+    over_lanes(f, kWarps);
+    turn ^= 1;
+    return f;
+  }
+  // The row's: sent to every CTA of the cluster.
+  __device__ __forceinline__ Found of_row(Found f) {
+    f = of_cta(f);
+    if (p.ctas == 1) return f;
     const cg::cluster_group cluster = cg::this_cluster();
     Found* to = &sh.rows[turn][rank];
-    if (p.ctas == 1) {
-      if (threadIdx.x == 0) *to = mine;
-      __syncthreads();
-    } else {
-      if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = mine;
-      cluster.sync();
-    }
-    turn ^= 1;
-    return sh.rows[turn ^ 1];
+    if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = f;
+    cluster.sync();
+    f = sh.rows[turn][threadIdx.x & (p.ctas - 1)];
+    over_lanes(f, p.ctas);
+    return f;
+  }
+  __device__ __forceinline__ First of_row(First f, float c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    over_lanes(f, 32, c);
+    if (lane == 0) sh.firsts[warp] = f;
+    __syncthreads();
+    f = sh.firsts[lane % kWarps];
+    over_lanes(f, kWarps, c);
+    if (p.ctas == 1) return f;
+    const cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_wait();  // all of them run
+    First* to = &sh.first_rows[rank];
+    if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = f;
+    cluster.sync();
+    f = sh.first_rows[threadIdx.x & (p.ctas - 1)];
+    over_lanes(f, p.ctas, c);
+    return f;
   }
 };
 
-__device__ __forceinline__ bool better(float r, int i, float than, int id) {
-  return r > than || (r == than && i < id);
+// Everything before the place returned is kept, and nothing else, where `out` is not: the last kept place
+// by bisection, first the logit, then the id.  check(place) says what lies before a place.
+template <class Kept, class Check>
+__device__ Pivot last_kept(const Pivot& out, float most, int vocab, const Kept& kept, const Check& check) {
+  uint32_t lo = key_of(out.x) - 1, hi = key_of(most);  // (hi, 0) is kept, (lo, 0), behind `out`, is not
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const Found f = check(Pivot{of_key(mid), 0});
+    if (kept(of_key(mid), f.count, f.mass))
+      hi = mid;
+    else
+      lo = mid;
+  }
+  int in = 0, behind = vocab;  // the place (hi, in) is kept, (hi, behind) is not or there is none
+  while (behind - in > 1) {
+    const int mid = in + (behind - in) / 2;
+    const Found f = check(Pivot{of_key(hi), mid});
+    if (kept(of_key(hi), f.count, f.mass))
+      in = mid;
+    else
+      behind = mid;
+  }
+  return Pivot{of_key(hi), in + 1};
 }
 
-// A thread's best of the race to that of the CTA, with the sums of a check.
-__device__ __forceinline__ Found gather(Smem& sh, float race, float x, int id, float mass, int count, bool overflow) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float r2 = __shfl_xor_sync(0xffffffffu, race, o), x2 = __shfl_xor_sync(0xffffffffu, x, o);
-    const int i2 = __shfl_xor_sync(0xffffffffu, id, o);
-    if (better(r2, i2, race, id)) {
-      race = r2;
-      x = x2;
-      id = i2;
-    }
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+// The candidates of all CTAs' lists, brought to the first one, which settles the row.
+template <class R, class Kept, class Finish>
+__device__ __forceinline__ void resolve(R& row, float c, float most, const Kept& kept, const Finish& finish) {
+  constexpr int kEach = kCandidates / kThreads;
+  const SampleParams& p = row.p;
+  Smem& sh = row.sh;
+  const cg::cluster_group cluster = cg::this_cluster();
+  if (row.rank != 0) {  // its lists stay until they have been read
+    cluster.barrier_arrive();
+    cluster.barrier_wait();
+    return;
   }
-  count = __reduce_add_sync(0xffffffffu, count);
-  overflow = __any_sync(0xffffffffu, overflow);
-  __syncthreads();  // what the last pass left here has been read
-  if (lane == 0) {
-    Found& f = sh.warps[warp];
-    f.race = race;
-    f.x = x;
-    f.id = id;
-    f.mass = mass;
-    f.count = count;
-    f.overflow = overflow;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lists = kWarps * p.ctas;
+  const auto of = [&](int cta) { return p.ctas == 1 ? &sh : cluster.map_shared_rank(&sh, cta); };
+  if (warp == 0) {  // where each list begins: four of them to a lane
+    static_assert(kWarps * kMostCtas <= 4 * 32, "lists over the lanes");
+    int n[4], run = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int l = 4 * lane + e;
+      n[e] = l < lists ? of(l / kWarps)->here[l % kWarps] : 0;
+      run += n[e];
+    }
+    int end = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    int at = end - run;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sh.base[4 * lane + e] = at;
+      at += n[e];
+    }
+    if (lane == 31) sh.base[4 * 32] = at;
   }
   __syncthreads();
-  Found all = sh.warps[0];
-#pragma unroll 4
-  for (int w = 1; w < kWarps; ++w) {
-    const Found& f = sh.warps[w];
-    if (better(f.race, f.id, all.race, all.id)) {
-      all.race = f.race;
-      all.x = f.x;
-      all.id = f.id;
+  const int total = sh.base[kWarps * kMostCtas];
+  float x[kEach], r[kEach], w[kEach];
+  int id[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * kThreads;
+    x[e] = -INFINITY;
+    id[e] = INT_MAX;
+    r[e] = -INFINITY;
+    w[e] = 0.f;
+    if (i >= total) continue;
+    int lo = 0, hi = lists;  // base[lo] <= i < base[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sh.base[mid] <= i) lo = mid;
+      else hi = mid;
     }
-    all.mass += f.mass;
-    all.count += f.count;
-    all.overflow |= f.overflow;
+    const Smem* from = of(lo / kWarps);
+    x[e] = from->x[lo % kWarps][i - sh.base[lo]];
+    id[e] = from->id[lo % kWarps][i - sh.base[lo]];
+    r[e] = __ldg(row.noise + id[e]);
   }
-  return all;
-}
-
-__device__ __forceinline__ Found merge(const Found* rows, int ctas) {
-  Found all = rows[0];
-  for (int c = 1; c < ctas; ++c) {
-    const Found& f = rows[c];
-    if (better(f.race, f.id, all.race, all.id)) {
-      all.race = f.race;
-      all.x = f.x;
-      all.id = f.id;
+  if (p.ctas > 1) cluster.barrier_arrive();  // the lists have been read
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (id[e] != INT_MAX) {
+      const float y = (x[e] - most) * c;
+      r[e] = y - log2f(tame_noise(r[e]));
+      w[e] = exp2_approx(y);
     }
-    all.mass += f.mass;
-    all.count += f.count;
-    all.overflow |= f.overflow;
+  // what lies before a place, and the best race there
+  const auto look = [&](const Pivot& at) {
+    Found f{-INFINITY, -INFINITY, INT_MAX, 0.f, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (id[e] != INT_MAX && at.before(x[e], id[e])) combine(f, Found{r[e], x[e], id[e], w[e], 1, 0});
+    return row.of_cta(f);
+  };
+  Found now = look(Pivot{-INFINITY, INT_MAX});
+  Pivot at{now.x, now.id};
+  bool done = false;
+  for (int round = 0; round < kRounds && !done; ++round) {
+    at = Pivot{now.x, now.id};
+    const Found f = look(at);
+    done = kept(at.x, f.count, f.mass);
+    if (!done) now = f;
   }
-  return all;
+  if (!done) now = look(last_kept(at, most, p.vocab, kept, look));
+  finish(now);
+  if (p.ctas > 1) cluster.barrier_wait();
 }
 
 template <class T, bool kHeld>
@@ -357,37 +480,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (lane == __ffs(who) - 1) key = 0;
     }
   }
-  {
-    float m = top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = sum * exp2_approx((top - m) * c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      sh.warps[warp].max = m;
-      sh.warps[warp].sum = s;
-      sh.warps[warp].bound = bound;
-    }
-  }
-  __syncthreads();
-  Found mine = {};
-  mine.max = -FLT_MAX;
-  mine.bound = INFINITY;
-  for (int w = 0; w < kWarps; ++w) {
-    mine.max = fmaxf(mine.max, sh.warps[w].max);
-    mine.bound = fminf(mine.bound, sh.warps[w].bound);
-  }
-  for (int w = 0; w < kWarps; ++w) mine.sum = fmaf(sh.warps[w].sum, exp2_approx((sh.warps[w].max - mine.max) * c), mine.sum);
-  if (p.ctas > 1) cg::this_cluster().barrier_wait();
-  const Found* all = row.exchange(mine);
-  float most = -FLT_MAX, z = 0.f;
-  bound = INFINITY;
-  for (int i = 0; i < p.ctas; ++i) {
-    most = fmaxf(most, all[i].max);
-    bound = fminf(bound, all[i].bound);
-  }
-  for (int i = 0; i < p.ctas; ++i) z = fmaf(all[i].sum, exp2_approx((all[i].max - most) * c), z);
+  const First whole = row.of_row(First{top, sum, bound}, c);
+  const float most = whole.max, z = whole.sum;
+  bound = whole.bound;
   if (z == 0.f) {  // nothing above -inf
     answer(-1, NAN);
     return;
@@ -401,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     row.every([&](float x, int i) {
       if (x == most) first = min(first, i);
     });
-    finish(merge(row.exchange(gather(sh, first == INT_MAX ? -INFINITY : 0.f, most, first, 0.f, 0, false)), p.ctas));
+    finish(row.of_row(Found{first == INT_MAX ? -INFINITY : 0.f, most, first, 0.f, 0, 0}));
     return;
   }
 
@@ -480,22 +575,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     best_of_thread();
   };
 
+  const auto raced = [&]() { return Found{race, best_x, best, 0.f, 0, 0}; };
+  // A token with `count` tokens before it, whose w sum to `mass`: is it kept?
+  const auto kept = [&](float x, int count, float mass) {
+    return count == 0 || (count < limit && (!by_p || mass < top_p * z) && (!by_floor || exp2_approx((x - most) * c) >= floor));
+  };
+  const bool limits = limit != INT_MAX || by_p || by_floor;
   bool listed = bound > -INFINITY;
-  int here = 0;  // candidates of this warp
-  Found now = {};
   if (listed) {
+    int here = 0;  // candidates of this warp
     float mass = 0.f;
-    bool overflow = false;
     const auto list = [&](bool hit, float x, int i) {
       const uint32_t hits = __ballot_sync(0xffffffffu, hit);
       const int at = here + __popc(hits & ((1u << lane) - 1u));
-      if (hit) {
+      if (hit && at < kList) {
         mass += exp2_approx((x - most) * c);
-        if (at < kList) {
-          sh.x[warp][at] = x;
-          sh.id[warp][at] = i;
-          run(x, i, tame_noise(__ldg(row.noise + i)));
-        }
+        sh.x[warp][at] = x;
+        sh.id[warp][at] = i;
       }
       here += __popc(hits);
     };
@@ -516,94 +612,46 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
       for (int j = 0; j < kN; ++j) list(any && x[j] >= bound, any ? x[j] : 0.f, row.head + v * kN + j);
     }
-    overflow = here > kList;
-    here = min(here, kList);
-    best_of_thread();
-    now = merge(row.exchange(gather(sh, race, best_x, best, mass, 0, overflow)), p.ctas);
+    if (lane == 0) sh.here[warp] = min(here, kList);
+    const Found f = row.of_row(Found{-INFINITY, 0.f, INT_MAX, mass, lane == 0 ? min(here, kList) : 0, here > kList});
     // (where the sums of w before the bound reach p Z, but for their rounding)
-    listed = !now.overflow && (!tried || bound == sure || now.mass >= top_p * z * (1.f + 0x1p-18f));
+    listed = !f.flags && f.count <= kCandidates && (!tried || bound == sure || f.mass >= top_p * z * (1.f + 0x1p-18f));
+    if (listed) {
+      resolve(row, c, most, kept, finish);
+      return;
+    }
   }
-  if (!listed) {
-    race_all(sure, Pivot{-INFINITY, INT_MAX});
-    now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
-  }
-  if (limit == INT_MAX && !by_p && !by_floor) {
+  race_all(sure, Pivot{-INFINITY, INT_MAX});
+  Found now = row.of_row(raced());
+  if (!limits) {
     finish(now);
     return;
   }
 
   // Rounds: is the winner kept?  Else the race among those ranked before it.
-  const auto kept = [&](float x, int count, float mass) {
-    return count == 0 || (count < limit && (!by_p || mass < top_p * z) && (!by_floor || exp2_approx((x - most) * c) >= floor));
-  };
-  // the tokens before the pivot, and with `again` their race
-  const auto check = [&](const Pivot& at, bool again) {
+  const auto check = [&](const Pivot& at) {
     float mass = 0.f;
     int count = 0;
-    race = best_x = -INFINITY;
-    best = INT_MAX;
-    if (listed) {
-      for (int j = lane; j < here; j += 32) {
-        const float x = sh.x[warp][j];
-        const int i = sh.id[warp][j];
-        if (!at.before(x, i)) continue;
-        mass += exp2_approx((x - most) * c);
-        ++count;
-        if (again) run(x, i, tame_noise(__ldg(row.noise + i)));
-      }
-      best_of_thread();
-    } else {
-      row.every([&](float x, int i) {
-        if (!at.before(x, i)) return;
-        mass += exp2_approx((x - most) * c);
-        ++count;
-      });
-    }
-    return merge(row.exchange(gather(sh, race, best_x, best, mass, count, false)), p.ctas);
+    row.every([&](float x, int i) {
+      if (!at.before(x, i)) return;
+      mass += exp2_approx((x - most) * c);
+      ++count;
+    });
+    return row.of_row(Found{-INFINITY, 0.f, INT_MAX, mass, count, 0});
   };
   Pivot at{now.x, now.id};
   for (int round = 0; round < kRounds; ++round) {
     at = Pivot{now.x, now.id};
-    const Found f = check(at, true);
+    const Found f = check(at);
     if (kept(at.x, f.count, f.mass)) {
       finish(now);
       return;
     }
-    if (listed) {
-      now = f;
-    } else {
-      race_all(sure, at);
-      now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
-    }
+    race_all(sure, at);
+    now = row.of_row(raced());
   }
-  // The last kept place by bisection, first the logit, then the id: (hi, 0) is kept, (lo, 0), behind
-  // the last winner that was not, is not.
-  uint32_t lo = key_of(at.x) - 1, hi = key_of(most);
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const Found f = check(Pivot{of_key(mid), 0}, false);
-    if (kept(of_key(mid), f.count, f.mass))
-      hi = mid;
-    else
-      lo = mid;
-  }
-  int in = 0, out = p.vocab;  // the place (hi, in) is kept, (hi, out) is not or there is none
-  while (out - in > 1) {
-    const int mid = in + (out - in) / 2;
-    const Found f = check(Pivot{of_key(hi), mid}, false);
-    if (kept(of_key(hi), f.count, f.mass))
-      in = mid;
-    else
-      out = mid;
-  }
-  const Pivot last{of_key(hi), in + 1};  // before this: everything kept
-  if (listed) {
-    now = check(last, true);
-  } else {
-    race_all(sure, last);
-    now = merge(row.exchange(gather(sh, race, best_x, best, 0.f, 0, false)), p.ctas);
-  }
-  finish(now);
+  race_all(sure, last_kept(at, most, p.vocab, kept, check));
+  finish(row.of_row(raced()));
 }
 
 template <class T>
