@@ -839,7 +839,8 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
  * T = 0 takes the first largest logit.  out_ids[r] = -1 if no logit is above
  * -inf, or if T is negative, infinite or NaN, or top_p or min_p NaN.
  * log_probs[r] = (x - max x) / T - log Z of the token drawn, before the limits
- * (with T = 1 where T = 0); NaN for id -1.
+ * (with T = 1 where T = 0); NaN for id -1.  (id -2 would say that the logits did
+ * not reach shared memory within seconds: a fault of the device, not of the call.)
  *   logits       device [rows][row_stride], PKV_LOGITS_F32 / BF16 / F16
  *   noise        device float [rows][noise_stride], noise_stride >= vocab; not
  *                read for rows with T = 0; may be NULL if no row draws

@@ -47,6 +47,9 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
 constexpr int kLeast = 4096;         // tokens of a CTA that make another one worth its barrier
 constexpr int kMostHeld = 100 << 10;  // bytes of logits in a CTA's shared memory
+constexpr int kChunk = 2 * kThreads;  // 16-byte vectors of a copy there
+constexpr int kChunks = (kMostHeld / 16 + kChunk - 1) / kChunk;
+constexpr uint32_t kWaitUs = 2000000;  // limit of the waits for the copies
 constexpr int kList = 64;            // candidates of a warp
 constexpr int kMostQ = 16;
 constexpr int kTryQ = 4;             // of the bound tried for top-p
@@ -135,6 +138,10 @@ struct Found {
   float mass;        // the sum of w of the tokens asked about
   int count, flags;  // how many they are; whether a list overflowed
 };
+struct Tally {  // of the lists
+  float mass;
+  int count, overflow;
+};
 __device__ __forceinline__ bool better(float r, int i, float than, int id) { return r > than || (r == than && i < id); }
 __device__ __forceinline__ void combine(First& a, const First& b, float c) {
   const float m = fmaxf(a.max, b.max);
@@ -163,6 +170,13 @@ __device__ __forceinline__ void over_lanes(First& f, int n, float c) {
     combine(f, g, c);
   }
 }
+__device__ __forceinline__ void over_lanes(Tally& f, int n) {
+  for (int o = n / 2; o > 0; o >>= 1) {
+    f.mass += __shfl_xor_sync(0xffffffffu, f.mass, o);
+    f.count += __shfl_xor_sync(0xffffffffu, f.count, o);
+    f.overflow |= __shfl_xor_sync(0xffffffffu, f.overflow, o);
+  }
+}
 __device__ __forceinline__ void over_lanes(Found& f, int n) {
   for (int o = n / 2; o > 0; o >>= 1) {
     Found g;
@@ -184,16 +198,17 @@ struct Pivot {
 
 struct Smem {
   First firsts[kWarps], first_rows[kMostCtas];
+  Tally tallies[kWarps], tally_rows[kMostCtas];
   Found warps[2][kWarps], rows[2][kMostCtas];  // two of each: one is read while the next is written
   float x[kWarps][kList];
   int id[kWarps][kList], here[kWarps];
-  int base[kWarps * kMostCtas + 1];
+  uint64_t landed[kChunks];
 };
 
 template <class T, bool kHeld>
 struct Row {
   static constexpr int kN = Wide<T>::kN;
-  static constexpr int kBatch = kHeld ? 8 : 4;  // 16-byte loads in flight per thread
+  static constexpr int kBatch = 4;  // 16-byte loads in flight per thread, where they are not held
   const SampleParams& p;
   Smem& sh;
   uint4* held;               // the part's logits, if they are held
@@ -221,9 +236,11 @@ struct Row {
     if (rank != 0 || (int)threadIdx.x >= loose) return -1;
     return (int)threadIdx.x < head ? (int)threadIdx.x : (int)threadIdx.x + vectors * kN;
   }
+  __device__ __forceinline__ void raw(int v, float (&x)[kN]) const {
+    Wide<T>::widen(kHeld ? held[v - v0] : __ldg(reinterpret_cast<const uint4*>(logits + head) + v), x);
+  }
   __device__ __forceinline__ void vector(int v, float (&x)[kN]) const {
-    const uint4 raw = kHeld ? held[v - v0] : __ldg(reinterpret_cast<const uint4*>(logits + head) + v);
-    Wide<T>::widen(raw, x);
+    raw(v, x);
 #pragma unroll
     for (int e = 0; e < kN; ++e) x[e] = tame(x[e]);
   }
@@ -260,6 +277,23 @@ struct Row {
     if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = f;
     cluster.sync();
     f = sh.rows[turn][threadIdx.x & (p.ctas - 1)];
+    over_lanes(f, p.ctas);
+    return f;
+  }
+  // (once, after the one of First)
+  __device__ __forceinline__ Tally of_row(Tally f) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    over_lanes(f, 32);
+    if (lane == 0) sh.tallies[warp] = f;
+    __syncthreads();
+    f = sh.tallies[lane % kWarps];
+    over_lanes(f, kWarps);
+    if (p.ctas == 1) return f;
+    const cg::cluster_group cluster = cg::this_cluster();
+    Tally* to = &sh.tally_rows[rank];
+    if ((int)threadIdx.x < p.ctas) *cluster.map_shared_rank(to, threadIdx.x) = f;
+    cluster.sync();
+    f = sh.tally_rows[threadIdx.x & (p.ctas - 1)];
     over_lanes(f, p.ctas);
     return f;
   }
@@ -307,72 +341,55 @@ __device__ Pivot last_kept(const Pivot& out, float most, int vocab, const Kept& 
   return Pivot{of_key(hi), in + 1};
 }
 
-// The candidates of all CTAs' lists, brought to the first one, which settles the row.
+struct Candidates {
+  float x[kCandidates], noise[kCandidates];
+  int id[kCandidates];
+};
+
+// The candidates of all CTAs' lists, brought to the first one, which settles the row.  noise: of this
+// lane's entries of its warp's list.  The logits held in shared memory make room for them.
 template <class R, class Kept, class Finish>
-__device__ __forceinline__ void resolve(R& row, float c, float most, const Kept& kept, const Finish& finish) {
+__device__ __forceinline__ void resolve(R& row, const float (&noise)[kList / 32], int total, float c, float most,
+                                        const Kept& kept, const Finish& finish) {
   constexpr int kEach = kCandidates / kThreads;
   const SampleParams& p = row.p;
   Smem& sh = row.sh;
   const cg::cluster_group cluster = cg::this_cluster();
-  if (row.rank != 0) {  // its lists stay until they have been read
-    cluster.barrier_arrive();
-    cluster.barrier_wait();
-    return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Candidates* mine = reinterpret_cast<Candidates*>(row.held);
+  {
+    Candidates* to = p.ctas == 1 ? mine : cluster.map_shared_rank(mine, 0);
+    int at = 0;  // of the warp's list among all
+    if (p.ctas > 1)
+      for (int i = 0; i < row.rank; ++i) at += sh.tally_rows[i].count;
+    for (int w = 0; w < warp; ++w) at += sh.here[w];
+#pragma unroll
+    for (int e = 0; e < kList / 32; ++e) {
+      const int j = lane + 32 * e;
+      if (j >= sh.here[warp]) break;
+      to->x[at + j] = sh.x[warp][j];
+      to->id[at + j] = sh.id[warp][j];
+      to->noise[at + j] = noise[e];
+    }
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lists = kWarps * p.ctas;
-  const auto of = [&](int cta) { return p.ctas == 1 ? &sh : cluster.map_shared_rank(&sh, cta); };
-  if (warp == 0) {  // where each list begins: four of them to a lane
-    static_assert(kWarps * kMostCtas <= 4 * 32, "lists over the lanes");
-    int n[4], run = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int l = 4 * lane + e;
-      n[e] = l < lists ? of(l / kWarps)->here[l % kWarps] : 0;
-      run += n[e];
-    }
-    int end = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += v;
-    }
-    int at = end - run;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sh.base[4 * lane + e] = at;
-      at += n[e];
-    }
-    if (lane == 31) sh.base[4 * 32] = at;
-  }
-  __syncthreads();
-  const int total = sh.base[kWarps * kMostCtas];
+  if (p.ctas > 1) cluster.sync();
+  else __syncthreads();
+  if (row.rank != 0) return;
   float x[kEach], r[kEach], w[kEach];
   int id[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int i = threadIdx.x + e * kThreads;
-    x[e] = -INFINITY;
-    id[e] = INT_MAX;
-    r[e] = -INFINITY;
+    x[e] = i < total ? mine->x[i] : -INFINITY;
+    id[e] = i < total ? mine->id[i] : INT_MAX;
+    r[e] = i < total ? mine->noise[i] : 1.f;
     w[e] = 0.f;
-    if (i >= total) continue;
-    int lo = 0, hi = lists;  // base[lo] <= i < base[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sh.base[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const Smem* from = of(lo / kWarps);
-    x[e] = from->x[lo % kWarps][i - sh.base[lo]];
-    id[e] = from->id[lo % kWarps][i - sh.base[lo]];
-    r[e] = __ldg(row.noise + id[e]);
   }
-  if (p.ctas > 1) cluster.barrier_arrive();  // the lists have been read
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
     if (id[e] != INT_MAX) {
       const float y = (x[e] - most) * c;
-      r[e] = y - log2f(tame_noise(r[e]));
+      r[e] = y - log2f(r[e]);
       w[e] = exp2_approx(y);
     }
   // what lies before a place, and the best race there
@@ -394,22 +411,44 @@ __device__ __forceinline__ void resolve(R& row, float c, float most, const Kept&
   }
   if (!done) now = look(last_kept(at, most, p.vocab, kept, look));
   finish(now);
-  if (p.ctas > 1) cluster.barrier_wait();
 }
 
-template <class T, bool kHeld>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+// kPerSm: three CTAs per SM spill a little (40 registers), but more than two waves of CTAs are faster
+// with them (256 fp32 rows of 128256 73 us, by twos 85 us), fewer are not (32 bf16 rows 21 and 18.5 us).
+template <class T, bool kHeld, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleParams p) {
   extern __shared__ uint4 held[];
   __shared__ Smem sh;
   using R = Row<T, kHeld>;
   constexpr int kN = R::kN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_id = blockIdx.x / p.ctas;
+  if (kHeld) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&sh.landed[i]), 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   // no CTA writes into another's shared memory before that one runs
   if (p.ctas > 1) cg::this_cluster().barrier_arrive();
   pdl_wait();
   pdl_launch_dependents();
   R row(p, sh, held);
+  if (kHeld && threadIdx.x == 0) {
+    for (int i = 0, v = row.v0; v < row.v1; ++i, v += kChunk) {
+      const uint32_t bytes = min(kChunk, row.v1 - v) * 16;
+      mbar_arrive_expect_tx(smem_u32(&sh.landed[i]), bytes);
+      bulk_load(smem_u32(held + (v - row.v0)), row.logits + row.head + (size_t)v * kN, bytes, smem_u32(&sh.landed[i]));
+    }
+  }
+  // a copy in flight needs its CTA's shared memory
+  const auto all_landed = [&]() {
+    bool good = true;
+    if (kHeld)
+      for (int i = 0, v = row.v0; v < row.v1; ++i, v += kChunk) good &= mbar_wait_bounded(smem_u32(&sh.landed[i]), 0, kWaitUs);
+    return good;
+  };
   const float temp = p.temperature ? p.temperature[row_id] : 1.f;
   const float top_p = p.top_p ? p.top_p[row_id] : 1.f, floor = p.min_p ? p.min_p[row_id] : 0.f;
   const int want_k = p.top_k ? p.top_k[row_id] : 0;
@@ -422,31 +461,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   };
   if (!(temp >= 0.f && temp < INFINITY) || top_p != top_p || floor != floor || (!greedy && !p.noise)) {
     answer(-1, NAN);
+    all_landed();
     if (p.ctas > 1) cg::this_cluster().barrier_wait();
     return;
   }
   const float c = greedy ? 1.4426950408889634f : fminf(1.4426950408889634f / temp, FLT_MAX);
   const int limit = want_k > 0 && want_k < p.vocab ? want_k : INT_MAX;
 
-  // First pass: the largest logit and the sum of w.
-  float top = -FLT_MAX, sum = 0.f;
-  const auto take = [&](const float* x, int n) {
-    float most = x[0];
+  // First pass: the largest logit and the sum of w, first as if all logits were finite or -inf: the sum
+  // of 2^(c x - at), one operation before the exponential, `at` near c times the largest one so far.
+  float top = -FLT_MAX, at = -FLT_MAX, sum = 0.f;
+  const auto take = [&](const float (&x)[kN]) {
+    float m = x[0];
 #pragma unroll
-    for (int e = 1; e < n; ++e) most = fmaxf(most, x[e]);
-    if (most > top) {
-      sum *= exp2_approx((top - most) * c);
-      top = most;
+    for (int e = 1; e < kN; ++e) m = fmaxf(m, x[e]);
+    if (m > top) {
+      const float now = __fmul_rn(m, c);
+      sum *= exp2_approx(at - now);
+      at = now;
+      top = m;
     }
+    float part = 0.f;
 #pragma unroll
-    for (int e = 0; e < n; ++e) sum += exp2_approx((x[e] - top) * c);
+    for (int e = 0; e < kN; ++e) part += exp2_approx(fmaf(x[e], c, -at));
+    sum += part;
   };
-  {
-    const int i = row.extra();
-    if (i >= 0) {
-      const float x[1] = {tame(Wide<T>::one(row.logits[i]))};
-      take(x, 1);
+  bool good = true;  // the logits have arrived
+  if (kHeld) {
+#pragma unroll 2
+    for (int v = row.v0 + threadIdx.x, i = 0; v < row.v1; v += kThreads, ++i) {
+      if (i % (kChunk / kThreads) == 0) good &= mbar_wait_bounded(smem_u32(&sh.landed[i / (kChunk / kThreads)]), 0, kWaitUs);
+      float x[kN];
+      Wide<T>::widen(held[v - row.v0], x);
+      take(x);
     }
+  } else {
     const uint4* src = reinterpret_cast<const uint4*>(row.logits + row.head);
     for (int v = row.v0 + threadIdx.x; v < row.v1; v += R::kBatch * kThreads) {
       uint4 raw[R::kBatch];
@@ -456,15 +505,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
       for (int u = 0; u < R::kBatch; ++u) {
         if (v + u * kThreads >= row.v1) break;
-        if (kHeld) held[v + u * kThreads - row.v0] = raw[u];
         float x[kN];
         Wide<T>::widen(raw[u], x);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) x[e] = tame(x[e]);
-        take(x, kN);
+        take(x);
       }
     }
   }
+  // Not so, or c x so large that its rounding shows, or one token more: again, one by one.  (No logit at
+  // all leaves `at` where it was.)
+  if (!(sum < INFINITY) || !(fabsf(at) < 0x1p20f) || row.extra() >= 0) {
+    top = -FLT_MAX;
+    sum = 0.f;
+    row.every([&](float x, int) {
+      if (x > top) {
+        sum *= exp2_approx((top - x) * c);
+        top = x;
+      }
+      sum += exp2_approx((x - top) * c);
+    });
+  } else {
+    sum *= exp2_approx(-fmaf(top, c, -at));  // from the rounded place to the exact one
+  }
+  if (!good) sum = NAN;  // every CTA of the row will see it
   // the q-th largest of the warp's thread maxima: with that many in every warp, at least `limit`
   const int teams = kWarps * p.ctas;
   const bool by_k = limit != INT_MAX && (limit + teams - 1) / teams <= kMostQ;
@@ -483,7 +545,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const First whole = row.of_row(First{top, sum, bound}, c);
   const float most = whole.max, z = whole.sum;
   bound = whole.bound;
-  if (z == 0.f) {  // nothing above -inf
+  if (!(z > 0.f)) {  // nothing above -inf, or (NaN) logits that did not arrive
+    if (z != z) {
+      all_landed();
+      answer(-2, NAN);
+      return;
+    }
     answer(-1, NAN);
     return;
   }
@@ -535,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const float x = tame(Wide<T>::one(row.logits[i]));
       if (in(x, i)) run(x, i, tame_noise(row.noise[i]));
     }
-    constexpr int kSteps = 2;
+    constexpr int kSteps = kN == 4 ? 2 : 1;
     for (int v = row.v0 + threadIdx.x; v < row.v1; v += kSteps * kThreads) {
       float e[kSteps][kN], x[kSteps][kN];
 #pragma unroll
@@ -602,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       float x[kN];
       bool any = false;
       if (v < row.v1) {
-        row.vector(v, x);
+        row.raw(v, x);
         float m = x[0];
 #pragma unroll
         for (int j = 1; j < kN; ++j) m = fmaxf(m, x[j]);
@@ -610,14 +677,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }
       if (!__any_sync(0xffffffffu, any)) continue;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) list(any && x[j] >= bound, any ? x[j] : 0.f, row.head + v * kN + j);
+      for (int j = 0; j < kN; ++j) list(any && x[j] >= bound, any ? tame(x[j]) : 0.f, row.head + v * kN + j);
     }
-    if (lane == 0) sh.here[warp] = min(here, kList);
-    const Found f = row.of_row(Found{-INFINITY, 0.f, INT_MAX, mass, lane == 0 ? min(here, kList) : 0, here > kList});
+    const bool overflow = here > kList;
+    here = min(here, kList);
+    if (lane == 0) sh.here[warp] = here;
+    __syncwarp();
+    float chance[kList / 32];  // on its way while the CTAs agree
+#pragma unroll
+    for (int e = 0; e < kList / 32; ++e)
+      chance[e] = lane + 32 * e < here ? tame_noise(__ldg(row.noise + sh.id[warp][lane + 32 * e])) : 1.f;
+    const Tally f = row.of_row(Tally{mass, lane == 0 ? here : 0, overflow});
     // (where the sums of w before the bound reach p Z, but for their rounding)
-    listed = !f.flags && f.count <= kCandidates && (!tried || bound == sure || f.mass >= top_p * z * (1.f + 0x1p-18f));
+    listed = !f.overflow && f.count <= kCandidates && (!tried || bound == sure || f.mass >= top_p * z * (1.f + 0x1p-18f));
     if (listed) {
-      resolve(row, c, most, kept, finish);
+      resolve(row, chance, f.count, c, most, kept, finish);
       return;
     }
   }
@@ -639,32 +713,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     });
     return row.of_row(Found{-INFINITY, 0.f, INT_MAX, mass, count, 0});
   };
-  Pivot at{now.x, now.id};
+  Pivot place{now.x, now.id};
   for (int round = 0; round < kRounds; ++round) {
-    at = Pivot{now.x, now.id};
-    const Found f = check(at);
-    if (kept(at.x, f.count, f.mass)) {
+    place = Pivot{now.x, now.id};
+    const Found f = check(place);
+    if (kept(place.x, f.count, f.mass)) {
       finish(now);
       return;
     }
-    race_all(sure, at);
+    race_all(sure, place);
     now = row.of_row(raced());
   }
-  race_all(sure, last_kept(at, most, p.vocab, kept, check));
+  race_all(sure, last_kept(place, most, p.vocab, kept, check));
   finish(row.of_row(raced()));
 }
 
 template <class T>
-int launch(const SampleParams& p, cudaLaunchConfig_t cfg) {
+int launch(const SampleParams& p, cudaLaunchConfig_t cfg, int sms) {
   const size_t part = ((size_t)p.vocab / Wide<T>::kN + p.ctas - 1) / p.ctas * 16;
-  const bool held = part <= kMostHeld;
-  cfg.dynamicSmemBytes = held ? part : 0;
-  auto* kernel = held ? sample_kernel<T, true> : sample_kernel<T, false>;
-  if (held) {
-    const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld),
-                               "cudaFuncSetAttribute(sample)");
-    if (rc != PKV_OK) return rc;
-  }
+  const bool held = part <= kMostHeld, many = (int)cfg.gridDim.x > 2 * sms;
+  cfg.dynamicSmemBytes = held && part > sizeof(Candidates) ? part : sizeof(Candidates);
+  auto* kernel = held ? (many ? sample_kernel<T, true, 3> : sample_kernel<T, true, 2>) : sample_kernel<T, false, 2>;
+  const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld),
+                             "cudaFuncSetAttribute(sample)");
+  if (rc != PKV_OK) return rc;
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(sample)");
 }
 
@@ -692,6 +764,8 @@ extern "C" int pkv_sample_logits(const void* logits, int dtype, int rows, int vo
   const int rc = bind_stream_device(stream, &dev);
   if (rc != PKV_OK) return rc;
 
+  const int sms = sm_count(dev);
+  if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
   SampleParams p;
   p.logits = logits;
   p.noise = noise;
@@ -720,7 +794,7 @@ extern "C" int pkv_sample_logits(const void* logits, int dtype, int rows, int vo
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (dtype == PKV_LOGITS_F32) return launch<float>(p, cfg);
-  if (dtype == PKV_LOGITS_BF16) return launch<__nv_bfloat16>(p, cfg);
-  return launch<__half>(p, cfg);
+  if (dtype == PKV_LOGITS_F32) return launch<float>(p, cfg, sms);
+  if (dtype == PKV_LOGITS_BF16) return launch<__nv_bfloat16>(p, cfg, sms);
+  return launch<__half>(p, cfg, sms);
 }
