@@ -11,13 +11,17 @@
 // is being popped, whose place in the stack is known, so that nothing waits for
 // the tables to be written.
 //
-// One cluster of CTAs does a call.  Every CTA works out the sums over all rows by
-// itself (8 bytes a row, from the L2) and keeps them in shared memory; pages and
-// tokens are then shared out over all threads, whatever the rows' lengths, and find
-// their row by bisection.  Lengths and the count may be changed in place, since no
-// CTA writes them before the cluster's barrier says that all have read them.
+// Every CTA works out the sums over all rows by itself (8 bytes a row, from the L2) and keeps them in
+// shared memory; pages and tokens are then shared out over all threads, whatever the rows' lengths, and
+// find their row by bisection.  A small call is one CTA's.  A large one is two kernels: one fills the
+// tables, or copies the pages, and leaves the lengths and the count as they are, since others may still
+// read them; the second changes these -- for a release when its cluster has checked what the first has
+// copied.  (A large grow into other lengths and another count than it reads needs only the first.)  The
+// second kernel's sums are done while the first one runs.
 //
-// Bound: latency.
+// Bound: latency, of five dependent loads and barriers behind a launch: a step of 32 rows and 16 layers
+// takes 4.5 us, 61000 tokens of 64 prompts with their slots in 16 layers 9.3 us (0.8 us of bytes), 131000
+// pages of 128 finished rows 11.3 us (0.2 us of bytes).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -42,6 +46,7 @@ struct StackParams {
   int32_t *tables, *free_pages, *lens_out, *count_out, *cu, *positions, *token_seq, *slots, *d_err;
   long long layer_stride;
   int row_stride, max_blocks, layers, num_pages, rows, T;
+  int fill, commit;  // which half of a call a kernel does: everything but the lengths and the count, and these
 };
 
 __device__ __forceinline__ int blocks_of(int n) { return (n + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS; }
@@ -50,22 +55,21 @@ struct Sums {
   int tokens[kMostRows + 1];  // new tokens of the rows before (grow)
   int pages[kMostRows + 1];   // pages of the rows before, over all layers
   long long warp_tokens[kMostThreads / 32], warp_pages[kMostThreads / 32];
-  int bad;                    // of the cluster's first CTA: a page id that cannot be one
 };
 
 // What row s brings: new tokens and pages per layer; false if it cannot be.
 template <bool kGrow>
 __device__ __forceinline__ bool row_of(const StackParams& p, int s, int& tokens, int& pages) {
-  const int n = p.lens[s];
+  const int n = __ldcg(p.lens + s);
   if (kGrow) {
-    tokens = p.added ? p.added[s] : 1;
+    tokens = p.added ? __ldcg(p.added + s) : 1;
     pages = 0;
     if (n < 0 || tokens < 0 || (long long)n + tokens > (long long)p.max_blocks * PKV_PAGE_TOKENS) return false;
     pages = blocks_of(n + tokens) - blocks_of(n);
     return true;
   }
   tokens = pages = 0;
-  if (!p.finished[s]) return true;
+  if (!__ldcg(p.finished + s)) return true;
   if (n < 0 || n > (long long)p.max_blocks * PKV_PAGE_TOKENS) return false;
   pages = blocks_of(n);
   return true;
@@ -139,30 +143,26 @@ __device__ __forceinline__ int row_at(const int* sums, int rows, int i) {
   return lo;
 }
 
-// One page of the call after another: row, layer and block.
+// One popped page of the call after another: row, layer and block.
 struct PageAt {
   int row, left, layer, block, first, per;  // left: pages of the row from this one on
-  __device__ __forceinline__ void seek(const StackParams& p, const Sums& sh, bool grow, int i) {
+  __device__ __forceinline__ void seek(const StackParams& p, const Sums& sh, int i) {
     row = row_at(sh.pages, p.rows, i);
-    enter(p, sh, grow, i - sh.pages[row]);
+    enter(p, sh, i - sh.pages[row]);
   }
-  __device__ __forceinline__ void enter(const StackParams& p, const Sums& sh, bool grow, int within) {
+  __device__ __forceinline__ void enter(const StackParams& p, const Sums& sh, int within) {
     const int need = sh.pages[row + 1] - sh.pages[row];
     per = need / p.layers;
-    first = 0;
-    if (grow) {  // behind the pages that the row has: the sums say where its new tokens end
-      const int n = p.lens[row];
-      first = blocks_of(n);
-    }
+    first = blocks_of(p.lens[row]);  // behind the pages that the row has
     left = need - within;
     layer = within / per;
     block = first + within % per;
   }
-  __device__ __forceinline__ void next(const StackParams& p, const Sums& sh, bool grow) {
+  __device__ __forceinline__ void next(const StackParams& p, const Sums& sh) {
     if (--left == 0) {
       do ++row;
       while (row < p.rows && sh.pages[row + 1] == sh.pages[row]);
-      if (row < p.rows) enter(p, sh, grow, 0);
+      if (row < p.rows) enter(p, sh, 0);
     } else if (++block == first + per) {
       block = first;
       ++layer;
@@ -173,31 +173,15 @@ struct PageAt {
   }
 };
 
-__global__ void __launch_bounds__(kMostThreads) grow_kernel(const StackParams p) {
-  __shared__ Sums sh;
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int threads = (int)blockDim.x * ctas, me = rank * (int)blockDim.x + (int)threadIdx.x;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int count = *p.count;
-  long long tokens, pages;
-  const bool good = sum_rows<true>(p, sh, tokens, pages);
-  const bool listed = p.positions || p.token_seq || p.slots;
-  int why = PKV_OK;
-  if (!good || count < 0 || count > p.num_pages || (listed && tokens > p.T) || tokens > 0x7FFFFFFF)
-    why = PKV_ERR_DEVICE_INDEX;
-  else if (pages > count)
-    why = PKV_ERR_POOL_EXHAUSTED;
-  if (why != PKV_OK && me == 0) report_error(p.d_err, why);
-  const int total = why == PKV_OK ? (int)tokens : 0, taken = why == PKV_OK ? (int)pages : 0;
-
+// Table entries, positions, rows and slots: `taken` pages, `total` tokens.
+__device__ __forceinline__ void fill_tables(const StackParams& p, const Sums& sh, int me, int threads, int count, int total,
+                                            int taken, bool listed) {
   bool odd = false;  // an id on the stack that cannot be one
   // pages: a few each, or runs of them
   const int run = taken <= threads ? 1 : kRun;
   for (long long i0 = (long long)me * run; i0 < taken; i0 += (long long)threads * run) {
     PageAt at;
-    at.seek(p, sh, true, (int)i0);
+    at.seek(p, sh, (int)i0);
     const int n = min(run, taken - (int)i0);
     int id[kRun];
 #pragma unroll
@@ -208,7 +192,7 @@ __global__ void __launch_bounds__(kMostThreads) grow_kernel(const StackParams p)
       if (u >= n) break;
       p.tables[at.entry(p)] = id[u];
       odd |= id[u] < 0 || id[u] >= p.num_pages;
-      if (u + 1 < n) at.next(p, sh, true);
+      if (u + 1 < n) at.next(p, sh);
     }
   }
   // tokens: 32 to a warp; a warp takes all layers of them, or a part where there are few
@@ -252,11 +236,39 @@ __global__ void __launch_bounds__(kMostThreads) grow_kernel(const StackParams p)
     }
   }
   if (odd) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
-  if (me == 0) p.cu[p.rows] = total;
-  for (int s = me; s < p.rows; s += threads) p.cu[s] = why == PKV_OK ? sh.tokens[s] : 0;
-  // lengths and count last: they may be the ones read, by the other CTAs too
-  if (ctas > 1) cluster.sync();
-  else __syncthreads();
+}
+
+__global__ void __launch_bounds__(kMostThreads) grow_kernel(const StackParams p) {
+  __shared__ Sums sh;
+  const int threads = (int)(blockDim.x * gridDim.x), me = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  // (behind a kernel for the other half, which has waited itself, what is read here is long there)
+  if (p.fill) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  const int count = __ldcg(p.count);
+  long long tokens, pages;
+  const bool good = sum_rows<true>(p, sh, tokens, pages);
+  const bool listed = p.positions || p.token_seq || p.slots;
+  int why = PKV_OK;
+  if (!good || count < 0 || count > p.num_pages || (listed && tokens > p.T) || tokens > 0x7FFFFFFF)
+    why = PKV_ERR_DEVICE_INDEX;
+  else if (pages > count)
+    why = PKV_ERR_POOL_EXHAUSTED;
+  if (why != PKV_OK && me == 0) report_error(p.d_err, why);  // (the first code stays)
+  const int total = why == PKV_OK ? (int)tokens : 0, taken = why == PKV_OK ? (int)pages : 0;
+
+  if (p.fill) fill_tables(p, sh, me, threads, count, total, taken, listed);
+  if (p.fill) {
+    if (me == 0) p.cu[p.rows] = total;
+    for (int s = me; s < p.rows; s += threads) p.cu[s] = why == PKV_OK ? sh.tokens[s] : 0;
+  }
+  if (!p.commit) return;
+  if (!p.fill) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  __syncthreads();  // they may be the ones read: then this CTA is alone
   for (int s = me; s < p.rows; s += threads) {
     const int n = p.lens[s];
     p.lens_out[s] = why == PKV_OK ? n + (sh.tokens[s + 1] - sh.tokens[s]) : n;
@@ -264,72 +276,102 @@ __global__ void __launch_bounds__(kMostThreads) grow_kernel(const StackParams p)
   if (me == 0) *p.count_out = count - taken;
 }
 
+// The copy (fill) by any number of CTAs; the check of what has been copied and the lengths (commit) by
+// one cluster.
 __global__ void __launch_bounds__(kMostThreads) release_kernel(const StackParams p) {
   __shared__ Sums sh;
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int threads = (int)blockDim.x * ctas, me = rank * (int)blockDim.x + (int)threadIdx.x;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int count = *p.count;
+  __shared__ int bad[kMostCtas];  // of the cluster's CTAs: a page id that cannot be one
+  const int threads = (int)(blockDim.x * gridDim.x), me = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  const bool several = p.commit && gridDim.x > 1;
+  if (several) cg::this_cluster().barrier_arrive();
+  // (behind a kernel for the other half, which has waited itself, what is read here is long there)
+  if (p.fill) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  const int count = __ldcg(p.count);
   long long tokens, pages;
-  if (threadIdx.x == 0) sh.bad = 0;
   const bool good = sum_rows<false>(p, sh, tokens, pages);
   const bool fits = good && count >= 0 && count <= p.num_pages && pages <= p.num_pages - count;
-  if (ctas > 1) cluster.sync();  // every CTA runs, and has cleared its word
-  bool odd = false;
   const int total = fits ? (int)pages : 0;
-  const int run = total <= threads ? 1 : kRun;
-  for (long long i0 = (long long)me * run; i0 < total; i0 += (long long)threads * run) {
-    PageAt at;
-    at.seek(p, sh, false, (int)i0);
-    const int n = min(run, total - (int)i0);
-    int id[kRun];
-#pragma unroll
-    for (int u = 0; u < kRun; ++u) {
-      if (u < n) {
-        id[u] = p.tables[at.entry(p)];
-        if (u + 1 < n) at.next(p, sh, false);
-      }
+  int32_t* to = p.free_pages + (fits ? count : 0);  // of no meaning until the count says so
+  if (p.fill) {
+    // a warp for each row and layer: its pages lie side by side in the table and on the stack
+    const int units = fits ? p.rows * p.layers : 0, lane = threadIdx.x & 31;
+    for (int u = me / 32; u < units; u += threads / 32) {
+      const int row = u / p.layers, layer = u % p.layers;
+      const int need = sh.pages[row + 1] - sh.pages[row];
+      if (need == 0) continue;
+      const int n = need / p.layers;
+      const int32_t* from = p.tables + layer * p.layer_stride + (long long)row * p.row_stride;
+      int32_t* here = to + sh.pages[row] + layer * n;
+#pragma unroll 4
+      for (int i = lane; i < n; i += 32) here[i] = from[i];
     }
-#pragma unroll
-    for (int u = 0; u < kRun; ++u)
-      if (u < n) {
-        p.free_pages[count + (int)i0 + u] = id[u];  // of no meaning until the count says so
-        odd |= id[u] < 0 || id[u] >= p.num_pages;
-      }
   }
-  if (odd) *cluster.map_shared_rank(&sh.bad, 0) = 1;
-  if (ctas > 1) cluster.sync();
-  else __syncthreads();
-  const bool done = fits && *cluster.map_shared_rank(&sh.bad, 0) == 0;
+  if (!p.commit) return;
+  if (!p.fill) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  __syncthreads();
+  bool odd = false;
+#pragma unroll 8
+  for (int i = me; i < total; i += threads) {
+    const int id = __ldcg(to + i);
+    odd |= id < 0 || id >= p.num_pages;
+  }
+  odd = __syncthreads_or(odd);
+  if (several) {
+    const cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_wait();  // all of them run
+    if (threadIdx.x < gridDim.x) *cluster.map_shared_rank(&bad[blockIdx.x], threadIdx.x) = odd;
+    cluster.sync();
+    for (int c = 0; c < (int)gridDim.x; ++c) odd |= bad[c] != 0;
+  }
+  const bool done = fits && !odd;
   if (!done && me == 0) report_error(p.d_err, PKV_ERR_DEVICE_INDEX);
   for (int s = me; s < p.rows; s += threads) {
     const int n = p.lens[s];
     p.lens_out[s] = done && p.finished[s] ? 0 : n;
   }
   if (me == 0) *p.count_out = done ? count + total : count;
-  if (ctas > 1) cluster.sync();  // the first CTA's word is read until here
 }
 
-// One CTA where little is to be done, else a cluster of eight.
-int launch(void (*kernel)(StackParams), const StackParams& p, long long items, void* stream, const char* what) {
-  const int ctas = items <= 4096 ? 1 : kMostCtas;
+// One kernel of a call: `ctas` CTAs, one cluster if `cluster`.
+int launch(void (*kernel)(StackParams), StackParams p, int fill, int commit, int ctas, int threads, bool cluster,
+           void* stream, const char* what) {
+  p.fill = fill;
+  p.commit = commit;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = cluster ? ctas : 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(items <= 1024 ? 512 : 1024);
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), what);
 }
+
+// Up to kAlone items of a grow (rows over all layers, and slots) and kAloneRows rows over all layers of a
+// release one CTA does a call (a step of 32 rows and 16 layers 4.5 us); with more, as many CTAs as have
+// kShare items each, or a warp for each row and layer (release of 64 rows of 16 layers and up to 125
+// pages: 6.8 us, by one CTA 28.8 us; of 8 such rows 5.9 and 8.4 us; of 4 6.0 us by either).
+constexpr long long kAlone = 1024;
+constexpr int kAloneRows = 64;
+constexpr int kShare = 2048, kFillThreads = 512;
+int fill_ctas(long long items, int sms) {
+  const long long n = (items + kShare - 1) / kShare;
+  return (int)(n < 2 * sms ? n : 2 * sms);
+}
+
+bool overlaps(const int32_t* a, const int32_t* b, int n) { return a < b + n && b < a + n; }
 
 // What both calls refuse on the host.
 int check(const StackParams& p) {
@@ -388,9 +430,17 @@ extern "C" int pkv_grow_block_tables(const int32_t* seq_lens, const int32_t* new
   int dev = 0;
   rc = bind_stream_device(stream, &dev);
   if (rc != PKV_OK) return rc;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
   const long long tokens = positions || token_seq || slots ? T : 0;
-  return launch(grow_kernel, p, (long long)num_seqs * num_layers + tokens * (slots ? num_layers : 1), stream,
-                "cudaLaunchKernelEx(grow)");
+  const long long items = (long long)num_seqs * num_layers + tokens * (slots ? num_layers : 1);
+  const char* what = "cudaLaunchKernelEx(grow)";
+  if (items <= kAlone) return launch(grow_kernel, p, 1, 1, 1, 512, false, stream, what);
+  // lengths and count that are read change behind all that read them, in a kernel of their own
+  const bool in_place = overlaps(seq_lens_out, seq_lens, num_seqs) || free_count_out == free_count;
+  rc = launch(grow_kernel, p, 1, !in_place, fill_ctas(items, sms), kFillThreads, false, stream, what);
+  if (rc != PKV_OK || !in_place) return rc;
+  return launch(grow_kernel, p, 0, 1, 1, 1024, false, stream, what);
 }
 
 extern "C" int pkv_release_pages(const int32_t* seq_lens, const uint8_t* finished, int num_seqs,
@@ -419,5 +469,12 @@ extern "C" int pkv_release_pages(const int32_t* seq_lens, const uint8_t* finishe
   int dev = 0;
   rc = bind_stream_device(stream, &dev);
   if (rc != PKV_OK) return rc;
-  return launch(release_kernel, p, (long long)num_seqs * num_layers * 8, stream, "cudaLaunchKernelEx(release)");
+  const int sms = sm_count(dev);
+  if (sms <= 0) return cuda_status(cudaErrorInvalidDevice, "sm_count");
+  const long long rows = (long long)num_seqs * num_layers;  // of the tables, of a few pages each
+  const char* what = "cudaLaunchKernelEx(release)";
+  if (rows <= kAloneRows) return launch(release_kernel, p, 1, 1, 1, 1024, false, stream, what);
+  rc = launch(release_kernel, p, 1, 0, fill_ctas(rows * (kShare * 32 / kFillThreads), sms), kFillThreads, false, stream, what);
+  if (rc != PKV_OK) return rc;
+  return launch(release_kernel, p, 0, 1, kMostCtas, 1024, true, stream, what);
 }
