@@ -8,7 +8,9 @@
 // order puts a token's V codes 2 bytes apart by 64, and a warp that has all 16 rows
 // of a page arranges them in shared memory and writes 512 bytes at once.
 //
-// Bound: memory, 2.6 KiB per token for K and V and 8 KiB for q.
+// Bound: memory, 2.6 KiB per token for K and V and 8 KiB for q: 14400 tokens of eight prompts, with q, and
+// the 906 pages read back, 38.7 us (29.1 us of bytes); a step of 32 tokens and the read 5.2 us, two launches
+// of five dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -13,18 +13,25 @@
 // A rejected winner is a random token of what is left, so a few rounds are enough; noise
 // that is made to take many is met by bisecting for the last kept token after kRounds.
 //
-// Candidates: k tokens are at least as large as the smallest of the warps' q-th largest
-// thread maxima when there are k / q warps; min-p bounds the logits by max x; for top-p
-// the same bound is tried, and holds if the tokens above it have p of the sum.  So there
-// are usually a few hundred candidates in a row, listed in shared memory warp by warp in
-// order, and only their noise is read.  Where the lists overflow, or without limits, the
-// passes go over all logits.
+// Candidates: k tokens are at least as large as the smallest of the warps' q-th largest thread maxima
+// when there are k / q warps; min-p bounds the logits by max x; for top-p the same bound is tried, and
+// holds if the tokens from it on have p of the sum.  So there are usually a few hundred candidates in a
+// row, listed in shared memory warp by warp in order, and only their noise is read; the row's first CTA
+// gets all lists and settles the row alone.  Where the lists overflow, or without limits, the passes go
+// over all logits, and the CTAs agree behind a cluster barrier after each.
 //
-// A cluster of CTAs has a row: each holds a part of it in shared memory (read once), and
-// after every pass sends its sums and its best to the others, behind a cluster barrier.
-// Sums are over fixed positions in a fixed order; ties of a race go to the lowest id.
+// A cluster of CTAs has a row, each a part of it in shared memory (bulk copies, read from the GPU's memory
+// once).  The first pass takes an operation, an exponential and an addition per logit: the exponent's
+// reference is c times a logit, rounded, and the sum is moved to the exact one at the end (logits that are
+// not finite, or so large that this rounding shows, are summed again one by one).  Sums are over fixed
+// positions in a fixed order; ties of a race go to the lowest id.
 //
-// Bound: memory, the logits read once, and the noise once where there are no limits.
+// Bound: the steps of a row, one after another -- its parts' copies, the first sums, the bound, the lists,
+// the first CTA's rounds, with two cluster barriers -- in as many rows at once as shared memory holds (57 of
+// 128256 fp32 logits).  One such row with top-k and top-p takes 10.4 us, 32 bf16 rows with top-p and min-p
+// 18.6 us, 256 fp32 rows with all limits 72.8 us (the logits alone are 19.3 us of bytes at the measured copy
+// rate, with the noise 38.7 us); 256 rows without limits 108 us, with a top-p that most of a flat row is in
+// 164 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
