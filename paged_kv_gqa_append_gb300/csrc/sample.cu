@@ -30,8 +30,8 @@
 // the first CTA's rounds, with two cluster barriers -- in as many rows at once as shared memory holds (57 of
 // 128256 fp32 logits).  One such row with top-k and top-p takes 10.4 us, 32 bf16 rows with top-p and min-p
 // 18.6 us, 256 fp32 rows with all limits 72.8 us (the logits alone are 19.3 us of bytes at the measured copy
-// rate, with the noise 38.7 us); 256 rows without limits 108 us, with a top-p that most of a flat row is in
-// 164 us.
+// rate, with the noise 38.7 us); 256 rows without limits 89 us, with a top-p that most of a flat row is in
+// 148 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -77,6 +77,12 @@ struct SampleParams {
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float log2_approx(float x) {  // of a normal number
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -259,6 +265,24 @@ struct Row {
     for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
       float x[kN];
       vector(v, x);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) f(x[e], head + v * kN + e);
+    }
+  }
+
+  // the same, but for some of those below x
+  template <class F>
+  __device__ __forceinline__ void every_from(float from, const F& f) const {
+    const int i = extra();
+    if (i >= 0) f(tame(Wide<T>::one(logits[i])), i);
+#pragma unroll 2
+    for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+      float x[kN];
+      vector(v, x);
+      float m = x[0];
+#pragma unroll
+      for (int e = 1; e < kN; ++e) m = fmaxf(m, x[e]);
+      if (m < from) continue;
 #pragma unroll
       for (int e = 0; e < kN; ++e) f(x[e], head + v * kN + e);
     }
@@ -584,44 +608,29 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SamplePa
     sure = fmaxf(sure, most + (y - fabsf(most) * 0x1p-20f));
     bound = fmaxf(bound, sure);
   }
-  const auto score = [&](float x, float e) { return (x - most) * c - __log2f(e); };
-  // a thread's best, its race computed with the accurate logarithm
-  const auto exactly = [&](float x, float e) { return (x - most) * c - log2f(e); };
-  float race = -INFINITY, best_x = -INFINITY, best_e = 1.f;
+  // The race over all logits from `least` on that are ranked before the pivot (`all`: the pivot is behind
+  // everything).  A thread looks for its best with the fast logarithm, then computes that one's again.
+  float race = -INFINITY, best_x = -INFINITY;
   int best = INT_MAX;
-  const auto run = [&](float x, int i, float e) {
-    const float r = score(x, e);
-    if (better(r, i, race, best)) {
-      race = r;
-      best_x = x;
-      best_e = e;
-      best = i;
-    }
-  };
-  const auto best_of_thread = [&]() { race = best == INT_MAX ? -INFINITY : exactly(best_x, best_e); };
-  // the race over all logits from `least` on that are ranked before the pivot
-  const auto race_all = [&](float least, const Pivot& at) {
-    race = best_x = -INFINITY;
+  const auto race_all = [&](float least, const Pivot& at, bool all) {
+    race = -INFINITY;
     best = INT_MAX;
-    const auto in = [&](float x, int i) { return x >= least && at.before(x, i); };
-    const int i = row.extra();
-    if (i >= 0) {
-      const float x = tame(Wide<T>::one(row.logits[i]));
-      if (in(x, i)) run(x, i, tame_noise(row.noise[i]));
-    }
     constexpr int kSteps = kN == 4 ? 2 : 1;
     for (int v = row.v0 + threadIdx.x; v < row.v1; v += kSteps * kThreads) {
       float e[kSteps][kN], x[kSteps][kN];
+      bool any[kSteps];
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
         const int vu = v + u * kThreads;
+        any[u] = false;
         if (vu >= row.v1) break;
         row.vector(vu, x[u]);
-        const int id = row.head + vu * kN;
-        bool any = false;
+        float m = x[u][0];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) any |= in(x[u][j], id + j);
-        if (!any) continue;
+        for (int j = 1; j < kN; ++j) m = fmaxf(m, x[u][j]);
+        any[u] = m >= least && m >= at.x;
+        if (!any[u]) continue;
+        const int id = row.head + vu * kN;
         if (row.wide_noise) {
 #pragma unroll
           for (int j = 0; j < kN; j += 4) {
@@ -638,17 +647,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SamplePa
       }
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
-        const int vu = v + u * kThreads;
-        if (vu >= row.v1) break;
-        const int id = row.head + vu * kN;
+        if (!any[u]) continue;
+        const int id = row.head + (v + u * kThreads) * kN;
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (in(x[u][j], id + j)) run(x[u][j], id + j, tame_noise(e[u][j]));
+        for (int j = 0; j < kN; ++j) {
+          const float r = (x[u][j] - most) * c - log2_approx(tame_noise(e[u][j]));
+          // (ids ascend: the first of equals stays)
+          if (r > race && (all || (x[u][j] >= least && at.before(x[u][j], id + j)))) {
+            race = r;
+            best = id + j;
+          }
+        }
       }
     }
-    best_of_thread();
+    const auto exactly = [&](int i) {
+      best_x = tame(Wide<T>::one(row.logits[i]));
+      return (best_x - most) * c - log2f(tame_noise(row.noise[i]));
+    };
+    best_x = -INFINITY;
+    race = best == INT_MAX ? -INFINITY : exactly(best);
+    const int i = row.extra();
+    if (i >= 0) {
+      const float x = best_x, x2 = tame(Wide<T>::one(row.logits[i]));
+      if (x2 >= least && at.before(x2, i)) {
+        const float r = exactly(i);
+        if (better(r, i, race, best)) {
+          race = r;
+          best = i;
+        } else {
+          best_x = x;
+        }
+      }
+    }
   };
-
   const auto raced = [&]() { return Found{race, best_x, best, 0.f, 0, 0}; };
   // A token with `count` tokens before it, whose w sum to `mass`: is it kept?
   const auto kept = [&](float x, int count, float mass) {
@@ -702,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SamplePa
       return;
     }
   }
-  race_all(sure, Pivot{-INFINITY, INT_MAX});
+  race_all(sure, Pivot{-INFINITY, INT_MAX}, sure == -INFINITY);
   Found now = row.of_row(raced());
   if (!limits) {
     finish(now);
@@ -713,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SamplePa
   const auto check = [&](const Pivot& at) {
     float mass = 0.f;
     int count = 0;
-    row.every([&](float x, int i) {
-      if (!at.before(x, i)) return;
-      mass += exp2_approx((x - most) * c);
-      ++count;
+    row.every_from(at.x, [&](float x, int i) {
+      const bool front = at.before(x, i);
+      mass += front ? exp2_approx((x - most) * c) : 0.f;
+      count += front;
     });
     return row.of_row(Found{-INFINITY, 0.f, INT_MAX, mass, count, 0});
   };
@@ -728,10 +759,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SamplePa
       finish(now);
       return;
     }
-    race_all(sure, place);
+    race_all(sure, place, false);
     now = row.of_row(raced());
   }
-  race_all(sure, last_kept(place, most, p.vocab, kept, check));
+  race_all(sure, last_kept(place, most, p.vocab, kept, check), false);
   finish(row.of_row(raced()));
 }
 
