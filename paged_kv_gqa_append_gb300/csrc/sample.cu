@@ -29,9 +29,9 @@
 // Bound: the steps of a row, one after another -- its parts' copies, the first sums, the bound, the lists,
 // the first CTA's rounds, with two cluster barriers -- in as many rows at once as shared memory holds (57 of
 // 128256 fp32 logits).  One such row with top-k and top-p takes 10.4 us, 32 bf16 rows with top-p and min-p
-// 18.6 us, 256 fp32 rows with all limits 72.8 us (the logits alone are 19.3 us of bytes at the measured copy
+// 18 us, 256 fp32 rows with all limits 61.5 us (the logits alone are 19.3 us of bytes at the measured copy
 // rate, with the noise 38.7 us); 256 rows without limits 89 us, with a top-p that most of a flat row is in
-// 148 us.
+// 146 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,11 +50,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
 constexpr int kLeast = 4096;         // tokens of a CTA that make another one worth its barrier
 constexpr int kMostHeld = 100 << 10;  // bytes of logits in a CTA's shared memory
-constexpr int kChunk = 2 * kThreads;  // 16-byte vectors of a copy there
+constexpr int kChunk = 1024;          // 16-byte vectors of a copy there
 constexpr int kChunks = (kMostHeld / 16 + kChunk - 1) / kChunk;
 constexpr uint32_t kWaitUs = 2000000;  // limit of the waits for the copies
 constexpr int kList = 64;            // candidates of a warp
@@ -209,7 +208,8 @@ struct Pivot {
   __device__ __forceinline__ bool before(float y, int i) const { return y > x || (y == x && i < id); }
 };
 
-struct Smem {
+template <int kWarps>
+struct SmemOf {
   First firsts[kWarps], first_rows[kMostCtas];
   Tally tallies[kWarps], tally_rows[kMostCtas];
   Found warps[2][kWarps], rows[2][kMostCtas];  // two of each: one is read while the next is written
@@ -218,8 +218,10 @@ struct Smem {
   uint64_t landed[kChunks];
 };
 
-template <class T, bool kHeld>
+template <class T, bool kHeld, int kCtaThreads>
 struct Row {
+  static constexpr int kThreads = kCtaThreads, kWarps = kThreads / 32;
+  using Smem = SmemOf<kWarps>;
   static constexpr int kN = Wide<T>::kN;
   static constexpr int kBatch = 4;  // 16-byte loads in flight per thread, where they are not held
   const SampleParams& p;
@@ -382,9 +384,9 @@ struct Candidates {
 template <class R, class Kept, class Finish>
 __device__ __forceinline__ void resolve(R& row, const float (&noise)[kList / 32], int total, float c, float most,
                                         const Kept& kept, const Finish& finish) {
-  constexpr int kEach = kCandidates / kThreads;
+  constexpr int kThreads = R::kThreads, kEach = kCandidates / kThreads;
   const SampleParams& p = row.p;
-  Smem& sh = row.sh;
+  typename R::Smem& sh = row.sh;
   const cg::cluster_group cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Candidates* mine = reinterpret_cast<Candidates*>(row.held);
@@ -444,14 +446,16 @@ __device__ __forceinline__ void resolve(R& row, const float (&noise)[kList / 32]
   finish(now);
 }
 
-// kPerSm: three CTAs per SM spill a little (40 registers), but more than two waves of CTAs are faster
-// with them (256 fp32 rows of 128256 73 us, by twos 85 us), fewer are not (32 bf16 rows 21 and 18.5 us).
-template <class T, bool kHeld, int kPerSm>
-__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const SampleParams p) {
+// kCtaThreads: with 512 a row is done sooner; with 256 a CTA spends less on its reductions, and three of
+// them share an SM, so that many rows with limits are done sooner (256 fp32 rows of 128256 63 us, with 512
+// threads, two CTAs per SM 85 us, three, which spill, 73 us; without limits 99 us, with 512 threads 89 us; 32
+// bf16 rows 23.7 and 18.1 us).
+template <class T, bool kHeld, int kCtaThreads, int kPerSm>
+__global__ void __launch_bounds__(kCtaThreads, kPerSm) sample_kernel(const SampleParams p) {
   extern __shared__ uint4 held[];
-  __shared__ Smem sh;
-  using R = Row<T, kHeld>;
-  constexpr int kN = R::kN;
+  using R = Row<T, kHeld, kCtaThreads>;
+  constexpr int kN = R::kN, kThreads = R::kThreads, kWarps = R::kWarps;
+  __shared__ typename R::Smem sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_id = blockIdx.x / p.ctas;
   if (kHeld) {
@@ -770,8 +774,12 @@ template <class T>
 int launch(const SampleParams& p, cudaLaunchConfig_t cfg, int sms) {
   const size_t part = ((size_t)p.vocab / Wide<T>::kN + p.ctas - 1) / p.ctas * 16;
   const bool held = part <= kMostHeld, many = (int)cfg.gridDim.x > 2 * sms;
+  const bool limits = p.top_k || p.top_p || p.min_p;
   cfg.dynamicSmemBytes = held && part > sizeof(Candidates) ? part : sizeof(Candidates);
-  auto* kernel = held ? (many ? sample_kernel<T, true, 3> : sample_kernel<T, true, 2>) : sample_kernel<T, false, 2>;
+  cfg.blockDim = dim3(held && many && limits ? 256 : 512);
+  auto* kernel = !held ? sample_kernel<T, false, 512, 2>
+                 : !many ? sample_kernel<T, true, 512, 2>
+                         : limits ? sample_kernel<T, true, 256, 3> : sample_kernel<T, true, 512, 3>;
   const int rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld),
                              "cudaFuncSetAttribute(sample)");
   if (rc != PKV_OK) return rc;
@@ -828,7 +836,6 @@ extern "C" int pkv_sample_logits(const void* logits, int dtype, int rows, int vo
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * p.ctas);
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;

@@ -344,6 +344,27 @@ def test_shares_longer_than_the_list_of_ids(lib, cuda_device):
         close(out[s:s + 1], *O4.attend(q[s:s + 1], pool, bt[s:s + 1], lens[s:s + 1], 0.125), lens[s:s + 1])
 
 
+def test_a_cta_for_each_of_many_sequences(lib, cuda_device):
+    """By the bound, every sequence is one CTA's: ragged, longer than the bound says (one beyond the
+    list of ids), empty, refused."""
+    g = np.random.default_rng(72)
+    S = 160
+    lens = g.integers(0, 300, S)
+    lens[[3, 50, S - 1]] = 17000, 0, 700
+    pages = int(sum(-(-n // 16) for n in lens)) + 1
+    pool = random_pages(73, pages)
+    bt = tables_for(74, lens, pages)
+    q = rows(75, S, 32, 64)
+    check(lib, cuda_device, q, pool, bt, lens, max_seq_len=300)
+    bad = [3, 7, 9]
+    lens[[7, 9]] = -2, 2 ** 31 - 1
+    bt[3, 1030] = pages
+    out, code = decode(lib, cuda_device, q, pool, bt, lens, max_seq_len=300)
+    assert code == lib.ERR_DEVICE_INDEX and (out[bad] == 0).all() and (out[50] == 0).all()
+    good = np.setdiff1d(np.arange(S), bad)
+    close(out[good], *O4.attend(q[good], pool, bt[good], lens[good], 0.125), lens[good])
+
+
 def test_pages_behind_4_gib(lib, cuda_device):
     dev, pages, n = cuda_device, 470000, 100
     pool = torch.empty((pages, 8, O4.BLOCK_BYTES), dtype=torch.uint8, device=dev)

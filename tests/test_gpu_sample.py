@@ -210,3 +210,37 @@ def test_streams_graphs_and_refusals(lib, cuda_device):
                     (dict(top_p=T.double()), TypeError), (dict(ids=ids.long()), TypeError), (dict(logprobs=lp[:2]), ValueError)):
         with pytest.raises(err):
             lib.sample_logits(**(dict(logits=x, noise=e) | kw))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_rows_of_a_large_vocabulary(lib, cuda_device, dtype):
+    """More CTAs than two for each SM work in another shape, with limits and without."""
+    dev, rows, vocab = cuda_device, 44, 33001
+    x, e = logits(13, rows, vocab, dtype, dev)
+    x[1::4], x[2::8] = x[1::4] * 0.05, 0.5                         # flat ones, tied ones
+    x[3, 5:], x[7] = -torch.inf, torch.nan
+    x[11, 7], x[11, 9000] = torch.inf, torch.inf
+    g = np.random.default_rng(14)
+    T = np.where(g.random(rows) < 0.1, 0.0, g.uniform(0.4, 1.5, rows))
+    check(lib, dev, x, e, T)
+    check(lib, dev, x, e, T, p=g.uniform(0.3, 1.0, rows))
+    check(lib, dev, x, e, T, k=g.integers(0, 400, rows), floor=g.uniform(-0.02, 0.1, rows))
+    if dtype == torch.float32:                                     # noise that takes many rounds
+        order = torch.argsort(x[:, :], dim=1, descending=True, stable=True)
+        rank = torch.empty_like(order).scatter_(1, order, torch.arange(vocab, device=dev).expand(rows, -1).contiguous())
+        check(lib, dev, x, torch.exp(80 * (0.5 - (rank + 1) / vocab)).float(), T, k=g.integers(1, 3000, rows), p=g.uniform(0.2, 0.9, rows))
+
+
+def test_masked_logits_of_the_processing(lib, cuda_device):
+    """process_logits with a grammar's mask, then sampling: what is masked out is never drawn."""
+    dev, rows, vocab = cuda_device, 6, 20000
+    x, e = logits(15, rows, vocab, torch.float32, dev)
+    allowed = torch.zeros(rows, vocab, dtype=torch.bool)
+    for r, n in enumerate((1, 3, 40, 1000, 19999, 0)):
+        allowed[r, torch.randperm(vocab, generator=torch.Generator("cpu").manual_seed(r))[:n]] = True
+    words = np.packbits(allowed.numpy(), axis=1, bitorder="little").view(np.int32)
+    kept = torch.empty(rows, vocab, device=dev)
+    lib.process_logits(x, out=kept, allow_mask=torch.from_numpy(words.copy()).to(dev))
+    for lim in (dict(), dict(k=50), dict(p=0.9), dict(floor=0.01)):
+        got = check(lib, dev, kept, e, [0.9] * rows, **{n: [v] * rows for n, v in lim.items()})
+        assert got[5] == -1 and all(bool(allowed[r, got[r]]) for r in range(5))
