@@ -869,8 +869,9 @@ int pkv_sample_logits(const void* logits, int dtype, int rows, int vocab, long l
  *   block_tables  device int32, layer l at + l * bt_layer_stride, row s at
  *               + s * bt_row_stride, max_blocks entries used; the first
  *               ceil(seq_lens[s] / 16) of a row are its pages
- * Both calls are all or nothing.  At most 4096 rows and 2^30 entries
- * num_layers * max_blocks.
+ * Both calls are all or nothing.  Calls on one stack, or on the same rows, follow each
+ * other on one stream (or are ordered by events).  Outputs overlap no input but where
+ * it says so.  At most 4096 rows and 2^30 entries num_layers * max_blocks.
  * ---------------------------------------------------------------------- */
 
 /* pkv_grow_block_tables: row s, which holds seq_lens[s] tokens, is to hold

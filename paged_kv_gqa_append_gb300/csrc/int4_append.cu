@@ -9,7 +9,7 @@
 // of a page arranges them in shared memory and writes 512 bytes at once.
 //
 // Bound: memory, 2.6 KiB per token for K and V and 8 KiB for q: 14400 tokens of eight prompts, with q, and
-// the 906 pages read back, 38.7 us (29.1 us of bytes); a step of 32 tokens and the read 5.2 us, two launches
+// the 906 pages read back, 38.7 us (29.1 us of bytes); a step of 32 tokens and the read 4.5 us, two launches
 // of five dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) int4_append_kernel(const
 
 // out[i] = the page page_ids[i] as bf16: lo + code * scale, rounded once.  One CTA per
 // page, which it holds in shared memory; bound by memory (9 KiB read, 32 KiB written
-// per page).
-constexpr int kReadThreads = 256;
-
+// per page): 906 pages take 8.6 us with 256 threads and 9.9 us with 1024, 100 pages 2.8
+// and 2.2 us, so that a grid of one CTA per SM at most takes 1024.
+template <int kReadThreads>
 __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(const uint8_t* __restrict__ pool, int num_pages,
                                                                  const int32_t* __restrict__ page_ids,
                                                                  uint16_t* __restrict__ out, int* d_err) {
@@ -248,11 +248,12 @@ extern "C" int kv_read_int4(const void* kv_pool, int num_pages, const int32_t* p
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)count);
-  cfg.blockDim = dim3(kReadThreads);
+  const bool few = count <= sm_count(dev);
+  cfg.blockDim = dim3(few ? 1024 : 256);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, int4_read_kernel, static_cast<const uint8_t*>(kv_pool), num_pages, page_ids,
+  return cuda_status(cudaLaunchKernelEx(&cfg, few ? int4_read_kernel<1024> : int4_read_kernel<256>, static_cast<const uint8_t*>(kv_pool), num_pages, page_ids,
                                         static_cast<uint16_t*>(out), d_err),
                      "cudaLaunchKernelEx(read int4)");
 }
