@@ -834,10 +834,12 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
  * and the kept token with the largest w_i / noise[r][i] is drawn (the first one
  * of equals), which follows the kept tokens' distribution when the noise holds
  * independent exponential variates.  A noise value below 2^-126 or a NaN counts
- * as 2^-126, infinity as the largest number.  Tokens of logit -inf are never drawn; where the largest logit is
- * +inf, the tokens that have it count as w = 1, all others as 0.
+ * as 2^-126, infinity as the largest number.  Tokens of logit -inf are never
+ * drawn; where the largest logit is +inf, the tokens that have it count as w = 1,
+ * all others as 0.
  * T = 0 takes the first largest logit.  out_ids[r] = -1 if no logit is above
- * -inf, or if T is negative, infinite or NaN, or top_p or min_p NaN.
+ * -inf, or if T is negative, infinite or NaN, or top_p or min_p NaN, or if T > 0
+ * and noise is NULL.
  * log_probs[r] = (x - max x) / T - log Z of the token drawn, before the limits
  * (with T = 1 where T = 0); NaN for id -1.  (id -2 would say that the logits did
  * not reach shared memory within seconds: a fault of the device, not of the call.)
