@@ -27,6 +27,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "page_units.cuh"
 #include "pkv.h"
 #include "ptx.cuh"
 
@@ -297,14 +298,13 @@ __global__ void __launch_bounds__(kMostThreads) release_kernel(const StackParams
   int32_t* to = p.free_pages + (fits ? count : 0);  // of no meaning until the count says so
   if (p.fill) {
     // a warp for each row and layer: its pages lie side by side in the table and on the stack
-    const int units = fits ? p.rows * p.layers : 0, lane = threadIdx.x & 31;
-    for (int u = me / 32; u < units; u += threads / 32) {
-      const int row = u / p.layers, layer = u % p.layers;
-      const int need = sh.pages[row + 1] - sh.pages[row];
+    const int rows = fits ? p.rows : 0, lane = threadIdx.x & 31;
+    for (UnitWalk u(me / 32, threads / 32, p.layers); u.row < rows; u.next()) {
+      const int need = sh.pages[u.row + 1] - sh.pages[u.row];
       if (need == 0) continue;
       const int n = need / p.layers;
-      const int32_t* from = p.tables + layer * p.layer_stride + (long long)row * p.row_stride;
-      int32_t* here = to + sh.pages[row] + layer * n;
+      const int32_t* from = p.tables + u.layer * p.layer_stride + (long long)u.row * p.row_stride;
+      int32_t* here = to + sh.pages[u.row] + u.layer * n;
 #pragma unroll 4
       for (int i = lane; i < n; i += 32) here[i] = from[i];
     }
