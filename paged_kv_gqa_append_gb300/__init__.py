@@ -1477,9 +1477,12 @@ def grow_block_tables(seq_lens, new_tokens, block_tables, free_pages, free_count
     slot = _opt(slots, "slots", _I32, dev, layers * T)
     if cu_new is None:
         cu_new = _empty(S + 1, _I32, dev, stream)
+    cu = _vec(cu_new, "cu_new", _I32, dev, S + 1)
+    if T == 0:  # a tensor of no elements has no address; it is given all the same, and nothing is written there
+        pos, seq, slot = (None if t is None else cu for t in (positions, token_seq, slots))
     _call(dev, stream, "pkv_grow_block_tables", (lens, new, S, bt, layers, layer, row,
           width if max_blocks is None else max_blocks, stack, pages, count, lens_to, count_to,
-          _vec(cu_new, "cu_new", _I32, dev, S + 1), pos, seq, slot, T, _device_error(d_err, dev)))
+          cu, pos, seq, slot, T, _device_error(d_err, dev)))
     return cu_new
 
 

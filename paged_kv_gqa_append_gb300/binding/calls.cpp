@@ -466,9 +466,14 @@ long grow_tables(Args& a) {
   void* added = a.opt(NEW, ScalarType::Int, s.seqs);
   void* cu = a.vec(CU, ScalarType::Int, (int64_t)s.seqs + 1);
   const int64_t T = !a.none(POS) ? a.elements(POS) : !a.none(SEQ) ? a.elements(SEQ) : a.none(SLOTS) ? 0 : a.elements(SLOTS) / s.layers;
-  void* pos = a.opt(POS, ScalarType::Int, T);
-  void* seq = a.opt(SEQ, ScalarType::Int, T);
-  void* slots = a.opt(SLOTS, ScalarType::Int, T * s.layers);
+  // (a tensor of no elements has no address; it is given all the same, and nothing is written there)
+  const auto output = [&](int i, int64_t n) {
+    void* to = a.opt(i, ScalarType::Int, n);
+    return n == 0 && !a.none(i) ? cu : to;
+  };
+  void* pos = output(POS, T);
+  void* seq = output(SEQ, T);
+  void* slots = output(SLOTS, T * s.layers);
   void* err = a.error_word(ERR);
   const int mb = a.integer(MB, s.width), tokens = a.to_int(T);
   if (!a.ok) return kOther;
