@@ -21,11 +21,11 @@
 // core, which would round them towards zero: with codes that are never negative that
 // would add up.
 //
-// References: R is the next whole number over the largest score, set again only when probabilities
+// References: R is the next whole number over the largest score, set again only when four probabilities
 // relative to it pass 8.  The weights p vs and p vl are multiplied by a power of two, `lift`, that brings the
-// largest of p vs and p vl / 16 near 2^14, set again only when one passes 2^15: a head's sums are near that,
-// whatever V's size.  Both are seldom, so the usual step -- two pages -- has one vote, on sums that it needs
-// anyway, and no reduction.  What is merged are means and the logarithms of their weights, which neither
+// largest of p vs and p vl / 16 to 2^12 or more, below 2^13, set again only when four p vs pass 2^16 or four p vl
+// 2^60 (int4_lift.cuh, with what makes both seldom): a head's sums are near that, whatever V's size.  So the usual
+// step -- two pages -- has one vote, on sums that it needs anyway, and no reduction.  What is merged are means and the logarithms of their weights, which neither
 // overflow nor vanish for any V that bf16 holds.
 //
 // Work (three ways, chosen on the host by the caller's bound): a CTA for each sequence, a warp per KV head;
@@ -49,6 +49,7 @@
 #include <stdint.h>
 
 #include "int4.cuh"
+#include "int4_lift.cuh"
 #include "internal.h"
 #include "pkv.h"
 #include "ptx.cuh"
@@ -273,8 +274,7 @@ struct Group {
     };
     weigh();
     float psum = sum_of(p), zsum = sum_of(z);
-    // (the scales of V are not negative, so the sum is at least the largest; NaN comes here too)
-    if (__any_sync(0xffffffffu, !(psum <= 8.f) || !(fabsf(sum_of(y)) <= 0x1p15f) || !(fabsf(zsum) <= 0x1p60f))) {
+    if (__any_sync(0xffffffffu, i4_votes(psum, sum_of(y), zsum))) {
       float x[kSlots], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
@@ -284,7 +284,7 @@ struct Group {
       }
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float now = top > ref + 1.f ? ceilf(top) : ref;
+      const float now = i4_reference(ref, top);
       const float keep = exp2_approx(ref - now);  // (a head whose reference stays: 1)
       l *= keep;
       // the lifted sums stay as they are, unless that lifts them too far
@@ -300,9 +300,8 @@ struct Group {
       }
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-      if (most * lift > 0x1p14f) {  // (the same for all lanes of a head)
-        // 2^13 up to 2^14; the largest weight is above 2^-112
-        const float to = __uint_as_float((uint32_t)max(1, 127 + 13 + 127 - (int)(__float_as_uint(most) >> 23)) << 23);
+      const float to = i4_lift(lift, most);
+      if (to != lift) {  // (the same for all lanes of a head)
         lower(to / lift);
         lift = to;
       }
