@@ -148,7 +148,7 @@ __device__ __forceinline__ int pages_of(const Int4DecodeParams& p, int s, bool& 
 // has the scores of head t with slots g and g + 8, and dims 8 g .. 8 g + 7 of its output.
 struct Group {
   uint32_t q[8];       // B operands of the four k-steps
-  float fa, fb, fl;    // x = (S fa) (ks fb) + kl fl
+  float fa, fb, fl;    // x = (S fa ks) fb + kl fl
   bool apart;          // some head's fa is not 1
   float ref, lift;
   float l, low;        // this lane's sum of p, of p vl lift
@@ -207,9 +207,11 @@ struct Group {
     const float c = scale * 1.4426950408889634f;
     const float d0 = __uint_as_float((uint32_t)(127 - u0) << 23), d1 = __uint_as_float((uint32_t)(127 - u1) << 23);
     // from the head of the q that this lane has to that of its scores
-    // (d0 d1 c 2^24 alone, unless a float does not hold that)
+    // S is below 2, 2^-10 or more times the largest q of a code of 1: S ks overflows for no scale that bf16
+    // holds, and where it loses bits (scales below 2^-116) the score is nothing unless d0 d1 c 2^24 is beyond
+    // 2^90 -- then S is multiplied by a part of that first.
     const float both = d0 * 0x1p24f * (d1 * c);
-    const bool far = !(fabsf(both) < 0x1p120f);
+    const bool far = !(fabsf(both) < 0x1p90f);
     fa = __shfl_sync(0xffffffffu, far ? d0 * 0x1p24f : 1.f, 8 * t);
     fb = __shfl_sync(0xffffffffu, far ? d1 * c : both, 8 * t);
     apart = __any_sync(0xffffffffu, far);
@@ -231,7 +233,7 @@ struct Group {
   __device__ __forceinline__ void step(uint32_t blocks, int live) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t words = blocks - 16 * (lane - g) + kI4Scales;
-    float r[kSlots], t[kSlots], p[kSlots], vs[kSlots], vl[kSlots];
+    float r[kSlots], p[kSlots], vs[kSlots], vl[kSlots];
 #pragma unroll
     for (int u = 0; u < kPages; ++u) {
       const uint4 k = lds128(blocks + u * kI4BlockBytes);
@@ -248,10 +250,10 @@ struct Group {
         r[2 * u] *= fa;
         r[2 * u + 1] *= fa;
       }
-      t[2 * u] = bf16lo_to_f32(sc.x) * fb;
-      t[2 * u + 1] = bf16lo_to_f32(sc.y) * fb;
-      p[2 * u] = exp2_approx(fmaf(r[2 * u], t[2 * u], fmaf(bf16hi_to_f32(sc.x), fl, -ref)));
-      p[2 * u + 1] = exp2_approx(fmaf(r[2 * u + 1], t[2 * u + 1], fmaf(bf16hi_to_f32(sc.y), fl, -ref)));
+      r[2 * u] *= bf16lo_to_f32(sc.x);
+      r[2 * u + 1] *= bf16lo_to_f32(sc.y);
+      p[2 * u] = exp2_approx(fmaf(r[2 * u], fb, fmaf(bf16hi_to_f32(sc.x), fl, -ref)));
+      p[2 * u + 1] = exp2_approx(fmaf(r[2 * u + 1], fb, fmaf(bf16hi_to_f32(sc.y), fl, -ref)));
       vs[2 * u] = bf16lo_to_f32(sc.z);
       vl[2 * u] = bf16hi_to_f32(sc.z);
       vs[2 * u + 1] = bf16lo_to_f32(sc.w);
@@ -279,7 +281,7 @@ struct Group {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
         const uint32_t word = lds32(words + (i >> 1) * kI4BlockBytes + 4 * (i & 1));
-        x[i] = g + 8 * i < live ? fmaf(r[i], t[i], bf16hi_to_f32(word) * fl) : -INFINITY;
+        x[i] = g + 8 * i < live ? fmaf(r[i], fb, bf16hi_to_f32(word) * fl) : -INFINITY;
         top = fmaxf(top, x[i]);
       }
 #pragma unroll
