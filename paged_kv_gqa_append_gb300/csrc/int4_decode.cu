@@ -100,12 +100,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
-  return v;
-}
-
 __device__ __forceinline__ void mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm(
@@ -229,11 +223,12 @@ struct Group {
   static constexpr int kSlots = 2 * kPages;  // of a lane: g and g + 8 of either page
 
   // Two pages whose blocks are in shared memory, at this lane's first bytes; `live` of their 32 slots
-  // are the sequence's.
+  // are the sequence's.  A score is rounded before the reference is taken from it, so that equal ones
+  // have equal probabilities whatever their size and whatever references they meet.
   __device__ __forceinline__ void step(uint32_t blocks, int live) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const uint32_t words = blocks - 16 * (lane - g) + kI4Scales;
-    float r[kSlots], p[kSlots], vs[kSlots], vl[kSlots];
+    float x[kSlots], p[kSlots], vs[kSlots], vl[kSlots];
 #pragma unroll
     for (int u = 0; u < kPages; ++u) {
       const uint4 k = lds128(blocks + u * kI4BlockBytes);
@@ -244,16 +239,14 @@ struct Group {
       const uint32_t a = k.x >> 8, b = k.z >> 8, c = k.y >> 8, d = k.w >> 8;
       mma_add(s, a & kLow, b & kLow, a & kHigh, b & kHigh, q[2], q[3]);
       mma_add(s, c & kLow, d & kLow, c & kHigh, d & kHigh, q[6], q[7]);
-      r[2 * u] = s[0];
-      r[2 * u + 1] = s[2];
       if (apart) {
-        r[2 * u] *= fa;
-        r[2 * u + 1] *= fa;
+        s[0] *= fa;
+        s[2] *= fa;
       }
-      r[2 * u] *= bf16lo_to_f32(sc.x);
-      r[2 * u + 1] *= bf16lo_to_f32(sc.y);
-      p[2 * u] = exp2_approx(fmaf(r[2 * u], fb, fmaf(bf16hi_to_f32(sc.x), fl, -ref)));
-      p[2 * u + 1] = exp2_approx(fmaf(r[2 * u + 1], fb, fmaf(bf16hi_to_f32(sc.y), fl, -ref)));
+      x[2 * u] = fmaf(s[0] * bf16lo_to_f32(sc.x), fb, bf16hi_to_f32(sc.x) * fl);
+      x[2 * u + 1] = fmaf(s[2] * bf16lo_to_f32(sc.y), fb, bf16hi_to_f32(sc.y) * fl);
+      p[2 * u] = exp2_approx(x[2 * u] - ref);
+      p[2 * u + 1] = exp2_approx(x[2 * u + 1] - ref);
       vs[2 * u] = bf16lo_to_f32(sc.z);
       vl[2 * u] = bf16hi_to_f32(sc.z);
       vs[2 * u + 1] = bf16lo_to_f32(sc.w);
@@ -262,7 +255,10 @@ struct Group {
     if (live < kPages * PKV_PAGE_TOKENS) {  // what lies behind the sequence's end may be anything
 #pragma unroll
       for (int i = 0; i < kSlots; ++i)
-        if (g + 8 * i >= live) p[i] = vs[i] = vl[i] = 0.f;
+        if (g + 8 * i >= live) {
+          x[i] = -INFINITY;
+          p[i] = vs[i] = vl[i] = 0.f;
+        }
     }
     float y[kSlots], z[kSlots];
     const auto sum_of = [](const float (&v)[kSlots]) { return (v[0] + v[1]) + (v[2] + v[3]); };
@@ -277,13 +273,9 @@ struct Group {
     weigh();
     float psum = sum_of(p), zsum = sum_of(z);
     if (__any_sync(0xffffffffu, i4_votes(psum, sum_of(y), zsum))) {
-      float x[kSlots], top = -INFINITY;
+      float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        const uint32_t word = lds32(words + (i >> 1) * kI4BlockBytes + 4 * (i & 1));
-        x[i] = g + 8 * i < live ? fmaf(r[i], fb, bf16hi_to_f32(word) * fl) : -INFINITY;
-        top = fmaxf(top, x[i]);
-      }
+      for (int i = 0; i < kSlots; ++i) top = fmaxf(top, x[i]);
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float now = i4_reference(ref, top);

@@ -1,5 +1,5 @@
-"""paged_gqa_decode_int4 where K lies at the ends of its range, in each of the
-three ways that a call is split (a CTA for each sequence, clusters, shares)."""
+"""paged_gqa_decode_int4 where scores are large or K lies at the ends of its range, in
+each of the three ways that a call is split (a CTA for each sequence, clusters, shares)."""
 import numpy as np
 import pytest
 import torch
@@ -36,6 +36,34 @@ def times(pool, kv, by):
     for p in range(len(pool)):
         w = rows_of(pool, p, kv)
         set_rows(pool, p, kv, OB.from_f32_rne((OB.to_f64(w) * by).astype(np.float32)))
+
+
+def same_key(pool, seed):
+    """Every token's K row the same (one for each head)."""
+    first = random_pages(seed, 1)
+    for r in range(16):
+        pool[:, :, O4.CODE_AT[0][r]] = first[:, :, O4.CODE_AT[0][0]]
+        for i in range(4):
+            pool[:, :, O4.SCALE_AT[0][r] + i] = first[:, :, O4.SCALE_AT[0][0] + i]
+
+
+def equal_scores(lib, dev, way, size):
+    """Tokens of the same key have the same score and probability, however large the score
+    (here to 2^20 and beyond), so the output is the mean of the values: off by what the sums
+    and products of the bound of test_gpu_int4.py are off by, without a term for scores."""
+    lens, pages, bt, bound = case(way, 80)
+    pool = random_pages(81, pages)
+    same_key(pool, 82)
+    q = rows(83, len(lens), 32, 64, scale=size)
+    out, code = decode(lib, dev, q, pool, bt, lens, max_seq_len=bound)
+    assert code == 0
+    ref, span, reach, most = O4.attend(q, pool, bt, lens, 0.125)
+    close(out, ref, span, 0 * reach, most, lens, way)
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 10, 2.0 ** 17])
+def test_equal_scores_weigh_the_same(lib, cuda_device, size):
+    equal_scores(lib, cuda_device, "own", size)
 
 
 @pytest.mark.parametrize("sign", [1.0, -1.0])
