@@ -2,8 +2,10 @@
 // (bs8_decode.cu, int4_decode.cu) leave, and their merge.
 //
 // Every CTA of such a kernel takes an equal share of the list of all pages.  A share
-// that begins or ends inside a sequence leaves a part of it: o [64], not divided,
-// (m, l) for each of the 32 heads, o and l relative to 2^m.
+// that begins or ends inside a sequence leaves a part of it: o [64], not divided by
+// the sum l of its probabilities, (m, l) for each of the 32 heads, o and l relative to
+// 2^m (of int4_decode.cu l lies in [1, 2) and o is 2^10 times smaller; of a part with a
+// bad page l is kNothing).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -66,6 +66,12 @@ def test_equal_scores_weigh_the_same(lib, cuda_device, size):
     equal_scores(lib, cuda_device, "own", size)
 
 
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 10, 2.0 ** 17])
+@pytest.mark.parametrize("way", WAYS[1:])
+def test_equal_scores_weigh_the_same_in_parts(lib, cuda_device, way, size):
+    equal_scores(lib, cuda_device, way, size)
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("way", WAYS)
 def test_largest_keys(lib, cuda_device, way, sign):
