@@ -698,5 +698,5 @@ extern "C" int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const fl
   if (rc != PKV_OK) return rc;
   rc = cuda_status(cudaLaunchKernelEx(&cfg, decode, map, p), "cudaLaunchKernelEx(decode bs8)");
   if (rc != PKV_OK || ctas == 1 || whole) return rc;  // one CTA splits nothing
-  return launch_merge(cfg, p.parts, p.span, p.out, num_seqs, (int)ctas, p.by_cta, sms, kRaise, "cudaLaunchKernelEx(merge bs8)");
+  return launch_merge<false>(cfg, p.parts, p.span, p.out, num_seqs, (int)ctas, p.by_cta, sms, kRaise, "cudaLaunchKernelEx(merge bs8)");
 }

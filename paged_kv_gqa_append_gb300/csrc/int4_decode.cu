@@ -26,10 +26,8 @@
 // largest of p vs and p vl / 16 to 2^12 or more, below 2^13, set again only when four p vs pass 2^16 or four p vl
 // 2^60 (int4_lift.cuh, with what makes both seldom): a head's sums are near that, whatever V's size.  So the usual
 // step -- two pages -- has one vote, on sums that it needs anyway, and no reduction.
-// What is merged are the sums over V divided by a power of two near their weight, which neither overflow nor
-// vanish for any V that bf16 holds, and that weight as a factor of [1, 2) and an exponent that goes into R: a whole
-// number beside a whole number, so that a large score costs the weight nothing (below 2^24; a logarithm beside
-// a score of 2^20 kept three bits).
+// What is merged are means, which neither overflow nor vanish for any V that bf16 holds, and their weights as R
+// and a sum relative to 2^R: a sum of the two, or a logarithm, would lose the latter beside a large R.
 //
 // Work (three ways, chosen on the host by the caller's bound): a CTA for each sequence, a warp per KV head;
 // a cluster for each sequence and KV head, the warps taking pairs of pages in turn and putting together what
@@ -76,7 +74,7 @@ constexpr int kList = 1024;              // page ids of a share held at a time (
 constexpr int kMostCluster = 8;
 constexpr float kStart = -1.5e38f;       // R before the first score
 constexpr float kMostLift = 0x1p126f;
-// What is merged is up to twice a mean, and 2^10 times smaller than it is: up to 304 of them are added up.
+// Means are merged 2^10 times smaller than they are: sums of 32 bits on their way to the largest of bf16.
 constexpr float kMeanDown = 0x1p-10f, kMeanUp = 0x1p10f;
 
 struct Int4DecodeParams {
@@ -351,43 +349,21 @@ struct Group {
       for (int e = 0; e < 4; ++e) o[w][e] *= by;
   }
 
-  // Sums over all lanes: weight(), of the probabilities, relative to 2^R, then of dims 8 g .. 8 g + 7 of
-  // head t, times `by`.
-  __device__ __forceinline__ float weight() {
+  // The means of dims 8 g .. 8 g + 7 of head t, times `unit`, and their weight: (R, the sum of the
+  // probabilities relative to 2^R), (kStart, 0) and means of 0 where there were no pages.
+  __device__ __forceinline__ float2 finish(float (&x)[8], float unit) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       l += __shfl_xor_sync(0xffffffffu, l, d);
       low += __shfl_xor_sync(0xffffffffu, low, d);
     }
-    return l;
-  }
-  __device__ __forceinline__ void outputs(float (&x)[8], float by, float unit) const {
-    const float down = unit / lift;
+    const float inv = l == 0.f ? 0.f : 1.f / l, down = unit / lift;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      x[2 * w] = fmaf(o[w][0] + o[w][1], 0x1p24f, low) * by * down;
-      x[2 * w + 1] = fmaf(o[w][2] + o[w][3], 0x1p20f, low) * by * down;
+      x[2 * w] = fmaf(o[w][0] + o[w][1], 0x1p24f, low) * inv * down;
+      x[2 * w + 1] = fmaf(o[w][2] + o[w][3], 0x1p20f, low) * inv * down;
     }
-  }
-  // The means.
-  __device__ __forceinline__ void whole(float (&x)[8]) {
-    const float sum = weight();
-    outputs(x, sum == 0.f ? 0.f : 1.f / sum, 1.f);
-  }
-  // A part of what other warps have too: sums and their weight f of [1, 2), both relative to 2^m; returns
-  // (m, f), and (kStart, 0) with sums of 0 where there were no pages.
-  __device__ __forceinline__ float2 part(float (&x)[8]) {
-    const float sum = weight();
-    if (sum == 0.f) {
-#pragma unroll
-      for (int d = 0; d < 8; ++d) x[d] = 0.f;
-      return make_float2(kStart, 0.f);
-    }
-    // (sum is at least about a half; of a NaN the outputs are NaN)
-    const uint32_t bits = __float_as_uint(sum);
-    const int e = (int)(bits >> 23 & 0xFFu) - 127;
-    outputs(x, __uint_as_float((uint32_t)(127 - min(e, 126)) << 23), kMeanDown);
-    return make_float2(ref + (float)e, __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u));
+    return make_float2(ref, l);
   }
 };
 
@@ -440,7 +416,7 @@ struct Ring {
   }
 };
 
-struct alignas(16) Held {  // what a warp of the kernel for whole sequences has found: sums and their weight (Group::part)
+struct alignas(16) Held {  // what a warp of the kernel for whole sequences has found: means and their weight (Group::finish)
   float o[PKV_GROUP][PKV_HEAD_DIM];
   float2 weight[PKV_GROUP];
   int bad;
@@ -505,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_whole_kernel(const 
     issue(i + kRing - 1);
   }
   float x[8];
-  const float2 weight = st.part(x);
+  const float2 weight = st.finish(x, kMeanDown);
   // into the warp's own ring, which nothing is on its way to any more
   static_assert(sizeof(Held) <= kRing * kStageBytes && kI4BlockBytes % 16 == 0, "room for what a warp found");
   cp_async_wait<0>();
@@ -523,17 +499,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_whole_kernel(const 
   const int h = threadIdx.x / PKV_HEAD_DIM, d = threadIdx.x % PKV_HEAD_DIM;
   static_assert(kThreads == PKV_GROUP * PKV_HEAD_DIM, "a thread for each output");
   const auto of = [&](int w) { return reinterpret_cast<const Held*>(dyn + w * (kRing * kStageBytes)); };
-  float ref = kStart, o = 0.f, total = 0.f;
+  float ref = kStart, o = 0.f, total = 0.f, scaled[kWarps];
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, of(w)->weight[h].x);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float scaled = exp2_approx(of(w)->weight[h].x - ref);
-    o = fmaf(scaled, of(w)->o[h][d], o);
-    total = fmaf(scaled, of(w)->weight[h].y, total);
-  }
+  for (int w = 0; w < kWarps; ++w) total += scaled[w] = exp2_approx(of(w)->weight[h].x - ref) * of(w)->weight[h].y;
+  const float inv = total == 0.f ? 0.f : 1.f / total;  // (a CTA that no pages are left for: 0)
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) o = fmaf(scaled[w] * inv, of(w)->o[h][d], o);
   if (ctas == 1) {
-    const float y = bad ? 0.f : o * (1.f / total) * kMeanUp, z = __shfl_down_sync(0xffffffffu, y, 1);
+    const float y = bad ? 0.f : o * kMeanUp, z = __shfl_down_sync(0xffffffffu, y, 1);
     if (d % 2 == 0) *reinterpret_cast<uint32_t*>(out + threadIdx.x) = pack_bf16x2(y, z);
     return;
   }
@@ -548,25 +523,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_whole_kernel(const 
     ref = kStart;
     total = 0.f;
     bad = false;
-    float2 weights[kMostCluster], sums[kMostCluster], y = make_float2(0.f, 0.f);
+    float2 weights[kMostCluster], means[kMostCluster], y = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < kMostCluster; ++c) {
       const Held* other = cluster.map_shared_rank(&sum, c < ctas ? c : 0);
       weights[c] = c < ctas ? other->weight[hh] : make_float2(kStart, 0.f);
-      sums[c] = c < ctas ? *reinterpret_cast<const float2*>(other->o[hh] + dd) : make_float2(0.f, 0.f);
+      means[c] = c < ctas ? *reinterpret_cast<const float2*>(other->o[hh] + dd) : make_float2(0.f, 0.f);
       if (c < ctas) bad |= other->bad != 0;
     }
 #pragma unroll
     for (int c = 0; c < kMostCluster; ++c) ref = fmaxf(ref, weights[c].x);
 #pragma unroll
     for (int c = 0; c < kMostCluster; ++c) {
-      const float scaled = c < ctas ? exp2_approx(weights[c].x - ref) : 0.f;
-      y.x = fmaf(scaled, sums[c].x, y.x);
-      y.y = fmaf(scaled, sums[c].y, y.y);
-      total = fmaf(scaled, weights[c].y, total);
+      weights[c].x = exp2_approx(weights[c].x - ref) * weights[c].y;
+      total += weights[c].x;
     }
-    const float inv = kMeanUp * (1.f / total);
-    *reinterpret_cast<uint32_t*>(out + at) = bad ? 0u : pack_bf16x2(y.x * inv, y.y * inv);
+    const float inv = 1.f / total;
+#pragma unroll
+    for (int c = 0; c < kMostCluster; ++c) {
+      const float scaled = weights[c].x * inv;
+      y.x = fmaf(scaled, means[c].x, y.x);
+      y.y = fmaf(scaled, means[c].y, y.y);
+    }
+    *reinterpret_cast<uint32_t*>(out + at) = bad ? 0u : pack_bf16x2(y.x * kMeanUp, y.y * kMeanUp);
   }
   cluster.sync();  // nobody's shared memory goes while it is read
 }
@@ -751,11 +730,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) int4_share_kernel(const 
       // the end of the sequence, or of the share inside it
       float x[8];
       const bool all = from == 0 && page == pages;
+      const float2 weight = st.finish(x, all ? 1.f : kMeanDown);
       if (all) {
-        st.whole(x);
         write_row(p.out, seq, head, x, bad);
       } else {
-        const float2 weight = st.part(x);
         const int g = lane >> 2, t = lane & 3, hq = head * PKV_GROUP + t;
         float* part = p.parts + ((size_t)blockIdx.x * 2 + (from > 0 ? 0 : 1)) * kPartFloats;
         float4* to = reinterpret_cast<float4*>(part + hq * PKV_HEAD_DIM + 8 * g);
@@ -884,5 +862,5 @@ extern "C" int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num
   cfg.numAttrs = 1;
   rc = cuda_status(cudaLaunchKernelEx(&cfg, kernel, p), "cudaLaunchKernelEx(decode int4)");
   if (rc != PKV_OK || shares == 1 || p.own) return rc;  // nothing is split
-  return launch_merge(cfg, p.parts, p.span, p.out, num_seqs, (int)shares, p.by_cta, sms, kMeanUp, "cudaLaunchKernelEx(merge int4)");
+  return launch_merge<true>(cfg, p.parts, p.span, p.out, num_seqs, (int)shares, p.by_cta, sms, kMeanUp, "cudaLaunchKernelEx(merge int4)");
 }

@@ -2,10 +2,10 @@
 // (bs8_decode.cu, int4_decode.cu) leave, and their merge.
 //
 // Every CTA of such a kernel takes an equal share of the list of all pages.  A share
-// that begins or ends inside a sequence leaves a part of it: o [64], not divided by
-// the sum l of its probabilities, (m, l) for each of the 32 heads, o and l relative to
-// 2^m (of int4_decode.cu l lies in [1, 2) and o is 2^10 times smaller; of a part with a
-// bad page l is kNothing).
+// that begins or ends inside a sequence leaves a part of it: o [64] and (m, l) for each
+// of the 32 heads, l the sum of its probabilities relative to 2^m (kNothing: it has a bad
+// page).  o is the sum over V, not divided, relative to 2^m (8 bits), or that divided by l
+// (4 bits: sums that neither overflow nor vanish whatever V's size).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,7 +48,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // (32 / heads)-th part of a head, weighted by 2^(m - M) / L, with everything a
 // thread needs loaded at once: this kernel is latency (the end of the decode
 // kernel seen, the record, the parts), about 3 us behind it.  The order is
-// fixed, so the result does not depend on timing.  Many sequences have few parts
+// fixed, so the result does not depend on timing.  kMeans: the parts' o are divided by
+// their l, which then belongs to their weight.  Many sequences have few parts
 // each: 8 or 16 heads per CTA, and the 16 lanes find M and L themselves from all
 // parts' (m, l), so that nothing is exchanged before the sums.  Few sequences
 // have up to two parts per SM: one head per CTA, whose threads fetch one (m, l)
@@ -60,7 +61,7 @@ constexpr int kKept = 4;        // of all parts' (m, l): those that a lane has i
 
 // kPerSm: 1 has the registers for everything in flight (90), where one wave is
 // enough; else two at a time matter more.
-template <bool kOneHead, int kPerSm>
+template <bool kOneHead, int kPerSm, bool kMeans>
 __global__ void __launch_bounds__(kMergeThreads, kPerSm) split_merge_kernel(const float* parts, const int2* span,
                                                                    uint16_t* out, int heads, int by_cta, float raise) {
   extern __shared__ float weights[];  // one head: of all parts
@@ -114,8 +115,9 @@ __global__ void __launch_bounds__(kMergeThreads, kPerSm) split_merge_kernel(cons
     for (int w = 0; w < kMergeThreads / 32; ++w) m = fmaxf(m, tops[w]);
     for (int i = all0; i < n; i += step) {
       const float2 e = i == all0 ? all[0] : ml_of(i);
-      weights[i] = exp2_approx(e.x - m);
-      sum = fmaf(e.y, weights[i], sum);
+      const float w = exp2_approx(e.x - m);
+      weights[i] = kMeans ? w * e.y : w;
+      sum = fmaf(e.y, w, sum);
       bad |= e.y == kNothing;
     }
 #pragma unroll
@@ -147,12 +149,15 @@ __global__ void __launch_bounds__(kMergeThreads, kPerSm) split_merge_kernel(cons
     bad = (__ballot_sync(0xffffffffu, bad) >> (lane & 16) & 0xFFFFu) != 0;
   }
 
+  const float inv = 1.f / sum;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = group;; i0 += kMergeBatch * groups) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      if (i0 + u * groups >= n) continue;
-      const float w = kOneHead ? weights[i0 + u * groups] : exp2_approx(mine[u] - m);
+      const int i = i0 + u * groups;
+      if (i >= n) continue;
+      float w = kOneHead ? weights[i] : exp2_approx(mine[u] - m);
+      if (kMeans) w *= kOneHead ? inv : ml_of(i).y * inv;  // (l is in the L1 since (m, l) was fetched)
       acc.x = fmaf(w, v[u].x, acc.x);
       acc.y = fmaf(w, v[u].y, acc.y);
       acc.z = fmaf(w, v[u].z, acc.z);
@@ -186,10 +191,10 @@ __global__ void __launch_bounds__(kMergeThreads, kPerSm) split_merge_kernel(cons
     acc.z += e.z;
     acc.w += e.w;
   }
-  const float inv = raise * (1.f / sum);
+  const float by = kMeans ? raise : raise * inv;
   *reinterpret_cast<uint2*>(out + (size_t)seq * PKV_NUM_Q_HEADS * PKV_HEAD_DIM + dims) =
       bad ? make_uint2(0, 0)
-          : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          : make_uint2(pack_bf16x2(acc.x * by, acc.y * by), pack_bf16x2(acc.z * by, acc.w * by));
 }
 
 // The merge behind a decode of `ctas` CTAs, with the attributes and the stream of `cfg`; `raise`
@@ -200,15 +205,16 @@ __global__ void __launch_bounds__(kMergeThreads, kPerSm) split_merge_kernel(cons
 // 8192 55.5, 50.3, 50.2; 39 of 2048 29.7, 24.3, 22.5; 256 of 2048 144, 105, 97.  Two CTAs per
 // SM from more CTAs than SMs on: 76 of 2048 (152 CTAs) 33.9, two per SM 35.5; 77 35.6 and
 // 35.9; 128 53.2 and 52.8; 256 of 1024 56.6 and 56.2.
-inline int launch_merge(cudaLaunchConfig_t cfg, const float* parts, const int2* span, uint16_t* out, int num_seqs,
-                        int ctas, int by_cta, int sms, float raise, const char* what) {
+template <bool kMeans>
+int launch_merge(cudaLaunchConfig_t cfg, const float* parts, const int2* span, uint16_t* out, int num_seqs,
+                 int ctas, int by_cta, int sms, float raise, const char* what) {
   const int heads = num_seqs <= 8 ? 1 : num_seqs * 4 <= sms ? 8 : 16;
   const long long items = by_cta ? ctas - 1 : num_seqs;  // nothing goes on behind the last CTA
   cfg.gridDim = dim3((unsigned)(items * (PKV_NUM_Q_HEADS / heads)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = heads == 1 ? (size_t)ctas * sizeof(float) : 0;
-  auto* merge = heads == 1 ? split_merge_kernel<true, 2>
-                : (int)cfg.gridDim.x > sms ? split_merge_kernel<false, 2> : split_merge_kernel<false, 1>;
+  auto* merge = heads == 1 ? split_merge_kernel<true, 2, kMeans>
+                : (int)cfg.gridDim.x > sms ? split_merge_kernel<false, 2, kMeans> : split_merge_kernel<false, 1, kMeans>;
   return cuda_status(cudaLaunchKernelEx(&cfg, merge, parts, span, out, heads, by_cta, raise), what);
 }
 

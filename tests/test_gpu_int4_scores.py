@@ -127,3 +127,20 @@ def test_zero_queries_under_the_largest_keys(lib, cuda_device, way):
     assert code == 0
     ref, span, reach, most = O4.attend(q * 0, pool, bt, lens, 0.125)
     close(out[:, ::2], ref[:, ::2], span[:, ::2], 0 * reach[:, ::2], most[:, ::2], lens)
+
+
+@pytest.mark.parametrize("score", [-9e37, 1.6e38])
+@pytest.mark.parametrize("way", WAYS)
+def test_equal_scores_at_the_ends_of_fp32(lib, cuda_device, way, score):
+    """Keys of one value each, under which every token's score is this: the mean of the values."""
+    lens, pages, bt, bound = case(way, 93)
+    pool = random_pages(94, pages)
+    for p in range(pages):
+        w = rows_of(pool, p, 0)
+        w[..., 0], w[..., 1] = 0, OB.from_f32_rne(np.float32(abs(score) / 64))
+        set_rows(pool, p, 0, w)
+    q = OB.from_f32_rne(np.full((len(lens), 32, 64), np.sign(score), np.float32))
+    out, code = decode(lib, cuda_device, q, pool, bt, lens, scale=1.0, max_seq_len=bound)
+    assert code == 0
+    ref, span, reach, most = O4.attend(q * 0, pool, bt, lens, 1.0)
+    close(out, ref, span, 0 * reach, most, lens)
