@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
@@ -72,7 +73,7 @@ constexpr int kMaxSeqsInt4 = 4096;
 constexpr int kMinPages = 4;             // least share of a CTA
 constexpr int kList = 1024;              // page ids of a share held at a time (even)
 constexpr int kMostCluster = 8;
-constexpr float kStart = -1.5e38f;       // R before the first score
+constexpr float kStart = -FLT_MAX;       // R before the first score
 constexpr float kMostLift = 0x1p126f;
 // Means are merged 2^10 times smaller than they are: sums of 32 bits on their way to the largest of bf16.
 constexpr float kMeanDown = 0x1p-10f, kMeanUp = 0x1p10f;

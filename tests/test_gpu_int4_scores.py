@@ -129,7 +129,7 @@ def test_zero_queries_under_the_largest_keys(lib, cuda_device, way):
     close(out[:, ::2], ref[:, ::2], span[:, ::2], 0 * reach[:, ::2], most[:, ::2], lens)
 
 
-@pytest.mark.parametrize("score", [-9e37, 1.6e38])
+@pytest.mark.parametrize("score", [-1.6e38, -1.2e38, -9e37, 1.6e38])
 @pytest.mark.parametrize("way", WAYS)
 def test_equal_scores_at_the_ends_of_fp32(lib, cuda_device, way, score):
     """Keys of one value each, under which every token's score is this: the mean of the values."""
