@@ -679,7 +679,8 @@ int paged_gqa_decode_bs8(const void* q, const void* kv_pool, const float* kv_sca
 /* kv_append_rope_int4: the newest tokens of every sequence written into their
  * pages; arguments, ragged rows, rotation and errors as kv_append_rope_bs8
  * (without its limit on two sequences of a call that write one page: rows are
- * independent of each other; a slot written twice by one call holds either). */
+ * independent of each other; a slot that one call writes twice, with different
+ * rows, holds codes, scale and minimum of either: some of one, some of the other). */
 int kv_append_rope_int4(const void* k, long long k_stride, const void* v, long long v_stride,
                         const int32_t* cu_new, const int32_t* seq_lens, int T,
                         const int32_t* block_tables, int num_seqs, int bt_row_stride,
@@ -690,8 +691,9 @@ int kv_append_rope_int4(const void* k, long long k_stride, const void* v, long l
 /* kv_read_int4: pages as bf16 pages, out[i] = bf16(lo + code * scale) of page
  * page_ids[i], device bf16 [count][2][8][16][64]: a bf16 pool of `count` pages,
  * e.g. for paged_gqa_prefill over a cached prefix.  Slots that hold no token
- * read as whatever their bytes stand for.  A page id outside [0, num_pages)
- * gives a zero page and sets *d_err. */
+ * read as whatever their bytes stand for; a row that reaches bf16's largest
+ * number within 2^-8 of it may read as infinity, as its scale is rounded.  A page
+ * id outside [0, num_pages) gives a zero page and sets *d_err. */
 int kv_read_int4(const void* kv_pool, int num_pages, const int32_t* page_ids, int count, void* out,
                  int* d_err, void* stream);
 
@@ -700,11 +702,18 @@ int kv_read_int4(const void* kv_pool, int num_pages, const int32_t* page_ids, in
  * lengths and bad page ids as paged_gqa_decode.
  * Codes enter fp16 tensor-core MMAs exactly.  Each q head is scaled by the
  * power of two that brings its largest |value| into [2^14, 2^15) and is exact in
- * fp16 but for values below 2^-27 of that one, which are off by at most 2^-36 of
+ * fp16 but for values below 2^-27 of that one, which are off by at most 2^-35 of
  * it.  A weight (a probability times its V row's scale) enters the product as two
- * fp16 values, off by 2^-22 of it and by no less than 2^-37 of the largest one.
+ * fp16 values, off by at most 2^-22 of it, or by 2^-37 of the largest that a
+ * probability times its row's scale or times a sixteenth of its |minimum| has been,
+ * or by 2^-151, whichever is most.
+ * A score is rounded to fp32 before the largest is subtracted; scores (with `scale`)
+ * and their two parts, of the codes and of the minima, are to stay below 2^127.
  *   max_seq_len  host upper bound of seq_lens (chooses how the work is split; a
- *                larger actual length is still handled; 0: 16 max_blocks)
+ *                larger actual length is still handled; 0: 16 max_blocks).  A bound
+ *                far above the lengths, as a captured loop has to give, costs what
+ *                another split takes: 32 sequences of 2048 tokens 12.5 us with their
+ *                length, 17.6 us with 8192 or 131072
  *   workspace    at least paged_gqa_decode_int4_workspace_bytes(num_seqs)
  *                bytes, 16-byte aligned, of any content: every call writes
  *                what it reads.  Calls that may run at the same time, two
@@ -826,7 +835,8 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
  * Row r with temperature T > 0, w_i = exp((x_i - max x) / T) over the tokens whose
  * logit is not NaN, Z = sum w; tokens are ranked by logit, ties by id.  Token i
  * is kept if all three hold (the limits look at the same distribution, so that
- * their order does not matter):
+ * their order does not matter; a top-p of what top-k left keeps fewer tokens, and
+ * is not to be had by these numbers):
  *   top_k   its rank is below top_k[r]             (top_k <= 0: no limit)
  *   top_p   the w of the tokens ranked before it sum to less than top_p[r] Z
  *           (the first one is always kept; top_p >= 1: no limit)
@@ -852,8 +862,12 @@ int pkv_process_logits(const void* logits, int dtype, int rows, int vocab, long 
  *   top_p, min_p device float [rows] or NULL
  *   out_ids      device int32 [rows]
  *   log_probs    device float [rows] or NULL
+ * Sums and the race are in fp32: a token within 2e-5 of a limit may fall on either
+ * side of it, and of two within 2e-5 of each other either may win.
  * One cluster of up to 8 CTAs per row; sums in a fixed order, so a call gives the
- * same result every time.  Host-side checks only (no device error).
+ * same result every time.  That order depends on the number of rows: at such an edge
+ * a row may get another token in a larger batch.  Host-side checks only (no device
+ * error).
  * ---------------------------------------------------------------------- */
 int pkv_sample_logits(const void* logits, int dtype, int rows, int vocab, long long row_stride,
                       const float* noise, long long noise_stride, const float* temperature,

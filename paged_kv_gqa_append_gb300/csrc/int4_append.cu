@@ -9,8 +9,8 @@
 // of a page arranges them in shared memory and writes 512 bytes at once.
 //
 // Bound: memory, 2.6 KiB per token for K and V and 8 KiB for q: 14400 tokens of eight prompts, with q, and
-// the 906 pages read back, 38.7 us (29.1 us of bytes); a step of 32 tokens and the read 4.5 us, two launches
-// of five dependent loads.
+// the 906 pages read back, 39.0 us (29.1 us of bytes); a step of 32 tokens and the read 4.5 us (5.2 on another
+// machine), two launches of five dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -126,9 +126,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) int4_append_kernel(const
 }
 
 // out[i] = the page page_ids[i] as bf16: lo + code * scale, rounded once.  One CTA per
-// page, which it holds in shared memory; bound by memory (9 KiB read, 32 KiB written
-// per page): 906 pages take 8.6 us with 256 threads and 9.9 us with 1024, 100 pages 2.8
-// and 2.2 us, so that a grid of one CTA per SM at most takes 1024.
+// page, which it holds in shared memory; bound by the instructions of the conversion
+// (half of the issue slots) and the wait for the page, with nothing of the next one
+// under way: 906 pages, 5.5 us of bytes (9 KiB read, 32 KiB written a page), take 8.6 us
+// with 256 threads and 9.9 us with 1024, 100 pages 2.8 and 2.2 us, so that a grid of one
+// CTA per SM at most takes 1024.
 template <int kReadThreads>
 __global__ void __launch_bounds__(kReadThreads) int4_read_kernel(const uint8_t* __restrict__ pool, int num_pages,
                                                                  const int32_t* __restrict__ page_ids,

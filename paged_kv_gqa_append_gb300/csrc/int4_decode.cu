@@ -38,9 +38,10 @@
 // which it issues no FP32 operation either), some 80 FP32 and 120 integer operations (2 cycles), 80 of these
 // for the unpacking: with 16 warps an SM takes 100 cycles for it (pages in the L2), as long as its share of
 // the measured copy rate takes for the 2304 bytes; more warps do not help (24: the same).  300 sequences of
-// 2048 tokens run at 79 % of the copy rate (66 us); 32 of 2048 tokens take 12.9 us (5.6 us of bytes), 97 ragged
-// ones to 8191 55 us (33.5), one of 131071 24.3 us (11.1), one of 37 2.9 us.  In shares 3.5 us go by before the
-// first copy and 4 to 6 us in the merge.
+// 2048 tokens run at 78 % of the copy rate (67 us); 32 of 2048 tokens take 12.5 us (5.6 us of bytes), 97 ragged
+// ones to 8191 54 us (33.5), one of 131071 24.4 us (11.1), one of 37 3.0 us; with near-equal scores and rows of one
+// size the same to 0.4 us.  In shares 3.5 us go by before the first copy and 4 to 6 us in the merge; of 32
+// sequences' 256 CTAs 104 SMs have two and 48 one.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -820,12 +821,13 @@ extern "C" int paged_gqa_decode_int4(const void* q, const void* kv_pool, int num
   const long long most_pages = (longest + PKV_PAGE_TOKENS - 1) / PKV_PAGE_TOKENS;
   // How the work is split, by the caller's bound (us: a CTA per sequence / clusters / shares):
   //  - a CTA for each of many sequences, if they are short, or if such CTAs keep the SMs about as busy as
-  //    shares would: 80 of 8 pages 7.3 / 9.6 / 11.5, 256 of 16 14.0 / 28.1 / 22.5, 2000 ragged to 4 39 / - /
-  //    48, 300 of 128 66 / - / 79; 100 of 64 24.1 / 22.8 / 24.1, 64 of 32 14.6 / 11.7 / 15.3;
+  //    shares would: 80 of 8 pages 7.0 / 9.6 / 11.3, 256 of 16 13.4 / 28.8 / 21.9, 2000 ragged to 4 38 /
+  //    - / 48, 300 of 128 66 / - / 79; 100 of 64 23.6 / 22.2 / 23.1, 64 of 32 14.1 / 11.6 / 15.0;
   //  - else a cluster for each sequence and KV head, as many CTAs as two for each SM allow, as long as
-  //    these take few pages each: 1 of 128 pages - / 4.8 / 7.5, 1 of 1024 - / 11.5 / 11.0, 4 of 128 - / 5.5
-  //    / 8.7, 32 of 128 - / 12.9 / 18.1, 64 of 128 - / 23.2 / 25.6, 32 of 512 - / 42.4 / 41.6;
-  //  - else shares: 1 of 8192 pages - / 40.5 / 24.4, 97 ragged to 512 - / 60 / 55.
+  //    these take few pages each: 1 of 128 pages - / 4.5 / 7.7, 4 of 128 - / 5.5 / 8.2, 32 of 128 - / 12.3 /
+  //    17.6, 64 of 128 - / 22.4 / 24.7;
+  //  - else shares: 1 of 8192 pages - / 39.9 / 24.0, 97 ragged to 512 - / 58 / 54.  (Between the two clusters are
+  //    ahead by now, 1 of 1024 - / 9.6 / 10.9, 32 of 512 - / 33.3 / 37.7; the limits are where both were even.)
   const int slots = kCtasPerSm * sms, waves = (num_seqs + slots - 1) / slots;
   const double busy = num_seqs <= sms ? 0.86 * num_seqs / sms : (double)num_seqs / (waves * slots);
   p.own = 2 * num_seqs > sms && (most_pages <= 24 || (most_pages <= 128 && busy >= 0.6));

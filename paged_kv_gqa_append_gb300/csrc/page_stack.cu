@@ -20,8 +20,8 @@
 // second kernel's sums are done while the first one runs.
 //
 // Bound: latency, of five dependent loads and barriers behind a launch: a step of 32 rows and 16 layers
-// takes 4.5 us, 61000 tokens of 64 prompts with their slots in 16 layers 9.3 us (0.8 us of bytes), 131000
-// pages of 128 finished rows 11.3 us (0.2 us of bytes).
+// takes 4.6 us, 61000 tokens of 64 prompts with their slots in 16 layers 9.3 us (0.8 us of bytes), 131000
+// pages of 128 finished rows 11.4 us (0.2 us of bytes).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -360,9 +360,11 @@ int launch(void (*kernel)(StackParams), StackParams p, int fill, int commit, int
 }
 
 // Up to kAlone items of a grow (rows over all layers, and slots) and kAloneRows rows over all layers of a
-// release one CTA does a call (a step of 32 rows and 16 layers 4.5 us); with more, as many CTAs as have
+// release one CTA does a call (a step of 32 rows and 16 layers 4.6 us); with more, as many CTAs as have
 // kShare items each, or a warp for each row and layer (release of 64 rows of 16 layers and up to 125
-// pages: 6.8 us, by one CTA 28.8 us; of 8 such rows 5.9 and 8.4 us; of 4 6.0 us by either).
+// pages: 6.8 us, by one CTA 28.8 us; of 8 such rows 5.9 and 8.4 us; of 4 6.0 us by either).  How many pages a
+// grow takes the host does not know: 64 prompts to 1920 tokens in 16 layers, without lists, are taken for a step
+// and cost one CTA 40 us; with their lists, in place, they are many CTAs' and take 9.5 us.
 constexpr long long kAlone = 1024;
 constexpr int kAloneRows = 64;
 constexpr int kShare = 2048, kFillThreads = 512;

@@ -29,9 +29,9 @@
 // Bound: the steps of a row, one after another -- its parts' copies, the first sums, the bound, the lists,
 // the first CTA's rounds, with two cluster barriers -- in as many rows at once as shared memory holds (57 of
 // 128256 fp32 logits).  One such row with top-k and top-p takes 10.4 us, 32 bf16 rows with top-p and min-p
-// 18 us, 256 fp32 rows with all limits 61.5 us (the logits alone are 19.3 us of bytes at the measured copy
-// rate, with the noise 38.7 us); 256 rows without limits 89 us, with a top-p that most of a flat row is in
-// 146 us.
+// 18 us, 256 fp32 rows with all limits 61.5 us (the logits, nearly all that such rows read, are 19.3 us of bytes
+// at the measured copy rate); 256 rows without limits 88 us (logits and noise: 38.7 us), with a top-p that most
+// of a flat row is in 146 to 175 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -447,9 +447,10 @@ __device__ __forceinline__ void resolve(R& row, const float (&noise)[kList / 32]
 }
 
 // kCtaThreads: with 512 a row is done sooner; with 256 a CTA spends less on its reductions, and three of
-// them share an SM, so that many rows with limits are done sooner (256 fp32 rows of 128256 63 us, with 512
-// threads, two CTAs per SM 85 us, three, which spill, 73 us; without limits 99 us, with 512 threads 89 us; 32
-// bf16 rows 23.7 and 18.1 us).
+// them share an SM, so that many rows with limits are done sooner (256 fp32 rows of 128256 61.5 us, with 512
+// threads, two CTAs per SM 85 us, three, which spill, 73 us; without limits 98 us, with 512 threads 88 us; 32
+// bf16 rows 23.7 and 18.0 us).  The host sees which limits are given, not their values: many rows whose limits are
+// all off cost the 98 us.
 template <class T, bool kHeld, int kCtaThreads, int kPerSm>
 __global__ void __launch_bounds__(kCtaThreads, kPerSm) sample_kernel(const SampleParams p) {
   extern __shared__ uint4 held[];
