@@ -76,7 +76,7 @@ constexpr int kList = 1024;              // page ids of a share held at a time (
 constexpr int kMostCluster = 8;
 constexpr float kStart = -FLT_MAX;       // R before the first score
 constexpr float kMostLift = 0x1p126f;
-// Means are merged 2^10 times smaller than they are: sums of 32 bits on their way to the largest of bf16.
+// Means are merged 2^10 times smaller than they are, so that roundings beside bf16's largest do not overflow.
 constexpr float kMeanDown = 0x1p-10f, kMeanUp = 0x1p10f;
 
 struct Int4DecodeParams {
